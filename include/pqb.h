@@ -98,7 +98,8 @@ typedef enum pqb_status {
   PQB_ERR_ALIGN = -5,     /* a pointer breaks the alignment rules */
   PQB_ERR_WORKSPACE = -6, /* workspace smaller than pqb_query_sizes asks */
   PQB_ERR_HIP = -7,       /* the HIP runtime refused a launch */
-  PQB_ERR_SCRATCH = -8    /* pqb_quantize_noalloc: needs more than its fixed scratch */
+  PQB_ERR_SCRATCH = -8,   /* pqb_quantize_noalloc: needs more than its fixed scratch */
+  PQB_ERR_VALUE = -9      /* a scalar argument outside its range */
 } pqb_status;
 
 typedef enum pqb_dtype { PQB_F32 = 0, PQB_BF16 = 1 } pqb_dtype;
@@ -308,6 +309,125 @@ pqb_status pqb_kv_read_kivi(const uint8_t* k_codes, const uint8_t* v_codes,
                             const float* v_mins, int64_t layers, int64_t tokens, int64_t heads,
                             int64_t head_dim, int bits, pqb_dtype out_dtype, void* k_out,
                             void* v_out, void* stream);
+
+/* Paged 8-bit KV cache: one layer's keys and values in pages of page_size
+ * tokens, E4M3 codes with one power-of-two scale per page and KV head (page
+ * "量化部署实战", KV Cache 量化: K and V quantized separately on every write;
+ * page "14. 量化：让每一步搬更少的字节", 路线三: a cache in 8 bits is half the
+ * bytes that every decoded token reads).
+ *   k_codes u8 [pages, heads, page_size, head_dim]
+ *   v_codes u8 [pages, heads, head_dim, page_size]   (transposed in its page)
+ *   k_scales, v_scales u8 [pages, heads]             E8M0: byte X + 127, value
+ *                                                    dec(code) * 2^X
+ * A request's tokens lie in the pages that its block table row names, in order;
+ * a slot is page * page_size + offset.  page_size is 16, 32, 64, 128 or 256;
+ * head_dim 64, 128, 192 or 256; 1 <= heads <= 4096; 0 <= pages and
+ * pages * page_size < 2^31.  Codes are 16-byte aligned.  Nothing has to be
+ * initialised: what lies behind a request's last token is never used. */
+typedef struct pqb_kv_pages {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t pages, heads, head_dim;
+  int32_t page_size;
+  int32_t reserved; /* must be 0 (else PQB_ERR_ENUM) */
+} pqb_kv_pages;
+
+/* Plans one step: request b (of `batch`) holds cached_lens[b] tokens and gets
+ * new_lens[b] more (both i32 in device memory).  Pages it lacks,
+ * ceil((cached + new) / page_size) - ceil(cached / page_size), are taken in
+ * request order from free_pages[*free_used ...] and written into its row of
+ * block_table (i32 [batch, table_width], in place; other entries stay).
+ * Written:
+ *   slots i32 [max_new]      the slot of each new token, requests in order; -1
+ *                            behind the last (a page id that is negative or
+ *                            whose slot passes 2^31 - 1 also gives -1)
+ *   q_starts i32 [batch + 1] the first new token of each request, and their sum
+ *   kv_lens i32 [batch]      cached + new
+ *   free_used_out i32 [1]    *free_used + pages taken
+ *   status i32 [4]           flags below (0: done), pages needed, new tokens, 0
+ * All or nothing: if a flag is set, block_table stays, slots are all -1,
+ * q_starts all 0, kv_lens = cached_lens and *free_used_out = *free_used.
+ * kv_lens may be cached_lens and free_used_out may be free_used (a step in
+ * place); no other arrays may overlap.  The lengths stay on the GPU, so a
+ * captured step can be replayed.  Workspace: pqb_kv_plan_workspace_bytes(), 4-
+ * byte aligned (0 bytes for up to 2048 requests and 4096 slots).
+ * Shape rules: batch, table_width, free_total and max_new in [0, 2^31), and
+ * table_width * page_size < 2^31 - 256.  All arrays 4-byte aligned.  Errors,
+ * before any launch: PQB_ERR_SHAPE, PQB_ERR_NULL, PQB_ERR_ALIGN,
+ * PQB_ERR_WORKSPACE. */
+enum {
+  PQB_PLAN_PAGES = 1,    /* the free list is too short */
+  PQB_PLAN_TABLE = 2,    /* a request outgrows its block table row */
+  PQB_PLAN_SLOTS = 4,    /* more than max_new new tokens */
+  PQB_PLAN_NEGATIVE = 8  /* a negative length, or *free_used outside the list */
+};
+size_t pqb_kv_plan_workspace_bytes(int64_t batch, int64_t max_new);
+pqb_status pqb_kv_plan_paged(const int32_t* cached_lens, const int32_t* new_lens, int64_t batch,
+                             int32_t* block_table, int64_t table_width, const int32_t* free_pages,
+                             int64_t free_total, const int32_t* free_used, int page_size,
+                             int64_t max_new, int32_t* slots, int32_t* q_starts, int32_t* kv_lens,
+                             int32_t* free_used_out, int32_t* status, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Quantizes `tokens` new tokens into their slots.  k and v: `dtype` [tokens,
+ * heads, head_dim], a token's heads and channels contiguous, tokens k_stride and
+ * v_stride elements apart (e.g. parts of one fused projection).  slots i32
+ * [tokens]; a slot outside [0, pages * page_size) skips its token (padding),
+ * whose k and v are not read.
+ * A run is a maximal sequence of tokens with consecutive slots in one page.  Per
+ * run, head and tensor, X_run is the smallest integer with
+ *   max(amax over the run, 1e-12) <= 448 * 2^X_run;
+ * the page's exponent becomes X_run if the run starts at offset 0, else
+ * X = max(X_held, X_run), and if that is larger than X_held, the codes of the
+ * offsets before the run become E4M3(dec(c) * 2^(X_held - X)).  The new codes are
+ * E4M3(x * 2^-X), both round-to-nearest-even.  Offsets behind the run stay.
+ * Inputs must be finite.  One call writes a page in one run only: if two runs
+ * of a call lie in one page, that page's codes and scales are unspecified (no
+ * other page is affected).
+ * Alignment: k and v 16 bytes, and strides a multiple of 16 bytes.  tokens <
+ * 2^27, strides in [heads * head_dim, 2^40).  Errors, before any launch:
+ * PQB_ERR_ENUM, PQB_ERR_SHAPE, PQB_ERR_NULL, PQB_ERR_ALIGN. */
+pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, int64_t tokens,
+                               int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                               const pqb_kv_pages* cache, void* stream);
+
+/* Attention of new tokens over their requests' pages:
+ *   out[t, g] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (q[t, g] . k_j) - max).
+ * q: `dtype` [q_rows, q_heads, head_dim], a token's heads and channels contiguous,
+ * tokens q_stride elements apart; out: the same type, contiguous.  Request b owns
+ * rows q_starts[b] .. q_starts[b + 1] - 1 (i32 [batch + 1], rising) and kv_lens[b]
+ * tokens (i32), its pages in block_table[b] (i32 [batch, table_width]); query
+ * head g reads KV head g / (q_heads / heads).  With causal != 0, query i of n sees
+ * the tokens j <= kv_lens[b] - n + i (its own among them, once appended), else all
+ * kv_lens[b], whatever n is (an encoder's states).  A row that sees no token is
+ * 0; rows outside every request are left as they were.  Lengths are read on the
+ * GPU and may differ from call to call of a captured graph; kv_lens beyond the
+ * table's width are cut there, and the tokens of a page id outside [0, pages) are
+ * not seen.
+ * max_q_len: a hint, the most query tokens of one request (0: unknown).  It
+ * decides workspace and launch shapes; results hold whatever it is.
+ * Numbers: float32 sums, maxima and outputs before one rounding to `dtype`;
+ * q . k exact products (float32 q in three bf16 parts); p rounded to 11 bits
+ * relative to its value down to 2^-29 of the largest (22 bits for float32 q).
+ * Shape rules: q_heads a multiple of heads; q_rows * q_heads and
+ * table_width * page_size < 2^31 - 256; batch < 2^23; q_stride in [q_heads * head_dim,
+ * 2^40).  scale: finite and >= 0 (else PQB_ERR_VALUE).  Workspace:
+ * pqb_kv_attend_workspace_bytes(), its contents on entry do not matter; calls
+ * that overlap in time need one each.  Alignment: q, out and workspace 16 bytes,
+ * q_stride a multiple of 16 bytes, the int arrays 4.  Errors, before any launch:
+ * PQB_ERR_ENUM, PQB_ERR_SHAPE, PQB_ERR_VALUE, PQB_ERR_NULL, PQB_ERR_ALIGN,
+ * PQB_ERR_WORKSPACE. */
+size_t pqb_kv_attend_workspace_bytes(int64_t q_rows, int64_t q_heads, int64_t heads,
+                                     int64_t head_dim, int64_t batch, int64_t table_width,
+                                     int page_size, int64_t max_q_len);
+pqb_status pqb_kv_attend_paged(const void* q, pqb_dtype dtype, int64_t q_rows, int64_t q_heads,
+                               int64_t q_stride, const pqb_kv_pages* cache,
+                               const int32_t* block_table, int64_t table_width,
+                               const int32_t* q_starts, const int32_t* kv_lens, int64_t batch,
+                               int causal, float scale, int64_t max_q_len, void* out,
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* Block-scaled FP8 GEMM, the consumer of the codes above (page "量化部署实战",
  * exercise section on FP8 blockwise scaling: within each 128-deep block of K

@@ -198,6 +198,7 @@ const char* pqb_status_string(pqb_status s) {
     case PQB_ERR_WORKSPACE: return "workspace too small";
     case PQB_ERR_HIP: return "HIP launch failed";
     case PQB_ERR_SCRATCH: return "needs more scratch than the fixed buffer of pqb_quantize_noalloc";
+    case PQB_ERR_VALUE: return "a scalar argument outside its range";
   }
   return "unknown status";
 }
@@ -655,6 +656,162 @@ pqb_status pqb_kv_read_kivi(const uint8_t* k_codes, const uint8_t* v_codes,
   if (v_codes)
     return hip_status(launch_kivi_v_dequant(v_codes, v_scales, v_mins, n, bits, bf16, v_out, st));
   return PQB_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Paged 8-bit KV cache
+// ---------------------------------------------------------------------------
+
+// log2 of a page size, or -1.
+static int page_shift(int64_t page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == (int64_t)1 << s) return s;
+  return -1;
+}
+
+static bool head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 192 || d == 256; }
+
+// Lengths and tables are 32-bit on the GPU; the margin keeps a length rounded up
+// to whole units of tokens inside them.
+constexpr int64_t kPagedMaxTokens = ((int64_t)1 << 31) - 256;
+constexpr int64_t kPagedMaxStride = (int64_t)1 << 40;
+
+static pqb_status check_pages(const pqb_kv_pages* c, int* shift) {
+  if (!c) return PQB_ERR_NULL;
+  if (c->reserved) return PQB_ERR_ENUM;
+  *shift = page_shift(c->page_size);
+  if (*shift < 0 || !head_dim_ok(c->head_dim) || c->heads < 1 || c->heads > 4096 || c->pages < 0 ||
+      c->pages >= (int64_t)1 << (31 - *shift))
+    return PQB_ERR_SHAPE;
+  if (c->pages > 0 && (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)) return PQB_ERR_NULL;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16)) return PQB_ERR_ALIGN;
+  return PQB_OK;
+}
+
+size_t pqb_kv_plan_workspace_bytes(int64_t batch, int64_t max_new) {
+  return batch < 0 || max_new < 0 ? 0 : plan_workspace_bytes(batch, max_new);
+}
+
+pqb_status pqb_kv_plan_paged(const int32_t* cached_lens, const int32_t* new_lens, int64_t batch,
+                             int32_t* block_table, int64_t table_width, const int32_t* free_pages,
+                             int64_t free_total, const int32_t* free_used, int page_size,
+                             int64_t max_new, int32_t* slots, int32_t* q_starts, int32_t* kv_lens,
+                             int32_t* free_used_out, int32_t* status, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  const int shift = page_shift(page_size);
+  if (shift < 0 || batch < 0 || batch > INT32_MAX || table_width < 0 ||
+      table_width >= kPagedMaxTokens >> shift || free_total < 0 || free_total > INT32_MAX ||
+      max_new < 0 || max_new > INT32_MAX)
+    return PQB_ERR_SHAPE;
+  if (!q_starts || !free_used || !free_used_out || !status) return PQB_ERR_NULL;
+  if (batch > 0 && (!cached_lens || !new_lens || !kv_lens || (table_width > 0 && !block_table)))
+    return PQB_ERR_NULL;
+  if ((free_total > 0 && !free_pages) || (max_new > 0 && !slots)) return PQB_ERR_NULL;
+  for (const void* p : {(const void*)cached_lens, (const void*)new_lens, (const void*)block_table,
+                        (const void*)free_pages, (const void*)free_used, (const void*)slots,
+                        (const void*)q_starts, (const void*)kv_lens, (const void*)free_used_out,
+                        (const void*)status, (const void*)workspace})
+    if (!aligned(p, 4)) return PQB_ERR_ALIGN;
+  const size_t need = plan_workspace_bytes(batch, max_new);
+  if (workspace_bytes < need) return PQB_ERR_WORKSPACE;
+  if (need && !workspace) return PQB_ERR_NULL;
+  return hip_status(launch_plan(
+      PlanArgs{cached_lens, new_lens, batch, block_table, table_width, free_pages, free_total, free_used,
+               shift, max_new, slots, q_starts, kv_lens, free_used_out, status, (int32_t*)workspace},
+      (hipStream_t)stream));
+}
+
+pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, int64_t tokens,
+                               int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                               const pqb_kv_pages* cache, void* stream) {
+  if (!valid_dtype(dtype)) return PQB_ERR_ENUM;
+  int shift;
+  const pqb_status e = check_pages(cache, &shift);
+  if (e != PQB_OK) return e;
+  const int64_t row = cache->heads * cache->head_dim, es = dtype == PQB_BF16 ? 2 : 4;
+  if (tokens < 0 || tokens >= 1 << 27) return PQB_ERR_SHAPE;  // the grid's thread limit
+  if (k_stride < row || v_stride < row || k_stride >= kPagedMaxStride || v_stride >= kPagedMaxStride)
+    return PQB_ERR_SHAPE;
+  if (tokens == 0 || cache->pages == 0) return PQB_OK;
+  if (!k || !v || !slots) return PQB_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || k_stride * es % 16 || v_stride * es % 16)
+    return PQB_ERR_ALIGN;
+  return hip_status(launch_append(
+      AppendArgs{k, v, tokens, cache->heads, k_stride, v_stride, slots, cache->pages, shift,
+                 cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales, 1},
+      dtype == PQB_BF16, (int)cache->head_dim, (hipStream_t)stream));
+}
+
+// Rows of one request that a call plans for: the hint, or what q holds.
+static int64_t attend_max_rows(int64_t q_rows, int64_t group, int64_t max_q_len) {
+  return (max_q_len > 0 && max_q_len < q_rows ? max_q_len : q_rows) * group;
+}
+
+static bool attend_dims_ok(int64_t q_rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t batch,
+                           int64_t table_width, int shift) {
+  return shift >= 0 && head_dim_ok(head_dim) && heads >= 1 && heads <= 4096 && q_heads >= 1 &&
+         q_heads % heads == 0 && q_heads < kPagedMaxTokens && q_rows >= 0 &&
+         q_rows < kPagedMaxTokens / q_heads && batch >= 0 && batch < 1 << 23 && table_width >= 0 &&
+         table_width < kPagedMaxTokens >> shift;
+}
+
+size_t pqb_kv_attend_workspace_bytes(int64_t q_rows, int64_t q_heads, int64_t heads, int64_t head_dim,
+                                     int64_t batch, int64_t table_width, int page_size,
+                                     int64_t max_q_len) {
+  const int shift = page_shift(page_size);
+  if (!attend_dims_ok(q_rows, q_heads, heads, head_dim, batch, table_width, shift)) return 0;
+  return attend_workspace_bytes(batch, heads, attend_max_rows(q_rows, q_heads / heads, max_q_len), table_width,
+                                shift, (int)head_dim);
+}
+
+pqb_status pqb_kv_attend_paged(const void* q, pqb_dtype dtype, int64_t q_rows, int64_t q_heads,
+                               int64_t q_stride, const pqb_kv_pages* cache,
+                               const int32_t* block_table, int64_t table_width,
+                               const int32_t* q_starts, const int32_t* kv_lens, int64_t batch,
+                               int causal, float scale, int64_t max_q_len, void* out,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(dtype)) return PQB_ERR_ENUM;
+  int shift;
+  const pqb_status e = check_pages(cache, &shift);
+  if (e != PQB_OK) return e;
+  if (!attend_dims_ok(q_rows, q_heads, cache->heads, cache->head_dim, batch, table_width, shift))
+    return PQB_ERR_SHAPE;
+  if (q_stride < q_heads * cache->head_dim || q_stride >= kPagedMaxStride) return PQB_ERR_SHAPE;
+  if (!(scale >= 0.0f) || scale > 3.0e38f) return PQB_ERR_VALUE;
+  if (q_rows == 0 || batch == 0) return PQB_OK;
+  if (!q || !out || !q_starts || !kv_lens || (table_width > 0 && !block_table)) return PQB_ERR_NULL;
+  const int64_t es = dtype == PQB_BF16 ? 2 : 4;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_stride * es % 16 || !aligned(workspace, 16) ||
+      !aligned(block_table, 4) || !aligned(q_starts, 4) || !aligned(kv_lens, 4))
+    return PQB_ERR_ALIGN;
+  const int64_t group = q_heads / cache->heads, max_rows = attend_max_rows(q_rows, group, max_q_len);
+  // with no page at all every table entry is out of range: nothing is seen
+  const int64_t width = cache->pages ? table_width : 0;
+  const size_t need = attend_workspace_bytes(batch, cache->heads, max_rows, width, shift, (int)cache->head_dim);
+  if (workspace_bytes < need) return PQB_ERR_WORKSPACE;
+  if (need && !workspace) return PQB_ERR_NULL;
+  AttendArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.q_rows = q_rows;
+  a.k_codes = cache->k_codes;
+  a.v_codes = cache->v_codes;
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
+  a.table = block_table;
+  a.width = width;
+  a.batch = batch;
+  a.starts = q_starts;
+  a.kv_lens = kv_lens;
+  a.heads = (int32_t)cache->heads;
+  a.group = (int32_t)group;
+  a.pages = cache->pages;
+  a.shift = shift;
+  a.causal = causal != 0;
+  a.c = scale * 1.44269504088896341f;
+  a.out = out;
+  return hip_status(launch_attend(a, dtype == PQB_BF16, (int)cache->head_dim, max_rows, workspace,
+                                  (hipStream_t)stream));
 }
 
 // Shape, code-pointer and output rules shared by the GEMM entry points (each

@@ -180,6 +180,61 @@ hipError_t launch_w4a16(const W4Job* jobs, int njobs, int M, bool out_bf16, hipS
 hipError_t launch_w4a16_mfma(const W4Job* jobs, int njobs, int64_t M, bool out_bf16,
                              hipStream_t st);
 
+// ---- paged 8-bit KV cache (layouts in paged.h) -------------------------------
+struct PlanArgs {
+  const int32_t *cached, *added;  // [batch]
+  int64_t batch;
+  int32_t* table;                 // [batch, width]
+  int64_t width;
+  const int32_t* free_pages;      // [free_total]
+  int64_t free_total;
+  const int32_t* free_used;
+  int shift;                      // page size 2^shift
+  int64_t max_new;
+  int32_t* slots;                 // [max_new]
+  int32_t* starts;                // [batch + 1]
+  int32_t* kv_lens;               // [batch]
+  int32_t* free_used_out;
+  int32_t* status;                // [4]
+  int32_t* base;                  // workspace [batch] (see plan_workspace_bytes)
+};
+size_t plan_workspace_bytes(int64_t batch, int64_t max_new);
+hipError_t launch_plan(const PlanArgs& a, hipStream_t st);
+
+struct AppendArgs {
+  const void *k, *v;
+  int64_t tokens, heads, k_stride, v_stride;  // strides in elements
+  const int32_t* slots;
+  int64_t pages;
+  int shift;
+  uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+  int window;                                 // set by the launcher
+};
+hipError_t launch_append(AppendArgs a, bool bf16, int head_dim, hipStream_t st);
+
+struct AttendArgs {
+  const void* q;
+  int64_t q_stride;                           // elements between tokens
+  int64_t q_rows;                             // rows of q and out
+  const uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+  const int32_t* table;
+  int64_t width, batch;
+  const int32_t *starts, *kv_lens;
+  int32_t heads, group;                       // KV heads; query heads per KV head
+  int64_t pages;
+  int shift;
+  int causal;
+  float c;                                    // softmax scale times log2(e)
+  void* out;                                  // [q_rows, heads * group, D]
+  float *part_o, *part_ml;                    // workspace of split rows
+  int32_t part_rows;                          // set by the launcher, as the two above
+};
+// The workspace for at most max_rows = max_q_len * group rows per request.
+size_t attend_workspace_bytes(int64_t batch, int64_t heads, int64_t max_rows, int64_t width,
+                              int shift, int head_dim);
+hipError_t launch_attend(AttendArgs a, bool bf16, int head_dim, int64_t max_rows, void* workspace,
+                         hipStream_t st);
+
 // ---- division checks (k_check.hip) -----------------------------------------
 hipError_t launch_check_recip(uint32_t first, int64_t n, float* out, hipStream_t st);
 hipError_t launch_check_div(const float* s, int64_t ns, uint32_t x_first, int64_t nx, float* out,

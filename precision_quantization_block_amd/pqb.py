@@ -58,6 +58,13 @@ class _W4Job(ctypes.Structure):
                 ("k", ctypes.c_int64)]
 
 
+class _KvPages(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class _Sizes(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_size_t), ("scales", ctypes.c_size_t),
                 ("aux", ctypes.c_size_t), ("workspace", ctypes.c_size_t)]
@@ -90,6 +97,14 @@ def lib():
         L.pqb_kv_write_fp8_ex.argtypes = [P, P, I, I64, I64, I64, I64, I, I, P, P, P, P, P, SZ, P]
         L.pqb_kv_write_kivi.argtypes = [P, P, I, I64, I64, I64, I64, I, P, P, P, P, P, P, P]
         L.pqb_kv_read_kivi.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I, I, P, P, P]
+        KV, F = ctypes.POINTER(_KvPages), ctypes.c_float
+        L.pqb_kv_plan_workspace_bytes.argtypes, L.pqb_kv_plan_workspace_bytes.restype = [I64, I64], SZ
+        L.pqb_kv_plan_paged.argtypes = [P, P, I64, P, I64, P, I64, P, I, I64, P, P, P, P, P, P, SZ, P]
+        L.pqb_kv_append_paged.argtypes = [P, P, I, I64, I64, I64, P, KV, P]
+        L.pqb_kv_attend_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64, I, I64]
+        L.pqb_kv_attend_workspace_bytes.restype = SZ
+        L.pqb_kv_attend_paged.argtypes = [P, I, I64, I64, I64, KV, P, I64, P, P, I64, I, F, I64, P,
+                                          P, SZ, P]
         L.pqb_gemm_fp8_blockscaled.argtypes = [P, P, P, P, I64, I64, I64, I, P, P]
         L.pqb_gemm_fp8_blockscaled_quant.argtypes = [P, P, P, P, I64, I64, I64, P, P, P]
         L.pqb_gemv_w4a16.argtypes = [P, I64, P, P, P, I64, I64, I, P, P]
@@ -107,7 +122,8 @@ def lib():
         for f in ("pqb_query_sizes", "pqb_quantize", "pqb_quantize_noalloc", "pqb_quantize_batch",
                   "pqb_dequantize", "pqb_dequantize_batch",
                   "pqb_kv_write_fp8", "pqb_kv_write_fp8_ex", "pqb_kv_write_kivi",
-                  "pqb_kv_read_kivi", "pqb_gemm_fp8_blockscaled",
+                  "pqb_kv_read_kivi", "pqb_kv_plan_paged", "pqb_kv_append_paged",
+                  "pqb_kv_attend_paged", "pqb_gemm_fp8_blockscaled",
                   "pqb_gemm_fp8_blockscaled_quant", "pqb_gemv_w4a16",
                   "pqb_gemv_w4a16_batch", "pqb_gemm_mxfp4", "pqb_gemm_nvfp4", "pqb_stream_reference", "pqb_gemm_w4a16",
                   "pqb_gemm_w4a16_batch",
@@ -423,6 +439,220 @@ def kv_read_kivi(k_parts, v_parts, shape, bits: int = 2, out_dtype=torch.bfloat1
         BF16 if out_dtype == torch.bfloat16 else F32, _ptr(outs[0]), _ptr(outs[1]), _stream(dev)),
         "kv_read_kivi")
     return outs[0], outs[1]
+
+
+# --------------------------------------------------------------------------
+# paged 8-bit KV cache
+# --------------------------------------------------------------------------
+
+@dataclass
+class PagedKV:
+    """One layer's paged 8-bit KV cache: E4M3 codes with a power-of-two scale
+    (E8M0 byte X + 127) per page and head; V is transposed inside its page."""
+    k_codes: torch.Tensor    # u8 [pages, heads, page_size, head_dim]
+    v_codes: torch.Tensor    # u8 [pages, heads, head_dim, page_size]
+    k_scales: torch.Tensor   # u8 [pages, heads]
+    v_scales: torch.Tensor   # u8 [pages, heads]
+
+
+def kv_paged_cache(pages: int, heads: int, page_size: int, head_dim: int, device="cuda") -> PagedKV:
+    """An empty PagedKV (uninitialised: nothing behind a request's last token is
+    ever used)."""
+    dev = torch.device(device)
+    return PagedKV(torch.empty((pages, heads, page_size, head_dim), dtype=torch.uint8, device=dev),
+                   torch.empty((pages, heads, head_dim, page_size), dtype=torch.uint8, device=dev),
+                   torch.empty((pages, heads), dtype=torch.uint8, device=dev),
+                   torch.empty((pages, heads), dtype=torch.uint8, device=dev))
+
+
+@dataclass
+class PagedPlan:
+    """What kv_plan_paged wrote (all int32 on the GPU)."""
+    slots: torch.Tensor      # [max_new] slot of each new token, -1 behind the last
+    q_starts: torch.Tensor   # [batch + 1] first new token of each request, and their sum
+    kv_lens: torch.Tensor    # [batch] tokens of each request with the new ones
+    free_used: torch.Tensor  # [1] entries of the free list handed out so far
+    status: torch.Tensor     # [4] flags (0: done), pages needed, new tokens, 0
+
+
+PLAN_FLAGS = {"pages": 1, "table": 2, "slots": 4, "negative": 8}
+
+
+def _on(dev, t, name, dtypes, contiguous=True):
+    """t, checked to be a contiguous tensor of `dev` (in-place arguments are never copied)."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _gpu_of(t, name):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def _call_on(dev, fn, *args):
+    """fn(*args, the device's current stream), with `dev` the current device."""
+    if dev.index == torch.cuda.current_device():
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+_I32, _U8 = (torch.int32,), (torch.uint8,)
+
+
+def _pages_struct(cache: PagedKV, dev) -> _KvPages:
+    kc = _on(dev, cache.k_codes, "k_codes", _U8)
+    vc = _on(dev, cache.v_codes, "v_codes", _U8)
+    ks = _on(dev, cache.k_scales, "k_scales", _U8)
+    vs = _on(dev, cache.v_scales, "v_scales", _U8)
+    if kc.dim() != 4:
+        raise ValueError("k_codes must be [pages, heads, page_size, head_dim]")
+    N, H, S, D = kc.shape
+    if vc.shape != (N, H, D, S) or ks.shape != (N, H) or vs.shape != (N, H):
+        raise ValueError("v_codes must be [pages, heads, head_dim, page_size], scales [pages, heads]")
+    return _KvPages(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), N, H, D, S, 0)
+
+
+def _token_rows(x: torch.Tensor):
+    """x [tokens, heads, head_dim] with a token's values contiguous and tokens a
+    16-byte multiple apart (copied if they are not), and the tokens' stride."""
+    T, H, D = x.shape
+    es = x.element_size()
+    if T > 1 and x.numel():
+        ld = x.stride(0)
+        if x.stride(2) != 1 or x.stride(1) != D and H > 1 or ld < H * D or ld * es % 16 or x.data_ptr() % 16:
+            x, ld = x.clone(memory_format=torch.contiguous_format), H * D
+    else:
+        ld = H * D
+        if not x.is_contiguous() or x.data_ptr() % 16:
+            x = x.clone(memory_format=torch.contiguous_format)
+    return x, ld
+
+
+def kv_plan_paged(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                  free_pages: torch.Tensor, free_used: torch.Tensor, page_size: int, max_new: int,
+                  out: PagedPlan | None = None) -> PagedPlan:
+    """Plan one step of a paged cache on the GPU: pages for new_lens [batch] more
+    tokens on top of cached_lens [batch], taken from free_pages[free_used ...]
+    into block_table [batch, width] (in place), and a slot per new token.  All
+    int32.  `max_new` is the capacity of the slots.  All or nothing: if
+    status[0] is not 0 (PLAN_FLAGS), nothing was handed out, the slots are -1 and
+    there are no query rows.  `out`: a plan of the same sizes to write into; its
+    kv_lens may be cached_lens and its free_used may be free_used."""
+    dev = _gpu_of(cached_lens, "cached_lens")
+    B = cached_lens.numel()
+    _on(dev, cached_lens, "cached_lens", _I32)
+    _on(dev, new_lens, "new_lens", _I32)
+    _on(dev, block_table, "block_table", _I32)
+    _on(dev, free_pages, "free_pages", _I32)
+    _on(dev, free_used, "free_used", _I32)
+    if new_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("new_lens must be [batch] and block_table [batch, width]")
+    if free_used.numel() != 1:
+        raise ValueError("free_used must hold one value")
+    if max_new < 0:
+        raise ValueError("max_new must not be negative")
+    L = lib()
+    need = L.pqb_kv_plan_workspace_bytes(B, max_new)
+    ws = torch.empty((need // 4,), dtype=torch.int32, device=dev) if need else None
+    if out is None:
+        # one allocation, cut into the plan's parts
+        buf = torch.empty((max_new + 2 * B + 6,), dtype=torch.int32, device=dev)
+        slots, starts, lens, used, status = buf.split([max_new, B + 1, B, 1, 4])
+        out = PagedPlan(slots, starts, lens, used, status)
+    else:
+        sizes = (max_new, B + 1, B, 1, 4)
+        parts = (out.slots, out.q_starts, out.kv_lens, out.free_used, out.status)
+        for t, n, name in zip(parts, sizes, ("slots", "q_starts", "kv_lens", "free_used", "status")):
+            if _on(dev, t, "out." + name, _I32).numel() != n:
+                raise ValueError(f"out.{name} must hold {n} values")
+    _check(_call_on(dev, L.pqb_kv_plan_paged, cached_lens.data_ptr(), new_lens.data_ptr(), B,
+                    block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(),
+                    free_pages.numel(), free_used.data_ptr(), page_size, max_new,
+                    out.slots.data_ptr(), out.q_starts.data_ptr(), out.kv_lens.data_ptr(),
+                    out.free_used.data_ptr(), out.status.data_ptr(), _ptr(ws), need),
+           "kv_plan_paged")
+    return out
+
+
+def kv_append_paged(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: PagedKV) -> None:
+    """Quantize new tokens' k and v [tokens, heads, head_dim] (float32 or bf16,
+    tokens at any stride) into their slots of the cache; tokens of a slot
+    outside the cache (-1) are skipped.  `slots` may hold more entries than
+    there are tokens (a plan's slots are max_new long)."""
+    dev = _gpu_of(k, "k")
+    for t, name in ((k, "k"), (v, "v")):
+        _on(dev, t, name, (torch.float32, torch.bfloat16), contiguous=False)
+    _on(dev, slots, "slots", _I32)
+    c = _pages_struct(cache, dev)
+    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must be [tokens, heads, head_dim] of one shape and dtype")
+    if k.shape[1] != c.heads or k.shape[2] != c.head_dim:
+        raise ValueError("k and v must have the cache's heads and head_dim")
+    if slots.numel() < k.shape[0]:
+        raise ValueError("slots must hold an entry per token")
+    k, k_ld = _token_rows(k)
+    v, v_ld = _token_rows(v)
+    _check(_call_on(dev, lib().pqb_kv_append_paged, k.data_ptr(), v.data_ptr(),
+                    BF16 if k.dtype == torch.bfloat16 else F32, k.shape[0], k_ld, v_ld,
+                    slots.data_ptr(), ctypes.byref(c)), "kv_append_paged")
+
+
+def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
+                    q_starts: torch.Tensor, kv_lens: torch.Tensor, causal: bool = True,
+                    scale: float | None = None, max_q_len: int | None = None,
+                    out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """softmax(scale q k^T) v of new tokens q [tokens, q_heads, head_dim] (float32 or
+    bf16, tokens at any stride) over their requests' pages.  Request b owns rows
+    q_starts[b] .. q_starts[b + 1] - 1 and kv_lens[b] cached tokens (int32).
+    causal: query i of n sees the tokens up to kv_lens[b] - n + i; otherwise all
+    of them (cross attention over an encoder's states, of any other length).
+    scale: 1 / sqrt(head_dim) unless given.  max_q_len: the most query tokens
+    of one request where the caller knows it (a hint for speed and workspace).
+    Rows outside every request are left as they were in `out`."""
+    dev = _gpu_of(q, "q")
+    _on(dev, q, "q", (torch.float32, torch.bfloat16), contiguous=False)
+    c = _pages_struct(cache, dev)
+    _on(dev, block_table, "block_table", _I32)
+    _on(dev, q_starts, "q_starts", _I32)
+    _on(dev, kv_lens, "kv_lens", _I32)
+    if q.dim() != 3 or q.shape[2] != c.head_dim or q.shape[1] % max(c.heads, 1):
+        raise ValueError("q must be [tokens, q_heads, head_dim] with q_heads a multiple of the cache's heads")
+    B = kv_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or q_starts.numel() != B + 1:
+        raise ValueError("block_table must be [batch, width] and q_starts [batch + 1]")
+    if max_q_len is not None and max_q_len < 1:
+        raise ValueError("max_q_len must be positive")
+    T, Hq, D = q.shape
+    q, ld = _token_rows(q)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    elif _on(dev, out, "out", (q.dtype,)).shape != (T, Hq, D):
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    if T == 0 or B == 0:
+        return out
+    L = lib()
+    hint = max_q_len or 0
+    need = L.pqb_kv_attend_workspace_bytes(T, Hq, c.heads, D, B, block_table.shape[1], c.page_size, hint)
+    if workspace is None:
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    else:
+        _on(dev, workspace, "workspace", (workspace.dtype,))
+    have = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(_call_on(dev, L.pqb_kv_attend_paged, q.data_ptr(), BF16 if q.dtype == torch.bfloat16 else F32,
+                    T, Hq, ld, ctypes.byref(c), block_table.data_ptr(), block_table.shape[1],
+                    q_starts.data_ptr(), kv_lens.data_ptr(), B, int(causal),
+                    1.0 / math.sqrt(D) if scale is None else scale, hint, out.data_ptr(),
+                    _ptr(workspace), have), "kv_attend_paged")
+    return out
 
 
 def gemm_fp8_blockscaled(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor,

@@ -33,6 +33,7 @@ constexpr int kWaves = 4, kThreads = kWaves * kWave;
 constexpr int kMinUnits = kWaves;                 // fewest units of a split
 constexpr int kMaxPartRows = 64;                  // rows of a request that may be split
 constexpr int64_t kGroupsWanted = 1024;           // workgroups a split aims at
+constexpr int64_t kMaxGridYZ = 65535;
 
 // ---------------------------------------------------------------------------
 // Work items.  Request b has u_b = ceil(kv_len / 64) units and is cut into
@@ -61,7 +62,7 @@ __device__ __forceinline__ int units_of(int32_t kv) { return (int)(((int64_t)kv 
 __device__ __forceinline__ int items_of(const AttendArgs& a, const Request& r, int C) {
   const int64_t rows = (int64_t)r.n * a.group;
   if (rows == 0) return 0;
-  if (rows > a.part_rows) return 1;
+  if (rows > a.part_rows) return a.wide ? 0 : 1;  // the wide kernel's, or not cut
   return max(1, (units_of(r.kv) + C - 1) / C);
 }
 
@@ -398,6 +399,320 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many query rows: prompts and chunks (bf16).
+//
+// A workgroup takes 128 rows of one KV head, 32 a wave, over its request's
+// units of 64 tokens; both tiles of a unit (64 D bytes each) go straight into
+// LDS by DMA, the next unit's under this one's products, one barrier a unit.
+//
+// S^T: the keys stay E4M3 and enter v_mfma_scale_f32_32x32x64_f8f6f4 with their
+// page's exponent as the block scale, so nothing decodes them.  A bf16 q row is
+// 2^e (hi + lo / 16) in E4M3, e from the row's largest value: hi rounds q to 4
+// significant bits and lo holds the other 4, exact down to 2^-14 of the row's
+// largest and within 2^-23 of it below.  Two products of twice the bf16 rate
+// cost what one bf16 product would, and half the LDS bytes.
+// O^T: V is decoded to f16 beside the products (v_cvt_scalef32_pk_f16_fp8).
+//
+// Key row m = 8 a + 4 h + b of tile t stands for token 32 h + 16 t + 4 a + b: a
+// lane (column n, half h) then holds 32 consecutive tokens of its query row.
+// The maximum is followed loosely: O and l are rescaled only when a row's
+// maximum passes its reference by a factor 2^4, p being held as 2^11 p' in f16
+// (p' <= 2^4), so 11 significant bits reach down to 2^-25.
+// ---------------------------------------------------------------------------
+
+constexpr int kWideRows = 32, kWideTile = kWaves * kWideRows;
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
+}
+
+// Wave-wide DMA of 16 bytes per lane from g to LDS address lds + 16 lane.
+__device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory");
+}
+
+__device__ __forceinline__ float swap_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(as_u(x), as_u(x), false, false);
+  return fmaxf(as_f(r[0]), as_f(r[1]));
+}
+__device__ __forceinline__ float swap_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(as_u(x), as_u(x), false, false);
+  return as_f(r[0]) + as_f(r[1]);
+}
+
+// 16-byte chunk of a key row in LDS: eight neighbouring key rows of a matrix
+// operand (tokens 0-3 and 32-35 of a unit) fall on eight different 16-byte columns.
+template <int kD>
+__device__ __forceinline__ int key_swizzle(int token) {
+  if constexpr (kD % 128 == 0)
+    return (token & 3) | ((token >> 5) << 2);
+  else
+    return ((token >> 1) & 1) | ((token >> 5) << 1);
+}
+
+// The tile of 128 rows that workgroup row y takes; b = -1 if there is none.  A
+// request's tiles begin at index floor(start * group / 128) + b, which leaves
+// room for the part tile of every request before it.
+struct WideTile {
+  int64_t b;
+  int tile;
+};
+__device__ __forceinline__ WideTile find_wide(const AttendArgs& a, int64_t y) {
+  int64_t lo = 0, hi = a.batch;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if ((int64_t)max(a.starts[mid], 0) * a.group / kWideTile + mid <= y)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int64_t i = y - ((int64_t)max(a.starts[lo], 0) * a.group / kWideTile + lo);
+  const int64_t rows = (int64_t)request(a, lo).n * a.group, tiles = (rows + kWideTile - 1) / kWideTile;
+  if (rows <= a.part_rows || i < 0 || i >= tiles) return WideTile{-1, 0};
+  return WideTile{lo, (int)(tiles - 1 - i)};  // the last tile sees the most tokens: first
+}
+
+template <int kD>
+__global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(const AttendArgs a) {
+  constexpr int kKS = kD / 64;    // 64-deep steps of S^T; also the DMA steps of a wave and tensor
+  constexpr int kDT = kD / 32;    // 32-channel tiles of O^T
+  constexpr int kKeyChunks = kD / 16;
+  __shared__ __align__(16) uint8_t kbuf[2][kUnit * kD], vbuf[2][kUnit * kD];
+  __shared__ int xk[2][4], xv[2][4];   // scale bytes of a unit's 16-token groups; xv -1: no page
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int n = lane & 31, half = lane >> 5;
+  const int h = blockIdx.x;
+  const WideTile wt = find_wide(a, a.wide_first + blockIdx.y);
+  if (wt.b < 0) return;
+  const Request rq = request(a, wt.b);
+  const int rows = rq.n * a.group, row0 = wt.tile * kWideTile + wave * kWideRows, row = row0 + n;
+  const bool valid = row < rows;
+  const int tok = row / a.group;
+  const int ahead = rq.kv - rq.n + 1;
+  const int limit = !valid ? 0 : a.causal ? ahead + tok : rq.kv;
+  const int first_limit = a.causal ? ahead + row0 / a.group : rq.kv;
+  const int wave_end = row0 >= rows ? 0 : a.causal ? ahead + (min(row0 + kWideRows, rows) - 1) / a.group : rq.kv;
+  const int tile_end = a.causal ? ahead + (min((wt.tile + 1) * kWideTile, rows) - 1) / a.group : rq.kv;
+  const int units = tile_end > 0 ? units_of(tile_end) : 0;
+  const int32_t* table = a.table + wt.b * a.width;
+  const int64_t page_bytes = (int64_t)kD << a.shift;
+  const int ps1 = (1 << a.shift) - 1;
+
+  // this lane's part of a unit's DMA: keys of group `wave`, V of token group vg
+  const int vg = (lane & 3) ^ ((lane >> 3) & 3);
+  auto page_at = [&](int u, int group) {   // the page of a 16-token group, or -1
+    const int t = u * kUnit + 16 * group;
+    const int p = t < rq.kv ? table[t >> a.shift] : -1;
+    return (uint32_t)p < (uint64_t)a.pages ? p : -1;
+  };
+  int sk_next = 0, sv_next = 0;            // threads 0-3: the staged unit's scale bytes
+  auto stage = [&](int u, int buf, int pk, int pv, int px) {
+    const uint8_t* kp = a.k_codes + ((int64_t)max(pk, 0) * a.heads + h) * page_bytes;
+    const uint8_t* vp = a.v_codes + ((int64_t)max(pv, 0) * a.heads + h) * page_bytes;
+#pragma unroll
+    for (int i = 0; i < kKS; ++i) {
+      const int j = i * kWave + lane, token = 16 * wave + j / kKeyChunks;
+      const int chunk = (j % kKeyChunks) ^ key_swizzle<kD>(token);
+      dma16(kp + (int64_t)((u * kUnit + token) & ps1) * kD + chunk * 16,
+            lds_addr(&kbuf[buf][16 * wave * kD + i * 1024]));
+    }
+#pragma unroll
+    for (int i = 0; i < kKS; ++i) {
+      const int d = (wave * kKS + i) * 16 + (lane >> 2);
+      dma16(vp + ((int64_t)d << a.shift) + ((u * kUnit + 16 * vg) & ps1),
+            lds_addr(&vbuf[buf][(wave * kKS + i) * 1024]));
+    }
+    if (tid < 4) {
+      const int64_t s = (int64_t)max(px, 0) * a.heads + h;
+      sk_next = a.k_scales[s];
+      sv_next = a.v_scales[s];
+    }
+  };
+
+  int pk = -1, pv = -1, px = -1;
+  bool hole_next = false;
+  if (units > 0) {
+    pk = page_at(0, wave), pv = page_at(0, vg), px = page_at(0, tid & 3);
+    stage(0, 0, pk, pv, px);
+    hole_next = px < 0;
+    if (units > 1) pk = page_at(1, wave), pv = page_at(1, vg), px = page_at(1, tid & 3);
+  }
+
+  // q as 2^e (hi + lo / 16)
+  v8i qh[kKS], ql[kKS];
+  int eh;
+  {
+    uint4 raw[kKS][4];
+    const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(rq.start + tok) * a.q_stride +
+                         (int64_t)(h * a.group + row % a.group) * kD + half * 32;
+    float mx = 0;
+#pragma unroll
+    for (int s = 0; s < kKS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        raw[s][i] = valid ? *reinterpret_cast<const uint4*>(qp + s * 64 + i * 8) : make_uint4(0, 0, 0, 0);
+        const uint32_t* w = &raw[s][i].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mx = max3f(mx, fabsf(as_f(w[j] << 16)), fabsf(as_f(w[j] & 0xFFFF0000u)));
+      }
+    const uint32_t b = as_u(fmaxf(swap_max(mx), 0x1p-100f));
+    const int e = min((int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0), 120);
+    const float inv = as_f((uint32_t)(127 - e) << 23);
+    eh = e + 127;
+#pragma unroll
+    for (int s = 0; s < kKS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t* w = &raw[s][i].x;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float v[4] = {as_f(w[2 * j] << 16) * inv, as_f(w[2 * j] & 0xFFFF0000u) * inv,
+                        as_f(w[2 * j + 1] << 16) * inv, as_f(w[2 * j + 1] & 0xFFFF0000u) * inv};
+          const uint32_t hi = e4m3_bytes4(v[0], v[1], v[2], v[3]);
+          const f32x2 d0 = e4m3x2_decode<false>(hi), d1 = e4m3x2_decode<true>(hi);
+          qh[s][2 * i + j] = (int)hi;
+          ql[s][2 * i + j] = (int)e4m3_bytes4((v[0] - d0[0]) * 16, (v[1] - d0[1]) * 16, (v[2] - d1[0]) * 16,
+                                              (v[3] - d1[1]) * 16);
+        }
+      }
+  }
+  const int el = eh - 4;
+
+  const float c = a.c, slack = fminf(4.0f / c, 1e37f);
+  float m = -INFINITY, r = 11.0f, l = 0;
+  int R = 1;
+  f32x16 o[kDT];
+#pragma unroll
+  for (int i = 0; i < kDT; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[i][j] = 0;
+
+  for (int u = 0; u < units; ++u) {
+    const int buf = u & 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's DMA of unit u has landed
+    if (tid < 4) {
+      xk[buf][tid] = min(max(sk_next, 1), 254);
+      xv[buf][tid] = hole_next ? -1 : min(max(sv_next, 1), 254);
+    }
+    __syncthreads();
+    if (u + 1 < units) {
+      stage(u + 1, buf ^ 1, pk, pv, px);
+      hole_next = px < 0;
+      if (u + 2 < units) pk = page_at(u + 2, wave), pv = page_at(u + 2, vg), px = page_at(u + 2, tid & 3);
+    }
+    const int x0 = xv[buf][0], x1 = xv[buf][1], x2 = xv[buf][2], x3 = xv[buf][3];
+    const bool hole = min(min(x0, x1), min(x2, x3)) < 0;
+    if (hole || (u + 1) * kUnit > rq.kv) {
+      // codes behind the last token, or of no page, may be anything: V's become 0
+      for (int i = tid; i < 4 * kD; i += kThreads) {
+        const int d = i >> 2, g = (i & 3) ^ ((d >> 1) & 3);
+        const int held = xv[buf][g] < 0 ? 0 : min(max(rq.kv - (u * kUnit + 16 * g), 0), 16);
+        uint32_t* p = reinterpret_cast<uint32_t*>(&vbuf[buf][i * 16]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int nb = min(max(held - 4 * w, 0), 4);
+          if (nb < 4) p[w] &= (1u << (8 * nb)) - 1;
+        }
+      }
+      __syncthreads();
+    }
+    if (u * kUnit >= wave_end) continue;
+
+    // S^T
+    f32x16 s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int token = 32 * ((n >> 2) & 1) + 16 * t + 4 * (n >> 3) + (n & 3), key = key_swizzle<kD>(token);
+      const int sk = xk[buf][2 * ((n >> 2) & 1) + t];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[t][j] = 0;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        const int ch = ks * 4 + half * 2;
+        const uint4 lo = *reinterpret_cast<const uint4*>(&kbuf[buf][token * kD + ((ch ^ key) << 4)]);
+        const uint4 hi = *reinterpret_cast<const uint4*>(&kbuf[buf][token * kD + (((ch + 1) ^ key) << 4)]);
+        const v8i kf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+        s[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, ql[ks], s[t], 0, 0, 0, sk, 0, el);
+        s[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qh[ks], s[t], 0, 0, 0, sk, 0, eh);
+      }
+    }
+    if (hole || (u + 1) * kUnit > first_limit) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int g = 2 * half + t, cnt = xv[buf][g] < 0 ? 0 : limit - (u * kUnit + 16 * g);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j >= cnt) s[t][j] = -INFINITY;
+      }
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[0][j]);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[1][j]);
+    mx = swap_max(mx);
+    const int xr = max(max(x0, x1), max(x2, x3));
+    const bool rise = mx > m + slack;
+    if (__ballot(rise || xr > R)) {
+      const float m_new = rise ? mx : m;
+      const float r_new = m_new == -INFINITY ? 11.0f : __builtin_fmaf(-m_new, c, 11.0f);
+      const float alpha = !rise ? 1.0f : m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(r_new - r);
+      const int R_new = max(R, xr);
+      const float f = R_new - R > 126 ? 0.0f : alpha * as_f((uint32_t)(127 - (R_new - R)) << 23);
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] *= f;
+      m = m_new;
+      r = r_new;
+      R = R_new;
+    }
+    // P and O^T
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t pw[8];
+      float sum = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][2 * j], c, r));
+        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][2 * j + 1], c, r));
+        sum += p0 + p1;
+        pw[j] = cvt_f16x2(p0, p1);
+      }
+      l += sum;
+      const float sv = as_f((uint32_t)(127 - min(max(R - xv[buf][2 * half + t], 0), 60)) << 23);
+      const f16x8 p0 = __builtin_bit_cast(f16x8, make_uint4(pw[0], pw[1], pw[2], pw[3]));
+      const f16x8 p1 = __builtin_bit_cast(f16x8, make_uint4(pw[4], pw[5], pw[6], pw[7]));
+#pragma unroll
+      for (int i = 0; i < kDT; ++i) {
+        const int d = 32 * i + n;
+        const uint4 w = *reinterpret_cast<const uint4*>(&vbuf[buf][d * 64 + (((2 * half + t) ^ ((d >> 1) & 3)) << 4)]);
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.x, w.y, sv), p0, o[i], 0, 0, 0);
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.z, w.w, sv), p1, o[i], 0, 0, 0);
+      }
+    }
+  }
+
+  if (!valid) return;
+  l = swap_sum(l);
+  const float unit = l > 0 ? as_f((uint32_t)R << 23) / l : 0.0f;
+  const int64_t at = ((int64_t)(rq.start + tok) * a.heads * a.group + h * a.group + row % a.group) * kD + 4 * half;
+#pragma unroll
+  for (int i = 0; i < kDT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v[4] = {o[i][4 * j] * unit, o[i][4 * j + 1] * unit, o[i][4 * j + 2] * unit, o[i][4 * j + 3] * unit};
+      store_row<false, 4>(a.out, at + 32 * i + 8 * j, v);
+    }
+}
+
 // Joins the items of each split request: one workgroup per request and KV head.
 template <int kD, bool kF32>
 __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a) {
@@ -441,6 +756,20 @@ int part_rows_of(int64_t max_rows) {
 
 template <int kD, bool kF32>
 hipError_t run(const AttendArgs& a, int64_t max_rows, hipStream_t st) {
+  if constexpr (!kF32) {
+    if (a.wide) {
+      const int64_t wide = a.q_rows * a.group / kWideTile + a.batch;
+      for (int64_t y = 0; y < wide; y += kMaxGridYZ) {
+        AttendArgs w = a;
+        w.wide_first = y;
+        hipLaunchKernelGGL((k_attend_wide<kD>), dim3((unsigned)a.heads, (unsigned)(wide - y < kMaxGridYZ ? wide - y : kMaxGridYZ)),
+                           dim3(kThreads), 0, st, w);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+      }
+      max_rows = kMaxPartRows;
+    }
+  }
   const int64_t tiles = (max_rows + kTile - 1) / kTile;
   const dim3 grid((unsigned)(a.part_o ? most_items(a.batch, a.heads) : a.batch), (unsigned)a.heads,
                   (unsigned)(tiles < 64 ? tiles : 64));
@@ -473,6 +802,11 @@ size_t attend_workspace_bytes(int64_t batch, int64_t heads, int64_t max_rows, in
 hipError_t launch_attend(AttendArgs a, bool bf16, int head_dim, int64_t max_rows, void* workspace,
                          hipStream_t st) {
   a.part_rows = part_rows_of(max_rows);
+  a.wide = bf16 && max_rows > kMaxPartRows;
+  a.wide_first = 0;
+  // scale 0 (all tokens alike) as a scale too small to matter, so that a masked
+  // -inf stays -inf through the product
+  if (a.c < 1e-37f) a.c = 1e-37f;
   a.part_o = a.part_ml = nullptr;
   if (may_split(a.width, a.shift)) {
     a.part_o = (float*)workspace;

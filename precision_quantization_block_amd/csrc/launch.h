@@ -227,7 +227,10 @@ struct AttendArgs {
   float c;                                    // softmax scale times log2(e)
   void* out;                                  // [q_rows, heads * group, D]
   float *part_o, *part_ml;                    // workspace of split rows
-  int32_t part_rows;                          // set by the launcher, as the two above
+  // set by the launcher, as the two above
+  int32_t part_rows;                          // rows of a request that may be split
+  int32_t wide;                               // requests of more rows go to the wide kernel
+  int64_t wide_first;
 };
 // The workspace for at most max_rows = max_q_len * group rows per request.
 size_t attend_workspace_bytes(int64_t batch, int64_t heads, int64_t max_rows, int64_t width,

@@ -412,15 +412,15 @@ pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, in
  * q . k exact products (float32 q in three bf16 parts); p rounded to 11 bits
  * relative to its value down to 2^-29 of the largest (22 bits for float32 q).
  * Shape rules: q_heads a multiple of heads; q_rows * q_heads and
- * table_width * page_size < 2^31 - 256; batch < 2^23; q_stride in [q_heads * head_dim,
+ * table_width * page_size < 2^31 - 256; batch < 2^23 / heads; q_stride in [q_heads * head_dim,
  * 2^40).  scale: finite and >= 0 (else PQB_ERR_VALUE).  Workspace:
  * pqb_kv_attend_workspace_bytes(), its contents on entry do not matter; calls
  * that overlap in time need one each.  Alignment: q, out and workspace 16 bytes,
  * q_stride a multiple of 16 bytes, the int arrays 4.  Errors, before any launch:
  * PQB_ERR_ENUM, PQB_ERR_SHAPE, PQB_ERR_VALUE, PQB_ERR_NULL, PQB_ERR_ALIGN,
  * PQB_ERR_WORKSPACE. */
-size_t pqb_kv_attend_workspace_bytes(int64_t q_rows, int64_t q_heads, int64_t heads,
-                                     int64_t head_dim, int64_t batch, int64_t table_width,
+size_t pqb_kv_attend_workspace_bytes(pqb_dtype dtype, int64_t q_rows, int64_t q_heads,
+                                     int64_t heads, int64_t head_dim, int64_t batch, int64_t table_width,
                                      int page_size, int64_t max_q_len);
 pqb_status pqb_kv_attend_paged(const void* q, pqb_dtype dtype, int64_t q_rows, int64_t q_heads,
                                int64_t q_stride, const pqb_kv_pages* cache,

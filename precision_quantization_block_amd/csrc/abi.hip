@@ -751,17 +751,18 @@ static bool attend_dims_ok(int64_t q_rows, int64_t q_heads, int64_t heads, int64
                            int64_t table_width, int shift) {
   return shift >= 0 && head_dim_ok(head_dim) && heads >= 1 && heads <= 4096 && q_heads >= 1 &&
          q_heads % heads == 0 && q_heads < kPagedMaxTokens && q_rows >= 0 &&
-         q_rows < kPagedMaxTokens / q_heads && batch >= 0 && batch < 1 << 23 && table_width >= 0 &&
+         q_rows < kPagedMaxTokens / q_heads && batch >= 0 && batch < (1 << 23) / heads && table_width >= 0 &&
          table_width < kPagedMaxTokens >> shift;
 }
 
-size_t pqb_kv_attend_workspace_bytes(int64_t q_rows, int64_t q_heads, int64_t heads, int64_t head_dim,
-                                     int64_t batch, int64_t table_width, int page_size,
+size_t pqb_kv_attend_workspace_bytes(pqb_dtype dtype, int64_t q_rows, int64_t q_heads, int64_t heads,
+                                     int64_t head_dim, int64_t batch, int64_t table_width, int page_size,
                                      int64_t max_q_len) {
   const int shift = page_shift(page_size);
-  if (!attend_dims_ok(q_rows, q_heads, heads, head_dim, batch, table_width, shift)) return 0;
-  return attend_workspace_bytes(batch, heads, attend_max_rows(q_rows, q_heads / heads, max_q_len), table_width,
-                                shift, (int)head_dim);
+  if (!valid_dtype(dtype) || !attend_dims_ok(q_rows, q_heads, heads, head_dim, batch, table_width, shift)) return 0;
+  const int64_t group = q_heads / heads;
+  return attend_workspace_bytes(q_rows, batch, heads, group, attend_max_rows(q_rows, group, max_q_len), table_width,
+                                shift, (int)head_dim, dtype == PQB_BF16);
 }
 
 pqb_status pqb_kv_attend_paged(const void* q, pqb_dtype dtype, int64_t q_rows, int64_t q_heads,
@@ -787,7 +788,8 @@ pqb_status pqb_kv_attend_paged(const void* q, pqb_dtype dtype, int64_t q_rows, i
   const int64_t group = q_heads / cache->heads, max_rows = attend_max_rows(q_rows, group, max_q_len);
   // with no page at all every table entry is out of range: nothing is seen
   const int64_t width = cache->pages ? table_width : 0;
-  const size_t need = attend_workspace_bytes(batch, cache->heads, max_rows, width, shift, (int)cache->head_dim);
+  const size_t need = attend_workspace_bytes(q_rows, batch, cache->heads, group, max_rows, width, shift,
+                                             (int)cache->head_dim, dtype == PQB_BF16);
   if (workspace_bytes < need) return PQB_ERR_WORKSPACE;
   if (need && !workspace) return PQB_ERR_NULL;
   AttendArgs a{};

@@ -17,6 +17,8 @@
 // the rounding's remainder as a second f16 part).  V enters as dec(c) 2^(X - R),
 // exact in f16 unless X is over 15 below R, the largest V exponent met so far; O
 // is kept in units of 2^R and rescaled when R or the row's maximum rises.
+#include <algorithm>
+
 #include "launch.h"
 #include "paged.h"
 
@@ -30,10 +32,12 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kUnit = 64;        // tokens a wave takes at a time
 constexpr int kTile = 16;        // query rows of a tile
 constexpr int kWaves = 4, kThreads = kWaves * kWave;
-constexpr int kMinUnits = kWaves;                 // fewest units of a split
-constexpr int kMaxPartRows = 64;                  // rows of a request that may be split
+constexpr int kMinUnits = 2 * kWaves;             // fewest units of a split
+constexpr int kMaxPartRows = 64;                  // rows of a float32 request that may be split
 constexpr int64_t kGroupsWanted = 1024;           // workgroups a split aims at
 constexpr int64_t kMaxGridYZ = 65535;
+constexpr int kMinWideUnits = 4;                  // the same for the wide kernel
+constexpr int64_t kMaxWideSplits = 32, kWideGroupsWanted = 1024;
 
 // ---------------------------------------------------------------------------
 // Work items.  Request b has u_b = ceil(kv_len / 64) units and is cut into
@@ -240,10 +244,18 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 #pragma unroll
     for (int i = 0; i < kDT; ++i) o[i] = f32x4{0, 0, 0, 0};
 
-    for (int u = unit0 + wave; u < end; u += kWaves) {
-      // the page of this lane's key rows (group col / 4) and of its V tokens (group g4)
+    // the pages of this lane's key rows (group col / 4) and of its V tokens (group
+    // g4), read a step ahead of the codes that they lead to
+    int pk1 = -1, pv1 = -1;
+    auto pages_at = [&](int u) {
       const int tk = u * kUnit + 16 * (col >> 2), tv = u * kUnit + 16 * g4;
-      const int pk0 = tk < rq.kv ? table[tk >> a.shift] : -1, pv0 = tv < rq.kv ? table[tv >> a.shift] : -1;
+      pk1 = tk < rq.kv ? table[tk >> a.shift] : -1;
+      pv1 = tv < rq.kv ? table[tv >> a.shift] : -1;
+    };
+    if (unit0 + wave < end) pages_at(unit0 + wave);
+    for (int u = unit0 + wave; u < end; u += kWaves) {
+      const int tk = u * kUnit + 16 * (col >> 2), tv = u * kUnit + 16 * g4;
+      const int pk0 = pk1, pv0 = pv1;
       const bool okk = (uint32_t)pk0 < (uint64_t)a.pages, okv = (uint32_t)pv0 < (uint64_t)a.pages;
       const int64_t pk = (int64_t)(okk ? pk0 : 0) * a.heads + h, pv = (int64_t)(okv ? pv0 : 0) * a.heads + h;
       uint4 kw[4][kKC], vw[kDT];
@@ -258,6 +270,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
         vw[i] = *reinterpret_cast<const uint4*>(vp + ((int64_t)i << (a.shift + 4)));
       const float sk = e8m0_pow2(a.k_scales[pk]);
       const int xv = min(max((int)a.v_scales[pv], 1), 254);
+      if (u + kWaves < end) pages_at(u + kWaves);
 
       f32x4 s[4];
 #pragma unroll
@@ -416,9 +429,10 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 //
 // Key row m = 8 a + 4 h + b of tile t stands for token 32 h + 16 t + 4 a + b: a
 // lane (column n, half h) then holds 32 consecutive tokens of its query row.
-// The maximum is followed loosely: O and l are rescaled only when a row's
-// maximum passes its reference by a factor 2^4, p being held as 2^11 p' in f16
-// (p' <= 2^4), so 11 significant bits reach down to 2^-25.
+// The maximum is followed loosely: p is held as 2^11 p' in f16 relative to a
+// reference that moves (and O and l with it) only when a lane's sum of p over a
+// unit passes 2^15, so a p' is at most 2^4 and 11 significant bits reach down to
+// 2^-25 of the reference.
 // ---------------------------------------------------------------------------
 
 constexpr int kWideRows = 32, kWideTile = kWaves * kWideRows;
@@ -433,6 +447,12 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // Wave-wide DMA of 16 bytes per lane from g to LDS address lds + 16 lane.
 __device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory");
+}
+
+// The same from a wave-uniform base plus an unsigned 32-bit offset per lane.
+__device__ __forceinline__ void dma16s(const void* g, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(g), "s"(lds)
+               : "memory");
 }
 
 __device__ __forceinline__ float swap_max(float x) {
@@ -476,13 +496,27 @@ __device__ __forceinline__ WideTile find_wide(const AttendArgs& a, int64_t y) {
   return WideTile{lo, (int)(tiles - 1 - i)};  // the last tile sees the most tokens: first
 }
 
-template <int kD>
+// A tile whose rows see `end` tokens at most is cut into `count` splits of `per`
+// units (the grid's z), so that few tiles over long requests fill the chip.
+struct WideSplit {
+  int units, per, count;
+};
+__device__ __forceinline__ WideSplit wide_split(const AttendArgs& a, int end) {
+  WideSplit w;
+  w.units = end > 0 ? units_of(end) : 0;
+  w.per = max((w.units + a.wide_splits - 1) / a.wide_splits, kMinWideUnits);
+  w.count = max((w.units + w.per - 1) / w.per, 1);
+  return w;
+}
+
+template <int kD, bool kWholePages>
 __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(const AttendArgs a) {
   constexpr int kKS = kD / 64;    // 64-deep steps of S^T; also the DMA steps of a wave and tensor
   constexpr int kDT = kD / 32;    // 32-channel tiles of O^T
   constexpr int kKeyChunks = kD / 16;
   __shared__ __align__(16) uint8_t kbuf[2][kUnit * kD], vbuf[2][kUnit * kD];
-  __shared__ int xk[2][4], xv[2][4];   // scale bytes of a unit's 16-token groups; xv -1: no page
+  // scale bytes of the staged units' 16-token groups (one page a unit: the first); xv -1: no page
+  __shared__ int xk[2][4], xv[2][4];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n = lane & 31, half = lane >> 5;
@@ -494,53 +528,84 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   const bool valid = row < rows;
   const int tok = row / a.group;
   const int ahead = rq.kv - rq.n + 1;
-  const int limit = !valid ? 0 : a.causal ? ahead + tok : rq.kv;
+  const int limit = a.causal && valid ? ahead + tok : rq.kv;
   const int first_limit = a.causal ? ahead + row0 / a.group : rq.kv;
   const int wave_end = row0 >= rows ? 0 : a.causal ? ahead + (min(row0 + kWideRows, rows) - 1) / a.group : rq.kv;
   const int tile_end = a.causal ? ahead + (min((wt.tile + 1) * kWideTile, rows) - 1) / a.group : rq.kv;
-  const int units = tile_end > 0 ? units_of(tile_end) : 0;
+  const int split = blockIdx.z;
+  const WideSplit ws = wide_split(a, tile_end);
+  if (split >= ws.count) return;
+  const int u0 = __builtin_amdgcn_readfirstlane(split * ws.per);
+  const int units = __builtin_amdgcn_readfirstlane(min(ws.units, u0 + ws.per));
   const int32_t* table = a.table + wt.b * a.width;
   const int64_t page_bytes = (int64_t)kD << a.shift;
   const int ps1 = (1 << a.shift) - 1;
 
-  // this lane's part of a unit's DMA: keys of group `wave`, V of token group vg
+  // Staging.  A wave's DMA takes the keys of 16-token group `wave` and a quarter of
+  // V's channels; this lane's V bytes are of group vg.  Keys are staged a unit
+  // ahead of V: S^T of unit u + 1 is formed under the softmax of unit u.  Where a
+  // unit lies in one page, the page is uniform and only offsets are per lane.
   const int vg = (lane & 3) ^ ((lane >> 3) & 3);
-  auto page_at = [&](int u, int group) {   // the page of a 16-token group, or -1
-    const int t = u * kUnit + 16 * group;
-    const int p = t < rq.kv ? table[t >> a.shift] : -1;
+  uint32_t koff[kKS], voff[kKS];
+#pragma unroll
+  for (int i = 0; i < kKS; ++i) {
+    const int j = i * kWave + lane, token = 16 * wave + j / kKeyChunks;
+    const int chunk = (j % kKeyChunks) ^ key_swizzle<kD>(token), d = (wave * kKS + i) * 16 + (lane >> 2);
+    koff[i] = (uint32_t)((kWholePages ? token : token & 15) * kD + chunk * 16);
+    voff[i] = (uint32_t)((d << a.shift) + (kWholePages ? 16 * vg : 0));
+  }
+  auto page_at = [&](int u, int group) {   // the page of a 16-token group (of the whole unit), or -1
+    const int t = u * kUnit + (kWholePages ? 0 : 16 * group);
+    int p = t < rq.kv ? table[t >> a.shift] : -1;
+    if constexpr (kWholePages) p = __builtin_amdgcn_readfirstlane(p);
     return (uint32_t)p < (uint64_t)a.pages ? p : -1;
   };
-  int sk_next = 0, sv_next = 0;            // threads 0-3: the staged unit's scale bytes
-  auto stage = [&](int u, int buf, int pk, int pv, int px) {
-    const uint8_t* kp = a.k_codes + ((int64_t)max(pk, 0) * a.heads + h) * page_bytes;
-    const uint8_t* vp = a.v_codes + ((int64_t)max(pv, 0) * a.heads + h) * page_bytes;
+  auto stage_k = [&](int u, int pk) {
+    const uint8_t* kp = a.k_codes + ((int64_t)max(pk, 0) * a.heads + h) * page_bytes +
+                        (int64_t)((u * kUnit + (kWholePages ? 0 : 16 * wave)) & ps1) * kD;
 #pragma unroll
     for (int i = 0; i < kKS; ++i) {
-      const int j = i * kWave + lane, token = 16 * wave + j / kKeyChunks;
-      const int chunk = (j % kKeyChunks) ^ key_swizzle<kD>(token);
-      dma16(kp + (int64_t)((u * kUnit + token) & ps1) * kD + chunk * 16,
-            lds_addr(&kbuf[buf][16 * wave * kD + i * 1024]));
-    }
-#pragma unroll
-    for (int i = 0; i < kKS; ++i) {
-      const int d = (wave * kKS + i) * 16 + (lane >> 2);
-      dma16(vp + ((int64_t)d << a.shift) + ((u * kUnit + 16 * vg) & ps1),
-            lds_addr(&vbuf[buf][(wave * kKS + i) * 1024]));
-    }
-    if (tid < 4) {
-      const int64_t s = (int64_t)max(px, 0) * a.heads + h;
-      sk_next = a.k_scales[s];
-      sv_next = a.v_scales[s];
+      const uint32_t to = lds_addr(&kbuf[u & 1][16 * wave * kD + i * 1024]);
+      if constexpr (kWholePages)
+        dma16s(kp, koff[i], to);
+      else
+        dma16(kp + koff[i], to);
     }
   };
-
-  int pk = -1, pv = -1, px = -1;
+  auto stage_v = [&](int u, int pv) {
+    const uint8_t* vp = a.v_codes + ((int64_t)max(pv, 0) * a.heads + h) * page_bytes +
+                        ((u * kUnit + (kWholePages ? 0 : 16 * vg)) & ps1);
+#pragma unroll
+    for (int i = 0; i < kKS; ++i) {
+      const uint32_t to = lds_addr(&vbuf[u & 1][(wave * kKS + i) * 1024]);
+      if constexpr (kWholePages)
+        dma16s(vp, voff[i], to);
+      else
+        dma16(vp + voff[i], to);
+    }
+  };
+  // Threads 0-3 carry the scale bytes of their group of a staged unit into LDS.
+  int sk_next = 0, sv_next = 0;
   bool hole_next = false;
-  if (units > 0) {
-    pk = page_at(0, wave), pv = page_at(0, vg), px = page_at(0, tid & 3);
-    stage(0, 0, pk, pv, px);
-    hole_next = px < 0;
-    if (units > 1) pk = page_at(1, wave), pv = page_at(1, vg), px = page_at(1, tid & 3);
+  auto scale_at = [&](const uint8_t* x, int px) { return (int)x[(int64_t)max(px, 0) * a.heads + h]; };
+  const int mine = kWholePages ? 0 : tid & 3;
+
+  int pk = -1, pv = -1, px = -1, px1 = -1;   // pages of unit u + 2 (keys, scales) and u + 1 (V, scales)
+  if (u0 < units) {
+    pk = page_at(u0, wave), px = page_at(u0, mine);
+    stage_k(u0, pk);
+    stage_v(u0, page_at(u0, vg));
+    if (tid < 4) {
+      xk[u0 & 1][tid] = min(max(scale_at(a.k_scales, px), 1), 254);
+      sv_next = scale_at(a.v_scales, px);
+      hole_next = px < 0;
+    }
+    if (u0 + 1 < units) {
+      stage_k(u0 + 1, page_at(u0 + 1, wave));
+      pv = page_at(u0 + 1, vg), px1 = page_at(u0 + 1, mine);
+      if (tid < 4) sk_next = scale_at(a.k_scales, px1);
+    }
+    if (u0 + 2 < units) pk = page_at(u0 + 2, wave), px = page_at(u0 + 2, mine);
   }
 
   // q as 2^e (hi + lo / 16)
@@ -584,8 +649,10 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   }
   const int el = eh - 4;
 
-  const float c = a.c, slack = fminf(4.0f / c, 1e37f);
-  float m = -INFINITY, r = 11.0f, l = 0;
+  const float c = a.c;
+  // m: the row's reference (the maximum when it was last moved), r = 11 - m c; O
+  // and l hold 2^11 p' relative to it.  r starts infinite: the first unit moves it.
+  float m = -INFINITY, r = INFINITY, l = 0;
   int R = 1;
   f32x16 o[kDT];
 #pragma unroll
@@ -593,26 +660,78 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[i][j] = 0;
 
-  for (int u = 0; u < units; ++u) {
+  auto scores = [&](int u, f32x16* to) {   // S^T of unit u
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int token = 32 * ((n >> 2) & 1) + 16 * t + 4 * (n >> 3) + (n & 3), key = key_swizzle<kD>(token);
+      const int sk = xk[u & 1][kWholePages ? 0 : 2 * ((n >> 2) & 1) + t];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) to[t][j] = 0;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        const int ch = ks * 4 + half * 2;
+        const uint4 lo = *reinterpret_cast<const uint4*>(&kbuf[u & 1][token * kD + ((ch ^ key) << 4)]);
+        const uint4 hi = *reinterpret_cast<const uint4*>(&kbuf[u & 1][token * kD + (((ch + 1) ^ key) << 4)]);
+        const v8i kf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+        to[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, ql[ks], to[t], 0, 0, 0, sk, 0, el);
+        to[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qh[ks], to[t], 0, 0, 0, sk, 0, eh);
+      }
+    }
+  };
+  // P of one unit as f16 pairs, and this lane's sum
+  auto weights = [&](const f32x16* s, float r, uint32_t (*pw)[8]) {
+    float sum = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][2 * j], c, r));
+        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][2 * j + 1], c, r));
+        sum += p0;
+        sum += p1;
+        pw[t][j] = cvt_f16x2(p0, p1);
+      }
+    return sum;
+  };
+
+  // One unit: s holds its S^T, next receives the following unit's.
+  auto unit = [&](int u, f32x16* s, f32x16* next) {
     const int buf = u & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's DMA of unit u has landed
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's DMA: keys of u + 1, V of u
     if (tid < 4) {
-      xk[buf][tid] = min(max(sk_next, 1), 254);
+      xk[buf ^ 1][tid] = min(max(sk_next, 1), 254);
       xv[buf][tid] = hole_next ? -1 : min(max(sv_next, 1), 254);
     }
     __syncthreads();
     if (u + 1 < units) {
-      stage(u + 1, buf ^ 1, pk, pv, px);
-      hole_next = px < 0;
-      if (u + 2 < units) pk = page_at(u + 2, wave), pv = page_at(u + 2, vg), px = page_at(u + 2, tid & 3);
+      stage_v(u + 1, pv);
+      if (tid < 4) {
+        sv_next = scale_at(a.v_scales, px1);
+        hole_next = px1 < 0;
+      }
+      if (u + 2 < units) {
+        stage_k(u + 2, pk);
+        px1 = kWholePages ? pk : px;
+        if (tid < 4) sk_next = scale_at(a.k_scales, px1);
+        pv = kWholePages ? pk : page_at(u + 2, vg);
+        if (u + 3 < units) {
+          pk = page_at(u + 3, wave);
+          if (!kWholePages) px = page_at(u + 3, mine);
+        }
+      }
     }
-    const int x0 = xv[buf][0], x1 = xv[buf][1], x2 = xv[buf][2], x3 = xv[buf][3];
-    const bool hole = min(min(x0, x1), min(x2, x3)) < 0;
-    if (hole || (u + 1) * kUnit > rq.kv) {
+    int xr, lo;   // the unit's largest V exponent; negative lo: some page is none
+    if constexpr (kWholePages) {
+      xr = lo = __builtin_amdgcn_readfirstlane(xv[buf][0]);
+    } else {
+      const int x0 = xv[buf][0], x1 = xv[buf][1], x2 = xv[buf][2], x3 = xv[buf][3];
+      xr = max(max(x0, x1), max(x2, x3)), lo = min(min(x0, x1), min(x2, x3));
+    }
+    if (lo < 0 || (u + 1) * kUnit > rq.kv) {
       // codes behind the last token, or of no page, may be anything: V's become 0
       for (int i = tid; i < 4 * kD; i += kThreads) {
         const int d = i >> 2, g = (i & 3) ^ ((d >> 1) & 3);
-        const int held = xv[buf][g] < 0 ? 0 : min(max(rq.kv - (u * kUnit + 16 * g), 0), 16);
+        const int held = xv[buf][kWholePages ? 0 : g] < 0 ? 0 : min(max(rq.kv - (u * kUnit + 16 * g), 0), 16);
         uint32_t* p = reinterpret_cast<uint32_t*>(&vbuf[buf][i * 16]);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -622,47 +741,34 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
       }
       __syncthreads();
     }
-    if (u * kUnit >= wave_end) continue;
+    if (u * kUnit >= wave_end) return;
 
-    // S^T
-    f32x16 s[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int token = 32 * ((n >> 2) & 1) + 16 * t + 4 * (n >> 3) + (n & 3), key = key_swizzle<kD>(token);
-      const int sk = xk[buf][2 * ((n >> 2) & 1) + t];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[t][j] = 0;
-#pragma unroll
-      for (int ks = 0; ks < kKS; ++ks) {
-        const int ch = ks * 4 + half * 2;
-        const uint4 lo = *reinterpret_cast<const uint4*>(&kbuf[buf][token * kD + ((ch ^ key) << 4)]);
-        const uint4 hi = *reinterpret_cast<const uint4*>(&kbuf[buf][token * kD + (((ch + 1) ^ key) << 4)]);
-        const v8i kf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-        s[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, ql[ks], s[t], 0, 0, 0, sk, 0, el);
-        s[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qh[ks], s[t], 0, 0, 0, sk, 0, eh);
-      }
-    }
-    if (hole || (u + 1) * kUnit > first_limit) {
+    if (lo < 0 || (u + 1) * kUnit > first_limit) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int g = 2 * half + t, cnt = xv[buf][g] < 0 ? 0 : limit - (u * kUnit + 16 * g);
+        const int g = 2 * half + t, cnt = xv[buf][kWholePages ? 0 : g] < 0 ? 0 : limit - (u * kUnit + 16 * g);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (j >= cnt) s[t][j] = -INFINITY;
       }
     }
-    float mx = s[0][0];
+    // The next unit's S^T (of whatever LDS holds behind the last unit: unused)
+    // beside this unit's P.
+    scores(u + 1, next);
+    uint32_t pw[2][8];
+    float sum = weights(s, r, pw);
+    // No maximum is taken while P fits: a p of 2^15 or more, or the first unit's
+    // infinite r, shows in the sum.
+    if (__ballot(!(sum <= 0x1p15f)) || xr > R) {
+      float mx = s[0][0];
 #pragma unroll
-    for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[0][j]);
+      for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[0][j]);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[1][j]);
-    mx = swap_max(mx);
-    const int xr = max(max(x0, x1), max(x2, x3));
-    const bool rise = mx > m + slack;
-    if (__ballot(rise || xr > R)) {
-      const float m_new = rise ? mx : m;
-      const float r_new = m_new == -INFINITY ? 11.0f : __builtin_fmaf(-m_new, c, 11.0f);
-      const float alpha = !rise ? 1.0f : m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(r_new - r);
+      for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[1][j]);
+      const float m_new = fmaxf(m, swap_max(mx));
+      const bool none = m_new == -INFINITY;
+      const float r_new = none ? 11.0f : __builtin_fmaf(-m_new, c, 11.0f);
+      const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(r_new - r);
       const int R_new = max(R, xr);
       const float f = R_new - R > 126 ? 0.0f : alpha * as_f((uint32_t)(127 - (R_new - R)) << 23);
       l *= alpha;
@@ -670,26 +776,18 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
       for (int i = 0; i < kDT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] *= f;
+      sum = weights(s, r_new, pw);
       m = m_new;
-      r = r_new;
+      r = none ? INFINITY : r_new;
       R = R_new;
     }
-    // P and O^T
+    l += sum;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      uint32_t pw[8];
-      float sum = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][2 * j], c, r));
-        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][2 * j + 1], c, r));
-        sum += p0 + p1;
-        pw[j] = cvt_f16x2(p0, p1);
-      }
-      l += sum;
-      const float sv = as_f((uint32_t)(127 - min(max(R - xv[buf][2 * half + t], 0), 60)) << 23);
-      const f16x8 p0 = __builtin_bit_cast(f16x8, make_uint4(pw[0], pw[1], pw[2], pw[3]));
-      const f16x8 p1 = __builtin_bit_cast(f16x8, make_uint4(pw[4], pw[5], pw[6], pw[7]));
+      const int x = kWholePages ? xr : xv[buf][2 * half + t];
+      const float sv = as_f((uint32_t)(127 - min(max(R - x, 0), 60)) << 23);
+      const f16x8 p0 = __builtin_bit_cast(f16x8, make_uint4(pw[t][0], pw[t][1], pw[t][2], pw[t][3]));
+      const f16x8 p1 = __builtin_bit_cast(f16x8, make_uint4(pw[t][4], pw[t][5], pw[t][6], pw[t][7]));
 #pragma unroll
       for (int i = 0; i < kDT; ++i) {
         const int d = 32 * i + n;
@@ -698,121 +796,261 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.z, w.w, sv), p1, o[i], 0, 0, 0);
       }
     }
+  };
+
+  f32x16 sa[2], sb[2];
+  if (u0 < units) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    scores(u0, sa);
+  }
+  for (int u = u0; u < units; u += 2) {
+    unit(u, sa, sb);
+    if (u + 1 < units) unit(u + 1, sb, sa);
   }
 
   if (!valid) return;
   l = swap_sum(l);
-  const float unit = l > 0 ? as_f((uint32_t)R << 23) / l : 0.0f;
-  const int64_t at = ((int64_t)(rq.start + tok) * a.heads * a.group + h * a.group + row % a.group) * kD + 4 * half;
+  const int64_t out_row = (int64_t)(rq.start + tok) * a.heads * a.group + h * a.group + row % a.group;
+  if (ws.count == 1) {
+    const float scale = l > 0 ? as_f((uint32_t)R << 23) / l : 0.0f;
 #pragma unroll
-  for (int i = 0; i < kDT; ++i)
+    for (int i = 0; i < kDT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float v[4] = {o[i][4 * j] * unit, o[i][4 * j + 1] * unit, o[i][4 * j + 2] * unit, o[i][4 * j + 3] * unit};
-      store_row<false, 4>(a.out, at + 32 * i + 8 * j, v);
+      for (int j = 0; j < 4; ++j) {
+        const float v[4] = {o[i][4 * j] * scale, o[i][4 * j + 1] * scale, o[i][4 * j + 2] * scale,
+                            o[i][4 * j + 3] * scale};
+        store_row<false, 4>(a.out, out_row * kD + 4 * half + 32 * i + 8 * j, v);
+      }
+  } else {
+    const int64_t slot = (int64_t)split * a.q_rows * a.heads * a.group + out_row;
+    const float scale = as_f((uint32_t)R << 23) * 0x1p-11f;
+#pragma unroll
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v[4] = {o[i][4 * j] * scale, o[i][4 * j + 1] * scale, o[i][4 * j + 2] * scale,
+                            o[i][4 * j + 3] * scale};
+        store_row<true, 4>(a.wide_o, slot * kD + 4 * half + 32 * i + 8 * j, v);
+      }
+    if (half == 0) {
+      a.wide_ml[2 * slot] = m;
+      a.wide_ml[2 * slot + 1] = l * 0x1p-11f;
     }
-}
-
-// Joins the items of each split request: one workgroup per request and KV head.
-template <int kD, bool kF32>
-__global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a) {
-  const int h = blockIdx.y, C = split_units(a);
-  const Item it = find_item<true>(a, blockIdx.x, C);
-  if (it.count < 2) return;
-  const Request rq = request(a, it.b);
-  const int rows = rq.n * a.group, tid = threadIdx.x;
-  for (int e = tid; e < rows * (kD / 4); e += kThreads) {
-    const int row = e / (kD / 4), d = e % (kD / 4) * 4;
-    const int64_t step = (int64_t)a.heads * a.part_rows;
-    const int64_t slot0 = (it.first * a.heads + h) * a.part_rows + row;
-    float M = -INFINITY;
-    for (int i = 0; i < it.count; ++i) M = fmaxf(M, a.part_ml[2 * (slot0 + i * step)]);
-    float L = 0, acc[4] = {0, 0, 0, 0};
-    for (int i = 0; i < it.count; ++i) {
-      const int64_t slot = slot0 + i * step;
-      const float mi = a.part_ml[2 * slot], wt = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mi - M) * a.c);
-      const uint4 w = *reinterpret_cast<const uint4*>(a.part_o + slot * kD + d);
-      L += a.part_ml[2 * slot + 1] * wt;
-      acc[0] += as_f(w.x) * wt;
-      acc[1] += as_f(w.y) * wt;
-      acc[2] += as_f(w.z) * wt;
-      acc[3] += as_f(w.w) * wt;
-    }
-    const float inv = L > 0 ? 1.0f / L : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] *= inv;
-    store_row<kF32, 4>(a.out, ((int64_t)(rq.start + row / a.group) * a.heads * a.group + h * a.group +
-                               row % a.group) * kD + d, acc);
   }
 }
 
-int64_t most_items(int64_t batch, int64_t heads) { return (kGroupsWanted + heads - 1) / heads + batch; }
+// Joins what was split: workgroups below `row_groups` take one request, KV head and
+// row (z, strided) of the row kernel's items; the others kGroups rows of the wide
+// kernel's each.  D / 4 threads cover a row.
+template <int kD, bool kF32>
+__device__ __forceinline__ void join_items(const AttendArgs& a, int64_t b, int h, int z, int nz) {
+  constexpr int kQuads = kD / 4, kGroups = kThreads / kQuads;
+  __shared__ float red_m[kWaves], red_l[kGroups];
+  __shared__ f32x4 red_o[kGroups][kQuads];
+  const Item it = find_item<true>(a, b, split_units(a));
+  if (it.count < 2) return;
+  const Request rq = request(a, b);
+  const int rows = rq.n * a.group, tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int quad = tid % kQuads, grp = tid / kQuads;   // every kGroups-th item; the sums meet in LDS
+  const int64_t step = (int64_t)a.heads * a.part_rows;
+  for (int row = z; row < rows; row += nz) {
+    const int64_t slot0 = (it.first * a.heads + h) * a.part_rows + row;
+    float M = -INFINITY;
+    for (int i = tid; i < it.count; i += kThreads) M = fmaxf(M, a.part_ml[2 * (slot0 + i * step)]);
+#pragma unroll
+    for (int d = kWave / 2; d; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
+    __syncthreads();  // the last row's reads of LDS are done
+    if (lane == 0) red_m[tid / kWave] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) M = fmaxf(M, red_m[w]);
+    float L = 0;
+    f32x4 acc = {0, 0, 0, 0};
+    if (grp < kGroups) {
+      for (int i = grp; i < it.count; i += kGroups) {
+        const int64_t slot = slot0 + i * step;
+        const float mi = a.part_ml[2 * slot], wt = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mi - M) * a.c);
+        L += a.part_ml[2 * slot + 1] * wt;
+        acc += *reinterpret_cast<const f32x4*>(a.part_o + slot * kD + 4 * quad) * wt;
+      }
+      red_o[grp][quad] = acc;
+      if (quad == 0) red_l[grp] = L;
+    }
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) {
+        acc += red_o[g][quad];
+        L += red_l[g];
+      }
+      const float inv = L > 0 ? 1.0f / L : 0.0f;
+      const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+      store_row<kF32, 4>(a.out, ((int64_t)(rq.start + row / a.group) * a.heads * a.group + h * a.group +
+                                 row % a.group) * kD + 4 * quad, v);
+    }
+  }
+}
+
+template <int kD>
+__device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t group) {
+  constexpr int kQuads = kD / 4, kGroups = kThreads / kQuads;
+  const int tid = threadIdx.x, quad = tid % kQuads, grp = tid / kQuads, q_heads = a.heads * a.group;
+  const int64_t total = a.q_rows * q_heads, at = group * kGroups + grp;
+  if (grp >= kGroups || at >= total) return;
+  const int t = (int)(at / q_heads), g = (int)(at % q_heads) % a.group;
+  int64_t lo = 0, hi = a.batch;   // the request of query row t
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (a.starts[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const Request rq = request(a, lo);
+  const int rows = rq.n * a.group, tok = t - rq.start;
+  if (rows <= a.part_rows || tok < 0 || tok >= rq.n) return;
+  const int last = min((tok * a.group + g) / kWideTile * kWideTile + kWideTile, rows) - 1;
+  const int n = wide_split(a, a.causal ? rq.kv - rq.n + 1 + last / a.group : rq.kv).count;
+  if (n < 2) return;
+  float M = -INFINITY, L = 0;
+  f32x4 acc = {0, 0, 0, 0};
+  for (int i = 0; i < n; ++i) M = fmaxf(M, a.wide_ml[2 * (i * total + at)]);
+  for (int i = 0; i < n; ++i) {
+    const int64_t slot = i * total + at;
+    const float mi = a.wide_ml[2 * slot], wt = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mi - M) * a.c);
+    L += a.wide_ml[2 * slot + 1] * wt;
+    acc += *reinterpret_cast<const f32x4*>(a.wide_o + slot * kD + 4 * quad) * wt;
+  }
+  const float inv = L > 0 ? 1.0f / L : 0.0f;
+  const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+  store_row<false, 4>(a.out, at * kD + 4 * quad, v);
+}
+
+template <int kD, bool kF32>
+__global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, int64_t row_groups, int nz) {
+  const int64_t x = blockIdx.x;
+  if (x < row_groups) {
+    const int64_t bh = x / nz;
+    join_items<kD, kF32>(a, bh / a.heads, (int)(bh % a.heads), (int)(x % nz), nz);
+  } else if constexpr (!kF32) {
+    join_wide<kD>(a, x - row_groups);
+  }
+}
+
+// Items that the lengths can lead to: their number is bounded by what a split
+// aims at, and by the table's width.
+int64_t most_items(int64_t batch, int64_t heads, int64_t width, int shift) {
+  const int64_t wanted = (kGroupsWanted + heads - 1) / heads + batch;
+  const int64_t each = ((width << shift) + kMinUnits * kUnit - 1) / (kMinUnits * kUnit);
+  return each * batch < wanted ? each * batch : wanted;
+}
 
 bool may_split(int64_t width, int shift) { return (width << shift) > (int64_t)kMinUnits * kUnit; }
 
-int part_rows_of(int64_t max_rows) {
-  return (int)((max_rows < kMaxPartRows ? max_rows + kTile - 1 : kMaxPartRows) / kTile * kTile);
+// How a call is laid out; the workspace query and the launch agree on it.
+struct Plan {
+  bool wide;
+  int part_rows;       // most rows of a request for the row kernel's splits
+  int64_t items;       // of the row kernel (0: nothing can be split)
+  int wide_splits;
+  size_t part_o, part_ml, wide_o, wide_ml, bytes;   // floats before each part, and all bytes
+};
+
+Plan plan_of(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_t max_rows, int64_t width,
+             int shift, int head_dim, bool bf16) {
+  Plan p{};
+  p.wide = bf16 && max_rows > kTile;
+  const int64_t most = bf16 ? kTile : kMaxPartRows;
+  p.part_rows = (int)((max_rows < most ? max_rows + kTile - 1 : most) / kTile * kTile);
+  p.items = may_split(width, shift) ? most_items(batch, heads, width, shift) : 0;
+  p.wide_splits = 1;
+  if (p.wide && (width << shift) > (int64_t)kMinWideUnits * kUnit) {
+    const int64_t groups = (q_rows * group + kWideTile - 1) / kWideTile * heads;
+    p.wide_splits = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxWideSplits, kWideGroupsWanted / groups));
+  }
+  const size_t rows = (size_t)p.items * heads * p.part_rows;
+  const size_t wide = p.wide_splits > 1 ? (size_t)p.wide_splits * q_rows * heads * group : 0;
+  p.part_ml = rows * head_dim;
+  p.wide_o = p.part_ml + (rows * 2 + 3) / 4 * 4;
+  p.wide_ml = p.wide_o + wide * head_dim;
+  p.bytes = 4 * (p.wide_ml + wide * 2);
+  return p;
+}
+
+template <int kD>
+hipError_t run_wide(AttendArgs a, const Plan& p, hipStream_t st) {
+  const int64_t tiles = a.q_rows * a.group / kWideTile + a.batch;
+  for (a.wide_first = 0; a.wide_first < tiles; a.wide_first += kMaxGridYZ) {
+    const int64_t left = tiles - a.wide_first;
+    const dim3 grid((unsigned)a.heads, (unsigned)(left < kMaxGridYZ ? left : kMaxGridYZ), (unsigned)p.wide_splits);
+    if ((1 << a.shift) >= kUnit)
+      hipLaunchKernelGGL((k_attend_wide<kD, true>), grid, dim3(kThreads), 0, st, a);
+    else
+      hipLaunchKernelGGL((k_attend_wide<kD, false>), grid, dim3(kThreads), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int kD, bool kF32>
-hipError_t run(const AttendArgs& a, int64_t max_rows, hipStream_t st) {
+hipError_t run(const AttendArgs& a, const Plan& p, int64_t max_rows, hipStream_t st) {
   if constexpr (!kF32) {
-    if (a.wide) {
-      const int64_t wide = a.q_rows * a.group / kWideTile + a.batch;
-      for (int64_t y = 0; y < wide; y += kMaxGridYZ) {
-        AttendArgs w = a;
-        w.wide_first = y;
-        hipLaunchKernelGGL((k_attend_wide<kD>), dim3((unsigned)a.heads, (unsigned)(wide - y < kMaxGridYZ ? wide - y : kMaxGridYZ)),
-                           dim3(kThreads), 0, st, w);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-      }
-      max_rows = kMaxPartRows;
+    if (p.wide) {
+      const hipError_t e = run_wide<kD>(a, p, st);
+      if (e != hipSuccess) return e;
     }
   }
-  const int64_t tiles = (max_rows + kTile - 1) / kTile;
-  const dim3 grid((unsigned)(a.part_o ? most_items(a.batch, a.heads) : a.batch), (unsigned)a.heads,
-                  (unsigned)(tiles < 64 ? tiles : 64));
-  hipLaunchKernelGGL((k_attend_rows<kD, kF32>), grid, dim3(kThreads), 0, st, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.part_o) return e;
-  hipLaunchKernelGGL((k_attend_join<kD, kF32>), dim3((unsigned)a.batch, (unsigned)a.heads), dim3(kThreads), 0,
-                     st, a);
+  const int64_t tiles = p.wide ? 1 : (max_rows + kTile - 1) / kTile;
+  hipLaunchKernelGGL((k_attend_rows<kD, kF32>),
+                     dim3((unsigned)(p.items ? p.items : a.batch), (unsigned)a.heads, (unsigned)(tiles < 64 ? tiles : 64)),
+                     dim3(kThreads), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (!p.items && p.wide_splits == 1)) return e;
+  constexpr int64_t kJoinRows = kThreads / (kD / 4);
+  const int nz = p.part_rows < 16 ? p.part_rows : (int)std::min<int64_t>(max_rows, 16);
+  const int64_t row_groups = p.items ? a.batch * a.heads * nz : 0;
+  const int64_t wide_groups =
+      p.wide_splits > 1 ? (a.q_rows * a.heads * a.group + kJoinRows - 1) / kJoinRows : 0;
+  hipLaunchKernelGGL((k_attend_join<kD, kF32>), dim3((unsigned)(row_groups + wide_groups)), dim3(kThreads), 0, st, a,
+                     row_groups, nz);
   return hipGetLastError();
 }
 
 template <bool kF32>
-hipError_t run_d(const AttendArgs& a, int head_dim, int64_t max_rows, hipStream_t st) {
+hipError_t run_d(const AttendArgs& a, const Plan& p, int head_dim, int64_t max_rows, hipStream_t st) {
   switch (head_dim) {
-    case 64: return run<64, kF32>(a, max_rows, st);
-    case 128: return run<128, kF32>(a, max_rows, st);
-    case 192: return run<192, kF32>(a, max_rows, st);
-    default: return run<256, kF32>(a, max_rows, st);
+    case 64: return run<64, kF32>(a, p, max_rows, st);
+    case 128: return run<128, kF32>(a, p, max_rows, st);
+    case 192: return run<192, kF32>(a, p, max_rows, st);
+    default: return run<256, kF32>(a, p, max_rows, st);
   }
 }
 
 }  // namespace
 
-size_t attend_workspace_bytes(int64_t batch, int64_t heads, int64_t max_rows, int64_t width, int shift,
-                              int head_dim) {
-  if (!may_split(width, shift) || batch == 0 || max_rows == 0) return 0;
-  return (size_t)most_items(batch, heads) * heads * part_rows_of(max_rows) * (head_dim + 2) * 4;
+size_t attend_workspace_bytes(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_t max_rows,
+                              int64_t width, int shift, int head_dim, bool bf16) {
+  if (batch == 0 || q_rows == 0) return 0;
+  return plan_of(q_rows, batch, heads, group, max_rows, width, shift, head_dim, bf16).bytes;
 }
 
 hipError_t launch_attend(AttendArgs a, bool bf16, int head_dim, int64_t max_rows, void* workspace,
                          hipStream_t st) {
-  a.part_rows = part_rows_of(max_rows);
-  a.wide = bf16 && max_rows > kMaxPartRows;
-  a.wide_first = 0;
+  const Plan p = plan_of(a.q_rows, a.batch, a.heads, a.group, max_rows, a.width, a.shift, head_dim, bf16);
+  float* ws = (float*)workspace;
+  a.part_rows = p.part_rows;
+  a.part_o = ws;
+  a.part_ml = ws + p.part_ml;
+  a.wide = p.wide;
+  a.wide_splits = p.wide_splits;
+  a.wide_o = ws + p.wide_o;
+  a.wide_ml = ws + p.wide_ml;
   // scale 0 (all tokens alike) as a scale too small to matter, so that a masked
   // -inf stays -inf through the product
   if (a.c < 1e-37f) a.c = 1e-37f;
-  a.part_o = a.part_ml = nullptr;
-  if (may_split(a.width, a.shift)) {
-    a.part_o = (float*)workspace;
-    a.part_ml = a.part_o + (size_t)most_items(a.batch, a.heads) * a.heads * a.part_rows * head_dim;
-  }
-  return bf16 ? run_d<false>(a, head_dim, max_rows, st) : run_d<true>(a, head_dim, max_rows, st);
+  return bf16 ? run_d<false>(a, p, head_dim, max_rows, st) : run_d<true>(a, p, head_dim, max_rows, st);
 }
 
 }  // namespace pqb

@@ -226,15 +226,17 @@ struct AttendArgs {
   int causal;
   float c;                                    // softmax scale times log2(e)
   void* out;                                  // [q_rows, heads * group, D]
-  float *part_o, *part_ml;                    // workspace of split rows
-  // set by the launcher, as the two above
+  // set by the launcher: the workspace's parts and how the call is laid out
+  float *part_o, *part_ml;                    // the row kernel's items: [items, heads, part_rows]
+  float *wide_o, *wide_ml;                    // the wide kernel's splits: [splits, q_rows, query heads]
   int32_t part_rows;                          // rows of a request that may be split
   int32_t wide;                               // requests of more rows go to the wide kernel
+  int32_t wide_splits;
   int64_t wide_first;
 };
 // The workspace for at most max_rows = max_q_len * group rows per request.
-size_t attend_workspace_bytes(int64_t batch, int64_t heads, int64_t max_rows, int64_t width,
-                              int shift, int head_dim);
+size_t attend_workspace_bytes(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_t max_rows,
+                              int64_t width, int shift, int head_dim, bool bf16);
 hipError_t launch_attend(AttendArgs a, bool bf16, int head_dim, int64_t max_rows, void* workspace,
                          hipStream_t st);
 

@@ -150,10 +150,14 @@ def test_null_cache_is_refused():
 
 def test_workspaces():
     L = pqb.lib()
-    ws = L.pqb_kv_attend_workspace_bytes
-    assert ws(64, 32, 8, 128, 64, 4, 64, 1) == 0 < ws(64, 32, 8, 128, 64, 5, 64, 1)   # 256 tokens: one item
-    assert ws(64, 32, 8, 128, 64, 500, 64, 1) < ws(64, 32, 8, 128, 64, 500, 64, 0)
-    assert ws(64, 32, 7, 128, 64, 500, 64, 0) == ws(0, 32, 8, 128, 64, 500, 64, 0) == 0
+
+    def ws(**kw):
+        d = dict(dtype=1, rows=64, q_heads=32, heads=8, dim=128, batch=64, width=500, page=64, hint=1) | kw
+        return L.pqb_kv_attend_workspace_bytes(*d.values())
+
+    assert ws(width=8) == 0 < ws(width=9)                  # 512 tokens: one item each
+    assert ws() <= ws(hint=0) and ws(dtype=0) <= ws(dtype=0, hint=0)
+    assert ws(heads=7) == ws(rows=0) == ws(batch=0) == ws(dtype=2) == ws(page=8) == ws(batch=1 << 20) == 0
     assert L.pqb_kv_plan_workspace_bytes(2048, 4096) == 0 and L.pqb_kv_plan_workspace_bytes(7, 4097) == 28
 
 

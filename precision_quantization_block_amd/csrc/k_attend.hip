@@ -76,11 +76,21 @@ __device__ __forceinline__ int64_t wave_sum64(int64_t v) {
   return v;
 }
 
-__device__ __forceinline__ int split_units(const AttendArgs& a) {
-  const int lane = threadIdx.x & (kWave - 1);
+// Request b0 + lane (none behind the last), and the one that lane `src` holds.
+__device__ __forceinline__ Request lane_request(const AttendArgs& a, int64_t b0) {
+  const int64_t b = b0 + (threadIdx.x & (kWave - 1));
+  return b < a.batch ? request(a, b) : Request{0, 0, 0};
+}
+__device__ __forceinline__ Request from_lane(const Request& r, int src) {
+  return Request{__builtin_amdgcn_readlane(r.start, src), __builtin_amdgcn_readlane(r.n, src),
+                 __builtin_amdgcn_readlane(r.kv, src)};
+}
+
+// The units of an item.  `first`: requests 0 .. 63, one a lane.
+__device__ __forceinline__ int split_units(const AttendArgs& a, const Request& first) {
   int64_t total = 0;
-  for (int64_t b = lane; b < a.batch; b += kWave) {
-    const Request r = request(a, b);
+  for (int64_t b0 = 0; b0 < a.batch; b0 += kWave) {
+    const Request r = b0 ? lane_request(a, b0) : first;
     const int64_t rows = (int64_t)r.n * a.group;
     if (rows > 0 && rows <= a.part_rows) total += units_of(r.kv);
   }
@@ -92,16 +102,18 @@ __device__ __forceinline__ int split_units(const AttendArgs& a) {
 struct Item {
   int64_t b, first;      // request, and its first item
   int32_t index, count;  // this item among the request's
+  Request rq;
 };
 
 // Item x (or, by_request, the items of request x); b = -1 if there is none.
 template <bool kByRequest>
-__device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t x, int C) {
+__device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t x, int C, const Request& first) {
   const int lane = threadIdx.x & (kWave - 1);
   int64_t base = 0;
   for (int64_t b0 = 0; b0 < a.batch; b0 += kWave) {
     const int64_t b = b0 + lane;
-    const int mine = b < a.batch ? items_of(a, request(a, b), C) : 0;
+    const Request r = b0 ? lane_request(a, b0) : first;
+    const int mine = items_of(a, r, C);
     int incl = mine;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
@@ -112,17 +124,18 @@ __device__ __forceinline__ Item find_item(const AttendArgs& a, int64_t x, int C)
     const uint64_t m = __ballot(hit);
     if (m) {
       const int src = __builtin_ctzll(m);
-      const int cnt = __shfl(mine, src), upto = __shfl(incl, src);
+      const int cnt = __builtin_amdgcn_readlane(mine, src), upto = __builtin_amdgcn_readlane(incl, src);
       Item it;
       it.b = b0 + src;
       it.first = base + upto - cnt;
       it.index = kByRequest ? 0 : (int32_t)(x - it.first);
       it.count = cnt;
+      it.rq = from_lane(r, src);
       return it;
     }
-    base += __shfl(incl, kWave - 1);
+    base += __builtin_amdgcn_readlane(incl, kWave - 1);
   }
-  return Item{-1, 0, 0, 0};
+  return Item{-1, 0, 0, 0, Request{0, 0, 0}};
 }
 
 // ---------------------------------------------------------------------------
@@ -210,10 +223,11 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
   const int col = lane & 15, g4 = lane >> 4;
   const int h = blockIdx.y;
 
-  const int C = split_units(a);
-  const Item it = find_item<false>(a, blockIdx.x, C);
+  const Request first = lane_request(a, 0);
+  const int C = split_units(a, first);
+  const Item it = find_item<false>(a, blockIdx.x, C, first);
   if (it.b < 0) return;
-  const Request rq = request(a, it.b);
+  const Request rq = it.rq;
   const int32_t rows = rq.n * a.group;
   const int all_units = units_of(rq.kv);
   const int unit0 = it.count == 1 ? 0 : it.index * C;
@@ -480,20 +494,22 @@ __device__ __forceinline__ int key_swizzle(int token) {
 struct WideTile {
   int64_t b;
   int tile;
+  Request rq;
 };
 __device__ __forceinline__ WideTile find_wide(const AttendArgs& a, int64_t y) {
-  int64_t lo = 0, hi = a.batch;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if ((int64_t)max(a.starts[mid], 0) * a.group / kWideTile + mid <= y)
-      lo = mid;
-    else
-      hi = mid;
+  for (int64_t b0 = 0; b0 < a.batch; b0 += kWave) {
+    const int64_t b = b0 + (threadIdx.x & (kWave - 1));
+    const Request r = lane_request(a, b0);
+    const int64_t tiles = ((int64_t)r.n * a.group + kWideTile - 1) / kWideTile;
+    const int64_t i = y - ((int64_t)r.start * a.group / kWideTile + b);
+    const uint64_t m = __ballot((int64_t)r.n * a.group > a.part_rows && i >= 0 && i < tiles);
+    if (m) {
+      const int src = __builtin_ctzll(m);
+      // the last tile sees the most tokens: first
+      return WideTile{b0 + src, __builtin_amdgcn_readlane((int)(tiles - 1 - i), src), from_lane(r, src)};
+    }
   }
-  const int64_t i = y - ((int64_t)max(a.starts[lo], 0) * a.group / kWideTile + lo);
-  const int64_t rows = (int64_t)request(a, lo).n * a.group, tiles = (rows + kWideTile - 1) / kWideTile;
-  if (rows <= a.part_rows || i < 0 || i >= tiles) return WideTile{-1, 0};
-  return WideTile{lo, (int)(tiles - 1 - i)};  // the last tile sees the most tokens: first
+  return WideTile{-1, 0, Request{0, 0, 0}};
 }
 
 // A tile whose rows see `end` tokens at most is cut into `count` splits of `per`
@@ -523,7 +539,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   const int h = blockIdx.x;
   const WideTile wt = find_wide(a, a.wide_first + blockIdx.y);
   if (wt.b < 0) return;
-  const Request rq = request(a, wt.b);
+  const Request rq = wt.rq;
   const int rows = rq.n * a.group, row0 = wt.tile * kWideTile + wave * kWideRows, row = row0 + n;
   const bool valid = row < rows;
   const int tok = row / a.group;
@@ -848,9 +864,10 @@ __device__ __forceinline__ void join_items(const AttendArgs& a, int64_t b, int h
   constexpr int kQuads = kD / 4, kGroups = kThreads / kQuads;
   __shared__ float red_m[kWaves], red_l[kGroups];
   __shared__ f32x4 red_o[kGroups][kQuads];
-  const Item it = find_item<true>(a, b, split_units(a));
+  const Request first = lane_request(a, 0);
+  const Item it = find_item<true>(a, b, split_units(a, first), first);
   if (it.count < 2) return;
-  const Request rq = request(a, b);
+  const Request rq = it.rq;
   const int rows = rq.n * a.group, tid = threadIdx.x, lane = tid & (kWave - 1);
   const int quad = tid % kQuads, grp = tid / kQuads;   // every kGroups-th item; the sums meet in LDS
   const int64_t step = (int64_t)a.heads * a.part_rows;

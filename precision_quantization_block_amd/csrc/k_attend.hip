@@ -449,6 +449,8 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 // 2^-25 of the reference.
 // ---------------------------------------------------------------------------
 
+constexpr int kStages = 4;        // units in LDS at a time
+constexpr int kMetaUnits = 64;    // units whose pages are looked up at a time
 constexpr int kWideRows = 32, kWideTile = kWaves * kWideRows;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -467,6 +469,11 @@ __device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
 __device__ __forceinline__ void dma16s(const void* g, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(g), "s"(lds)
                : "memory");
+}
+
+template <int kN>
+__device__ __forceinline__ void wait_vmcnt() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kN) : "memory");
 }
 
 __device__ __forceinline__ float swap_max(float x) {
@@ -530,9 +537,10 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   constexpr int kKS = kD / 64;    // 64-deep steps of S^T; also the DMA steps of a wave and tensor
   constexpr int kDT = kD / 32;    // 32-channel tiles of O^T
   constexpr int kKeyChunks = kD / 16;
-  __shared__ __align__(16) uint8_t kbuf[2][kUnit * kD], vbuf[2][kUnit * kD];
-  // scale bytes of the staged units' 16-token groups (one page a unit: the first); xv -1: no page
-  __shared__ int xk[2][4], xv[2][4];
+  constexpr int kGroups = kWholePages ? 1 : 4;   // pages that a unit may lie in
+  __shared__ __align__(16) uint8_t kbuf[kStages][kUnit * kD], vbuf[kStages][kUnit * kD];
+  // page and scales of the units ahead: pg -1 if there is none, xs K's byte and V's << 8
+  __shared__ int pg[2 * kMetaUnits * kGroups], xs[2 * kMetaUnits * kGroups];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n = lane & 31, half = lane >> 5;
@@ -557,71 +565,81 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   const int64_t page_bytes = (int64_t)kD << a.shift;
   const int ps1 = (1 << a.shift) - 1;
 
-  // Staging.  A wave's DMA takes the keys of 16-token group `wave` and a quarter of
-  // V's channels; this lane's V bytes are of group vg.  Keys are staged a unit
-  // ahead of V: S^T of unit u + 1 is formed under the softmax of unit u.  Where a
-  // unit lies in one page, the page is uniform and only offsets are per lane.
+  // What the units lie in: kMetaUnits units' pages and scales at a time.
+  auto meta_at = [&](int u, int group) { return (u & (2 * kMetaUnits - 1)) * kGroups + (kWholePages ? 0 : group); };
+  auto load_meta = [&](int first) {
+    for (int i = tid; i < kMetaUnits * kGroups; i += kThreads) {
+      const int u = first + i / kGroups, t = u * kUnit + 16 * (i % kGroups);
+      int p = u < units && t < rq.kv ? table[t >> a.shift] : -1, x = 0x0101;
+      if ((uint32_t)p < (uint64_t)a.pages) {
+        const int64_t at = (int64_t)p * a.heads + h;
+        x = min(max((int)a.k_scales[at], 1), 254) | min(max((int)a.v_scales[at], 1), 254) << 8;
+      } else {
+        p = -1;
+      }
+      pg[meta_at(u, i % kGroups)] = p;
+      xs[meta_at(u, i % kGroups)] = x;
+    }
+  };
+
+  // Staging, kStages - 1 units ahead of V's use and one more for keys: S^T of unit
+  // u + 1 is formed under the softmax of unit u.  A wave's DMA takes the keys of
+  // 16-token group `wave` and a quarter of V's channels; this lane's V bytes are
+  // of group vg.  A key group lies in one page, so its address is uniform.
   const int vg = (lane & 3) ^ ((lane >> 3) & 3);
   uint32_t koff[kKS], voff[kKS];
 #pragma unroll
   for (int i = 0; i < kKS; ++i) {
     const int j = i * kWave + lane, token = 16 * wave + j / kKeyChunks;
     const int chunk = (j % kKeyChunks) ^ key_swizzle<kD>(token), d = (wave * kKS + i) * 16 + (lane >> 2);
-    koff[i] = (uint32_t)((kWholePages ? token : token & 15) * kD + chunk * 16);
+    koff[i] = (uint32_t)((token & 15) * kD + chunk * 16);
     voff[i] = (uint32_t)((d << a.shift) + (kWholePages ? 16 * vg : 0));
   }
-  auto page_at = [&](int u, int group) {   // the page of a 16-token group (of the whole unit), or -1
-    const int t = u * kUnit + (kWholePages ? 0 : 16 * group);
-    int p = t < rq.kv ? table[t >> a.shift] : -1;
-    if constexpr (kWholePages) p = __builtin_amdgcn_readfirstlane(p);
-    return (uint32_t)p < (uint64_t)a.pages ? p : -1;
-  };
-  auto stage_k = [&](int u, int pk) {
-    const uint8_t* kp = a.k_codes + ((int64_t)max(pk, 0) * a.heads + h) * page_bytes +
-                        (int64_t)((u * kUnit + (kWholePages ? 0 : 16 * wave)) & ps1) * kD;
+  auto stage_k = [&](int u) {
+    const int p = __builtin_amdgcn_readfirstlane(pg[meta_at(u, wave)]);
+    const uint8_t* kp = a.k_codes + ((int64_t)max(p, 0) * a.heads + h) * page_bytes +
+                        (int64_t)((u * kUnit + 16 * wave) & ps1) * kD;
 #pragma unroll
-    for (int i = 0; i < kKS; ++i) {
-      const uint32_t to = lds_addr(&kbuf[u & 1][16 * wave * kD + i * 1024]);
-      if constexpr (kWholePages)
-        dma16s(kp, koff[i], to);
-      else
-        dma16(kp + koff[i], to);
-    }
+    for (int i = 0; i < kKS; ++i) dma16s(kp, koff[i], lds_addr(&kbuf[u % kStages][16 * wave * kD + i * 1024]));
   };
-  auto stage_v = [&](int u, int pv) {
-    const uint8_t* vp = a.v_codes + ((int64_t)max(pv, 0) * a.heads + h) * page_bytes +
+  auto stage_v = [&](int u) {
+    int p = pg[meta_at(u, vg)];
+    if constexpr (kWholePages) p = __builtin_amdgcn_readfirstlane(p);
+    const uint8_t* vp = a.v_codes + ((int64_t)max(p, 0) * a.heads + h) * page_bytes +
                         ((u * kUnit + (kWholePages ? 0 : 16 * vg)) & ps1);
 #pragma unroll
     for (int i = 0; i < kKS; ++i) {
-      const uint32_t to = lds_addr(&vbuf[u & 1][(wave * kKS + i) * 1024]);
+      const uint32_t to = lds_addr(&vbuf[u % kStages][(wave * kKS + i) * 1024]);
       if constexpr (kWholePages)
         dma16s(vp, voff[i], to);
       else
         dma16(vp + voff[i], to);
     }
   };
-  // Threads 0-3 carry the scale bytes of their group of a staged unit into LDS.
-  int sk_next = 0, sv_next = 0;
-  bool hole_next = false;
-  auto scale_at = [&](const uint8_t* x, int px) { return (int)x[(int64_t)max(px, 0) * a.heads + h]; };
-  const int mine = kWholePages ? 0 : tid & 3;
-
-  int pk = -1, pv = -1, px = -1, px1 = -1;   // pages of unit u + 2 (keys, scales) and u + 1 (V, scales)
+  // Waits until at most `steps` of this wave's newest staging steps (keys of a
+  // unit and V of the one before: 2 kKS loads) are in flight.
+  auto wait_steps = [&](int steps) {
+    static_assert(kStages == 4, "one wait for each number of steps");
+    if (steps >= 3)
+      wait_vmcnt<6 * kKS>();
+    else if (steps == 2)
+      wait_vmcnt<4 * kKS>();
+    else if (steps == 1)
+      wait_vmcnt<2 * kKS>();
+    else
+      wait_vmcnt<0>();
+  };
+  load_meta(u0);
+  __syncthreads();
+  wait_vmcnt<0>();
   if (u0 < units) {
-    pk = page_at(u0, wave), px = page_at(u0, mine);
-    stage_k(u0, pk);
-    stage_v(u0, page_at(u0, vg));
-    if (tid < 4) {
-      xk[u0 & 1][tid] = min(max(scale_at(a.k_scales, px), 1), 254);
-      sv_next = scale_at(a.v_scales, px);
-      hole_next = px < 0;
-    }
-    if (u0 + 1 < units) {
-      stage_k(u0 + 1, page_at(u0 + 1, wave));
-      pv = page_at(u0 + 1, vg), px1 = page_at(u0 + 1, mine);
-      if (tid < 4) sk_next = scale_at(a.k_scales, px1);
-    }
-    if (u0 + 2 < units) pk = page_at(u0 + 2, wave), px = page_at(u0 + 2, mine);
+    stage_k(u0);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+      if (u0 + i < units) {
+        stage_v(u0 + i);
+        stage_k(u0 + i + 1);   // behind the last unit: page 0's bytes, unused
+      }
   }
 
   // q as 2^e (hi + lo / 16)
@@ -680,14 +698,14 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int token = 32 * ((n >> 2) & 1) + 16 * t + 4 * (n >> 3) + (n & 3), key = key_swizzle<kD>(token);
-      const int sk = xk[u & 1][kWholePages ? 0 : 2 * ((n >> 2) & 1) + t];
+      const int sk = xs[meta_at(u, 2 * ((n >> 2) & 1) + t)] & 0xFF;
 #pragma unroll
       for (int j = 0; j < 16; ++j) to[t][j] = 0;
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         const int ch = ks * 4 + half * 2;
-        const uint4 lo = *reinterpret_cast<const uint4*>(&kbuf[u & 1][token * kD + ((ch ^ key) << 4)]);
-        const uint4 hi = *reinterpret_cast<const uint4*>(&kbuf[u & 1][token * kD + (((ch + 1) ^ key) << 4)]);
+        const uint4 lo = *reinterpret_cast<const uint4*>(&kbuf[u % kStages][token * kD + ((ch ^ key) << 4)]);
+        const uint4 hi = *reinterpret_cast<const uint4*>(&kbuf[u % kStages][token * kD + (((ch + 1) ^ key) << 4)]);
         const v8i kf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
         to[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, ql[ks], to[t], 0, 0, 0, sk, 0, el);
         to[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qh[ks], to[t], 0, 0, 0, sk, 0, eh);
@@ -712,42 +730,30 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
 
   // One unit: s holds its S^T, next receives the following unit's.
   auto unit = [&](int u, f32x16* s, f32x16* next) {
-    const int buf = u & 1;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's DMA: keys of u + 1, V of u
-    if (tid < 4) {
-      xk[buf ^ 1][tid] = min(max(sk_next, 1), 254);
-      xv[buf][tid] = hole_next ? -1 : min(max(sv_next, 1), 254);
-    }
+    const int buf = u % kStages;
+    wait_steps(min(kStages - 2, units - 1 - u));  // this wave's DMA: keys of u + 1, V of u
     __syncthreads();
-    if (u + 1 < units) {
-      stage_v(u + 1, pv);
-      if (tid < 4) {
-        sv_next = scale_at(a.v_scales, px1);
-        hole_next = px1 < 0;
+    if (u + kStages - 1 < units) {
+      if (((u + kStages - u0) & (kMetaUnits - 1)) == 0) {
+        load_meta(u + kStages);
+        __syncthreads();
       }
-      if (u + 2 < units) {
-        stage_k(u + 2, pk);
-        px1 = kWholePages ? pk : px;
-        if (tid < 4) sk_next = scale_at(a.k_scales, px1);
-        pv = kWholePages ? pk : page_at(u + 2, vg);
-        if (u + 3 < units) {
-          pk = page_at(u + 3, wave);
-          if (!kWholePages) px = page_at(u + 3, mine);
-        }
-      }
+      stage_v(u + kStages - 1);
+      stage_k(u + kStages);
     }
     int xr, lo;   // the unit's largest V exponent; negative lo: some page is none
     if constexpr (kWholePages) {
-      xr = lo = __builtin_amdgcn_readfirstlane(xv[buf][0]);
+      xr = __builtin_amdgcn_readfirstlane(xs[meta_at(u, 0)]) >> 8;
+      lo = __builtin_amdgcn_readfirstlane(pg[meta_at(u, 0)]);
     } else {
-      const int x0 = xv[buf][0], x1 = xv[buf][1], x2 = xv[buf][2], x3 = xv[buf][3];
-      xr = max(max(x0, x1), max(x2, x3)), lo = min(min(x0, x1), min(x2, x3));
+      xr = max(max(xs[meta_at(u, 0)], xs[meta_at(u, 1)]), max(xs[meta_at(u, 2)], xs[meta_at(u, 3)])) >> 8;
+      lo = min(min(pg[meta_at(u, 0)], pg[meta_at(u, 1)]), min(pg[meta_at(u, 2)], pg[meta_at(u, 3)]));
     }
     if (lo < 0 || (u + 1) * kUnit > rq.kv) {
       // codes behind the last token, or of no page, may be anything: V's become 0
       for (int i = tid; i < 4 * kD; i += kThreads) {
         const int d = i >> 2, g = (i & 3) ^ ((d >> 1) & 3);
-        const int held = xv[buf][kWholePages ? 0 : g] < 0 ? 0 : min(max(rq.kv - (u * kUnit + 16 * g), 0), 16);
+        const int held = pg[meta_at(u, g)] < 0 ? 0 : min(max(rq.kv - (u * kUnit + 16 * g), 0), 16);
         uint32_t* p = reinterpret_cast<uint32_t*>(&vbuf[buf][i * 16]);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -762,7 +768,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
     if (lo < 0 || (u + 1) * kUnit > first_limit) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int g = 2 * half + t, cnt = xv[buf][kWholePages ? 0 : g] < 0 ? 0 : limit - (u * kUnit + 16 * g);
+        const int g = 2 * half + t, cnt = pg[meta_at(u, g)] < 0 ? 0 : limit - (u * kUnit + 16 * g);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (j >= cnt) s[t][j] = -INFINITY;
@@ -800,7 +806,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
     l += sum;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int x = kWholePages ? xr : xv[buf][2 * half + t];
+      const int x = kWholePages ? xr : xs[meta_at(u, 2 * half + t)] >> 8;
       const float sv = as_f((uint32_t)(127 - min(max(R - x, 0), 60)) << 23);
       const f16x8 p0 = __builtin_bit_cast(f16x8, make_uint4(pw[t][0], pw[t][1], pw[t][2], pw[t][3]));
       const f16x8 p1 = __builtin_bit_cast(f16x8, make_uint4(pw[t][4], pw[t][5], pw[t][6], pw[t][7]));
@@ -816,7 +822,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
 
   f32x16 sa[2], sb[2];
   if (u0 < units) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    wait_steps(min(kStages - 1, units - u0));
     __syncthreads();
     scores(u0, sa);
   }

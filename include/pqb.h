@@ -410,7 +410,7 @@ pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, in
  * decides workspace and launch shapes; results hold whatever it is.
  * Numbers: float32 sums, maxima and outputs before one rounding to `dtype`;
  * q . k exact products (float32 q in three bf16 parts); p rounded to 11 bits
- * relative to its value down to 2^-29 of the largest (22 bits for float32 q).
+ * relative to its value down to 2^-23 of the largest (22 bits for float32 q).
  * Shape rules: q_heads a multiple of heads; q_rows * q_heads and
  * table_width * page_size < 2^31 - 256; batch < 2^23 / heads; q_stride in [q_heads * head_dim,
  * 2^40).  scale: finite and >= 0 (else PQB_ERR_VALUE).  Workspace:

@@ -107,7 +107,7 @@ def attend(q, k_codes, v_codes, k_scales, v_scales, table, starts, kv_lens, caus
         a bf16 q may be taken as two E4M3 parts, each value within 2^-23 of the
         row's largest |q|, so 2^-22 max |q| sum |k| scale more;
       p rounded to f16, 2^-11 of itself (float32: remainder kept, 2^-22), and
-        2^-36 of the largest below 2^-25; V to 2^-25 of its request's largest
+        2^-34 of the largest below 2^-23; V to 2^-25 of its request's largest
         scale;
       sums over n tokens and at most n / 64 joins and rescalings: (2 n + 64) 2^-24 A;
       the output's rounding, 2^-8 (bf16) or 2^-24 of it."""
@@ -152,7 +152,7 @@ def attend(q, k_codes, v_codes, k_scales, v_scales, table, starts, kv_lens, caus
                 A = p @ np.abs(v) / safe
                 e = (p * ds) @ np.abs(v) / safe + A * (p * ds).sum(1, keepdims=True) / safe
                 e += A * ((2.0 ** -22 if f32 else 2.0 ** -11) + (2 * kv + 64) * u)
-                e += 2.0 ** -36 * np.abs(v).sum(0) / safe + 2.0 ** -25 * top
+                e += 2.0 ** -34 * np.abs(v).sum(0) / safe + 2.0 ** -25 * top
                 out[rows, g] = o
                 bound[rows, g] = np.where(total == 0, 0, e + (u if f32 else 2.0 ** -8) * (np.abs(o) + e))
     return out, bound

@@ -443,12 +443,14 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 //
 // Key row m = 8 a + 4 h + b of tile t stands for token 32 h + 16 t + 4 a + b: a
 // lane (column n, half h) then holds 32 consecutive tokens of its query row.
-// The maximum is followed loosely: p is held as 2^11 p' in f16 relative to a
-// reference that moves (and O and l with it) only when a lane's sum of p over a
-// unit passes 2^15, so a p' is at most 2^4 and 11 significant bits reach down to
-// 2^-25 of the reference.
+// The maximum is followed loosely: p is held as 2^9 p' in f16 relative to a
+// reference that moves to the maximum (and O and l with it) only when a lane's
+// sum of its 32 p of a unit passes 65000, so that no p passes f16's 65504.  Just
+// after a move that sum is 2^14 at most, however flat the row, so a move is rare;
+// 11 significant bits reach down to 2^-23 of the reference.
 // ---------------------------------------------------------------------------
 
+constexpr float kPExp = 9.0f;      // p is held times 2^9
 constexpr int kStages = 4;        // units in LDS at a time
 constexpr int kMetaUnits = 64;    // units whose pages are looked up at a time
 constexpr int kWideRows = 32, kWideTile = kWaves * kWideRows;
@@ -684,8 +686,8 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   const int el = eh - 4;
 
   const float c = a.c;
-  // m: the row's reference (the maximum when it was last moved), r = 11 - m c; O
-  // and l hold 2^11 p' relative to it.  r starts infinite: the first unit moves it.
+  // m: the row's reference (the maximum when it was last moved), r = 9 - m c; O
+  // and l hold 2^9 p' relative to it.  r starts infinite: the first unit moves it.
   float m = -INFINITY, r = INFINITY, l = 0;
   int R = 1;
   f32x16 o[kDT];
@@ -779,9 +781,9 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
     scores(u + 1, next);
     uint32_t pw[2][8];
     float sum = weights(s, r, pw);
-    // No maximum is taken while P fits: a p of 2^15 or more, or the first unit's
+    // No maximum is taken while P fits f16: what does not, or the first unit's
     // infinite r, shows in the sum.
-    if (__ballot(!(sum <= 0x1p15f)) || xr > R) {
+    if (__ballot(!(sum <= 65000.0f)) || xr > R) {
       float mx = s[0][0];
 #pragma unroll
       for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[0][j]);
@@ -789,7 +791,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
       for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[1][j]);
       const float m_new = fmaxf(m, swap_max(mx));
       const bool none = m_new == -INFINITY;
-      const float r_new = none ? 11.0f : __builtin_fmaf(-m_new, c, 11.0f);
+      const float r_new = none ? kPExp : __builtin_fmaf(-m_new, c, kPExp);
       const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(r_new - r);
       const int R_new = max(R, xr);
       const float f = R_new - R > 126 ? 0.0f : alpha * as_f((uint32_t)(127 - (R_new - R)) << 23);
@@ -846,7 +848,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
       }
   } else {
     const int64_t slot = (int64_t)split * a.q_rows * a.heads * a.group + out_row;
-    const float scale = as_f((uint32_t)R << 23) * 0x1p-11f;
+    const float scale = as_f((uint32_t)R << 23) * 0x1p-9f;
 #pragma unroll
     for (int i = 0; i < kDT; ++i)
 #pragma unroll
@@ -857,7 +859,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
       }
     if (half == 0) {
       a.wide_ml[2 * slot] = m;
-      a.wide_ml[2 * slot + 1] = l * 0x1p-11f;
+      a.wide_ml[2 * slot + 1] = l * 0x1p-9f;
     }
   }
 }

@@ -411,9 +411,9 @@ pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, in
  * Numbers: float32 sums, maxima and outputs before one rounding to `dtype`;
  * q . k exact products (float32 q in three bf16 parts); p rounded to 11 bits
  * relative to its value down to 2^-23 of the largest (22 bits for float32 q).
- * Shape rules: q_heads a multiple of heads; q_rows * q_heads and
- * table_width * page_size < 2^31 - 256; batch < 2^23 / heads; q_stride in [q_heads * head_dim,
- * 2^40).  scale: finite and >= 0 (else PQB_ERR_VALUE).  Workspace:
+ * Shape rules: q_heads a multiple of heads; q_rows * q_heads < 2^30;
+ * table_width * page_size < 2^31 - 256; batch * heads < 2^21; q_stride in
+ * [q_heads * head_dim, 2^40).  scale: finite and >= 0 (else PQB_ERR_VALUE).  Workspace:
  * pqb_kv_attend_workspace_bytes(), its contents on entry do not matter; calls
  * that overlap in time need one each.  Alignment: q, out and workspace 16 bytes,
  * q_stride a multiple of 16 bytes, the int arrays 4.  Errors, before any launch:

@@ -675,6 +675,9 @@ static bool head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 192 || d
 // to whole units of tokens inside them.
 constexpr int64_t kPagedMaxTokens = ((int64_t)1 << 31) - 256;
 constexpr int64_t kPagedMaxStride = (int64_t)1 << 40;
+// Query rows (token and head) of a call, and requests times KV heads below 2^21:
+// the attention grids stay within 2^32 - 1 threads.
+constexpr int64_t kAttendMaxRows = (int64_t)1 << 30;
 
 static pqb_status check_pages(const pqb_kv_pages* c, int* shift) {
   if (!c) return PQB_ERR_NULL;
@@ -750,8 +753,8 @@ static int64_t attend_max_rows(int64_t q_rows, int64_t group, int64_t max_q_len)
 static bool attend_dims_ok(int64_t q_rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t batch,
                            int64_t table_width, int shift) {
   return shift >= 0 && head_dim_ok(head_dim) && heads >= 1 && heads <= 4096 && q_heads >= 1 &&
-         q_heads % heads == 0 && q_heads < kPagedMaxTokens && q_rows >= 0 &&
-         q_rows < kPagedMaxTokens / q_heads && batch >= 0 && batch < (1 << 23) / heads && table_width >= 0 &&
+         q_heads % heads == 0 && q_heads < kAttendMaxRows && q_rows >= 0 && q_rows < kAttendMaxRows / q_heads &&
+         batch >= 0 && batch < (1 << 21) / heads && table_width >= 0 &&
          table_width < kPagedMaxTokens >> shift;
 }
 

@@ -36,8 +36,9 @@ constexpr int kMinUnits = 2 * kWaves;             // fewest units of a split
 constexpr int kMaxPartRows = 64;                  // rows of a float32 request that may be split
 constexpr int64_t kGroupsWanted = 1024;           // workgroups a split aims at
 constexpr int64_t kMaxGridYZ = 65535;
-constexpr int kMinWideUnits = 4;                  // the same for the wide kernel
-constexpr int64_t kMaxWideSplits = 32, kWideGroupsWanted = 1024;
+constexpr int64_t kMaxGroups = 1 << 23;            // workgroups of a join
+constexpr int kMinWideUnits = 8;                  // the same for the wide kernel
+constexpr int64_t kMaxWideSplits = 32, kWideGroupsWanted = 512;
 
 // ---------------------------------------------------------------------------
 // Work items.  Request b has u_b = ceil(kv_len / 64) units and is cut into
@@ -542,7 +543,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   constexpr int kGroups = kWholePages ? 1 : 4;   // pages that a unit may lie in
   __shared__ __align__(16) uint8_t kbuf[kStages][kUnit * kD], vbuf[kStages][kUnit * kD];
   // page and scales of the units ahead: pg -1 if there is none, xs K's byte and V's << 8
-  __shared__ int pg[2 * kMetaUnits * kGroups], xs[2 * kMetaUnits * kGroups];
+  __shared__ __align__(16) int pg[2 * kMetaUnits * kGroups], xs[2 * kMetaUnits * kGroups];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n = lane & 31, half = lane >> 5;
@@ -566,6 +567,18 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   const int32_t* table = a.table + wt.b * a.width;
   const int64_t page_bytes = (int64_t)kD << a.shift;
   const int ps1 = (1 << a.shift) - 1;
+
+  // q's loads go out first: they return under the page lookups and the first DMA
+  uint4 raw[kKS][4];
+  {
+    const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(rq.start + tok) * a.q_stride +
+                         (int64_t)(h * a.group + row % a.group) * kD + half * 32;
+#pragma unroll
+    for (int s = 0; s < kKS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        raw[s][i] = valid ? *reinterpret_cast<const uint4*>(qp + s * 64 + i * 8) : make_uint4(0, 0, 0, 0);
+  }
 
   // What the units lie in: kMetaUnits units' pages and scales at a time.
   auto meta_at = [&](int u, int group) { return (u & (2 * kMetaUnits - 1)) * kGroups + (kWholePages ? 0 : group); };
@@ -597,18 +610,22 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
     koff[i] = (uint32_t)((token & 15) * kD + chunk * 16);
     voff[i] = (uint32_t)((d << a.shift) + (kWholePages ? 16 * vg : 0));
   }
-  auto stage_k = [&](int u) {
-    const int p = __builtin_amdgcn_readfirstlane(pg[meta_at(u, wave)]);
-    const uint8_t* kp = a.k_codes + ((int64_t)max(p, 0) * a.heads + h) * page_bytes +
-                        (int64_t)((u * kUnit + 16 * wave) & ps1) * kD;
+  const uint8_t *k_head = a.k_codes + h * page_bytes, *v_head = a.v_codes + h * page_bytes;
+  const uint32_t page_step = (uint32_t)(a.heads * page_bytes);   // at most 4096 heads of 64 KiB
+  auto k_from = [&](int u) {
+    const uint32_t p = (uint32_t)max(__builtin_amdgcn_readfirstlane(pg[meta_at(u, wave)]), 0);
+    return k_head + (uint64_t)p * page_step + (uint32_t)(((u * kUnit + 16 * wave) & ps1) * kD);
+  };
+  auto v_from = [&](int u) {
+    int p = pg[meta_at(u, vg)];
+    if constexpr (kWholePages) p = __builtin_amdgcn_readfirstlane(p);
+    return v_head + (uint64_t)(uint32_t)max(p, 0) * page_step + ((u * kUnit + (kWholePages ? 0 : 16 * vg)) & ps1);
+  };
+  auto stage_k = [&](int u, const uint8_t* kp) {
 #pragma unroll
     for (int i = 0; i < kKS; ++i) dma16s(kp, koff[i], lds_addr(&kbuf[u % kStages][16 * wave * kD + i * 1024]));
   };
-  auto stage_v = [&](int u) {
-    int p = pg[meta_at(u, vg)];
-    if constexpr (kWholePages) p = __builtin_amdgcn_readfirstlane(p);
-    const uint8_t* vp = a.v_codes + ((int64_t)max(p, 0) * a.heads + h) * page_bytes +
-                        ((u * kUnit + (kWholePages ? 0 : 16 * vg)) & ps1);
+  auto stage_v = [&](int u, const uint8_t* vp) {
 #pragma unroll
     for (int i = 0; i < kKS; ++i) {
       const uint32_t to = lds_addr(&vbuf[u % kStages][(wave * kKS + i) * 1024]);
@@ -633,30 +650,27 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   };
   load_meta(u0);
   __syncthreads();
-  wait_vmcnt<0>();
+  const uint8_t *k_next = nullptr, *v_next = nullptr;   // where the next staging step reads
   if (u0 < units) {
-    stage_k(u0);
+    stage_k(u0, k_from(u0));
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i)
       if (u0 + i < units) {
-        stage_v(u0 + i);
-        stage_k(u0 + i + 1);   // behind the last unit: page 0's bytes, unused
+        stage_v(u0 + i, v_from(u0 + i));
+        stage_k(u0 + i + 1, k_from(u0 + i + 1));   // behind the last unit: page 0's bytes, unused
       }
+    k_next = k_from(u0 + kStages), v_next = v_from(u0 + kStages - 1);
   }
 
   // q as 2^e (hi + lo / 16)
   v8i qh[kKS], ql[kKS];
   int eh;
   {
-    uint4 raw[kKS][4];
-    const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(rq.start + tok) * a.q_stride +
-                         (int64_t)(h * a.group + row % a.group) * kD + half * 32;
     float mx = 0;
 #pragma unroll
     for (int s = 0; s < kKS; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        raw[s][i] = valid ? *reinterpret_cast<const uint4*>(qp + s * 64 + i * 8) : make_uint4(0, 0, 0, 0);
         const uint32_t* w = &raw[s][i].x;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -730,27 +744,38 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
     return sum;
   };
 
+  // The unit's largest V exponent, negative lo where some page is none, and the V
+  // exponents of this lane's two token groups.
+  int xr_next = 1, lo_next = 0, xv_next[2] = {1, 1};
+  auto scales_of = [&](int u) {
+    if constexpr (kWholePages) {
+      xr_next = __builtin_amdgcn_readfirstlane(xs[meta_at(u, 0)]) >> 8;
+      lo_next = __builtin_amdgcn_readfirstlane(pg[meta_at(u, 0)]);
+      xv_next[0] = xv_next[1] = xr_next;
+    } else {
+      const int4 x = *reinterpret_cast<const int4*>(&xs[meta_at(u, 0)]), p = *reinterpret_cast<const int4*>(&pg[meta_at(u, 0)]);
+      xr_next = max(max(x.x, x.y), max(x.z, x.w)) >> 8;
+      lo_next = min(min(p.x, p.y), min(p.z, p.w));
+      xv_next[0] = (half ? x.z : x.x) >> 8;
+      xv_next[1] = (half ? x.w : x.y) >> 8;
+    }
+  };
+
   // One unit: s holds its S^T, next receives the following unit's.
   auto unit = [&](int u, f32x16* s, f32x16* next) {
     const int buf = u % kStages;
     wait_steps(min(kStages - 2, units - 1 - u));  // this wave's DMA: keys of u + 1, V of u
     __syncthreads();
     if (u + kStages - 1 < units) {
-      if (((u + kStages - u0) & (kMetaUnits - 1)) == 0) {
-        load_meta(u + kStages);
+      stage_v(u + kStages - 1, v_next);
+      stage_k(u + kStages, k_next);
+      if (((u + kStages + 1 - u0) & (kMetaUnits - 1)) == 0) {
+        load_meta(u + kStages + 1);
         __syncthreads();
       }
-      stage_v(u + kStages - 1);
-      stage_k(u + kStages);
     }
-    int xr, lo;   // the unit's largest V exponent; negative lo: some page is none
-    if constexpr (kWholePages) {
-      xr = __builtin_amdgcn_readfirstlane(xs[meta_at(u, 0)]) >> 8;
-      lo = __builtin_amdgcn_readfirstlane(pg[meta_at(u, 0)]);
-    } else {
-      xr = max(max(xs[meta_at(u, 0)], xs[meta_at(u, 1)]), max(xs[meta_at(u, 2)], xs[meta_at(u, 3)])) >> 8;
-      lo = min(min(pg[meta_at(u, 0)], pg[meta_at(u, 1)]), min(pg[meta_at(u, 2)], pg[meta_at(u, 3)]));
-    }
+    const int xr = xr_next, lo = lo_next;
+    int xv[2] = {xv_next[0], xv_next[1]};
     if (lo < 0 || (u + 1) * kUnit > rq.kv) {
       // codes behind the last token, or of no page, may be anything: V's become 0
       for (int i = tid; i < 4 * kD; i += kThreads) {
@@ -765,6 +790,9 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
       }
       __syncthreads();
     }
+    // for the next unit, ahead of its barrier
+    scales_of(u + 1);
+    k_next = k_from(u + kStages + 1), v_next = v_from(u + kStages);
     if (u * kUnit >= wave_end) return;
 
     if (lo < 0 || (u + 1) * kUnit > first_limit) {
@@ -808,8 +836,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
     l += sum;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int x = kWholePages ? xr : xs[meta_at(u, 2 * half + t)] >> 8;
-      const float sv = as_f((uint32_t)(127 - min(max(R - x, 0), 60)) << 23);
+      const float sv = as_f((uint32_t)(127 - min(max(R - xv[t], 0), 60)) << 23);
       const f16x8 p0 = __builtin_bit_cast(f16x8, make_uint4(pw[t][0], pw[t][1], pw[t][2], pw[t][3]));
       const f16x8 p1 = __builtin_bit_cast(f16x8, make_uint4(pw[t][4], pw[t][5], pw[t][6], pw[t][7]));
 #pragma unroll
@@ -824,6 +851,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
 
   f32x16 sa[2], sb[2];
   if (u0 < units) {
+    scales_of(u0);
     wait_steps(min(kStages - 1, units - u0));
     __syncthreads();
     scores(u0, sa);
@@ -1034,7 +1062,7 @@ hipError_t run(const AttendArgs& a, const Plan& p, int64_t max_rows, hipStream_t
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!p.items && p.wide_splits == 1)) return e;
   constexpr int64_t kJoinRows = kThreads / (kD / 4);
-  const int nz = p.part_rows < 16 ? p.part_rows : (int)std::min<int64_t>(max_rows, 16);
+  const int nz = (int)std::max<int64_t>(1, std::min<int64_t>({max_rows, 16, kMaxGroups / (a.batch * a.heads)}));
   const int64_t row_groups = p.items ? a.batch * a.heads * nz : 0;
   const int64_t wide_groups =
       p.wide_splits > 1 ? (a.q_rows * a.heads * a.group + kJoinRows - 1) / kJoinRows : 0;

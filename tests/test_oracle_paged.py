@@ -127,8 +127,8 @@ def test_append_refuses(kw, cache, status):
 
 @pytest.mark.parametrize("kw,cache,status", [
     (dict(dtype=7), {}, -2), (dict(), dict(res=3), -2), (dict(), dict(page=0), -4), (dict(heads=3), {}, -4),
-    (dict(heads=0), {}, -4), (dict(rows=-1), {}, -4), (dict(rows=1 << 30), {}, -4), (dict(batch=-1), {}, -4),
-    (dict(batch=1 << 23), {}, -4), (dict(width=1 << 27), {}, -4), (dict(ld=255), {}, -4), (dict(ld=260), {}, -5),
+    (dict(heads=0), {}, -4), (dict(rows=-1), {}, -4), (dict(rows=1 << 28), {}, -4), (dict(batch=-1), {}, -4),
+    (dict(batch=1 << 20), {}, -4), (dict(width=1 << 27), {}, -4), (dict(ld=255), {}, -4), (dict(ld=260), {}, -5),
     (dict(scale=-1.0), {}, -9), (dict(scale=float("nan")), {}, -9), (dict(scale=float("inf")), {}, -9),
     (dict(q=None), {}, -1), (dict(out=None), {}, -1), (dict(table=None), {}, -1), (dict(starts=None), {}, -1),
     (dict(kv=None), {}, -1), (dict(q=ctypes.c_void_p(8)), {}, -5), (dict(out=ctypes.c_void_p(24)), {}, -5),

@@ -26,5 +26,6 @@ _EXPORTS = {
 def __getattr__(name):
     if name in _EXPORTS:
         from . import pqb
-        return getattr(pqb, name)
+        value = globals()[name] = getattr(pqb, name)
+        return value
     raise AttributeError(name)

@@ -489,6 +489,20 @@ def _on(dev, t, name, dtypes, contiguous=True):
     return t
 
 
+def _all_on(dev, dtypes, names, *ts):
+    """_on for several contiguous tensors at the price of one call."""
+    try:
+        for t in ts:
+            if t.device != dev or t.dtype not in dtypes or not t.is_contiguous():
+                break
+        else:
+            return
+    except AttributeError:
+        pass
+    for t, name in zip(ts, names.split()):
+        _on(dev, t, name, dtypes)
+
+
 def _gpu_of(t, name):
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name} must be a GPU tensor")
@@ -505,24 +519,25 @@ def _call_on(dev, fn, *args):
         return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
 
 
-_I32, _U8 = (torch.int32,), (torch.uint8,)
+_I32, _U8, _FLOATS = (torch.int32,), (torch.uint8,), (torch.bfloat16, torch.float32)
 
 
 def _pages_struct(cache: PagedKV, dev) -> _KvPages:
-    kc, vc = _on(dev, cache.k_codes, "k_codes", _U8), _on(dev, cache.v_codes, "v_codes", _U8)
-    ks, vs = _on(dev, cache.k_scales, "k_scales", _U8), _on(dev, cache.v_scales, "v_scales", _U8)
-    if kc.dim() != 4:
+    kc, vc, ks, vs = cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales
+    _all_on(dev, _U8, "k_codes v_codes k_scales v_scales", kc, vc, ks, vs)
+    shape, per_head = kc.shape, ks.shape
+    if len(shape) != 4:
         raise ValueError("k_codes must be [pages, heads, page_size, head_dim]")
-    N, H, S, D = kc.shape
-    if vc.shape != (N, H, D, S) or ks.shape != (N, H) or vs.shape != (N, H):
+    N, H, S, D = shape
+    if vc.shape != (N, H, D, S) or per_head != (N, H) or vs.shape != per_head:
         raise ValueError("v_codes must be [pages, heads, head_dim, page_size], scales [pages, heads]")
     return _KvPages(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), N, H, D, S, 0)
 
 
-def _token_rows(x: torch.Tensor):
+def _token_rows(x: torch.Tensor, shape):
     """x [tokens, heads, head_dim] with a token's values contiguous and tokens a
     16-byte multiple apart (copied if they are not), and the tokens' stride."""
-    T, H, D = x.shape
+    T, H, D = shape
     ld, head, one = x.stride()
     if T < 2:
         ld = H * D
@@ -544,12 +559,10 @@ def kv_plan_paged(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     kv_lens may be cached_lens and its free_used may be free_used."""
     dev = _gpu_of(cached_lens, "cached_lens")
     B = cached_lens.numel()
-    _on(dev, cached_lens, "cached_lens", _I32)
-    _on(dev, new_lens, "new_lens", _I32)
-    _on(dev, block_table, "block_table", _I32)
-    _on(dev, free_pages, "free_pages", _I32)
-    _on(dev, free_used, "free_used", _I32)
-    if new_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
+    _all_on(dev, _I32, "cached_lens new_lens block_table free_pages free_used", cached_lens, new_lens,
+            block_table, free_pages, free_used)
+    shape = block_table.shape
+    if new_lens.numel() != B or len(shape) != 2 or shape[0] != B:
         raise ValueError("new_lens must be [batch] and block_table [batch, width]")
     if free_used.numel() != 1:
         raise ValueError("free_used must hold one value")
@@ -560,7 +573,7 @@ def kv_plan_paged(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     ws = torch.empty((need // 4,), dtype=torch.int32, device=dev) if need else None
     if out is None:
         # one allocation, cut into the plan's parts
-        buf = torch.empty((max_new + 2 * B + 6,), dtype=torch.int32, device=dev)
+        buf = cached_lens.new_empty(max_new + 2 * B + 6)
         out = PagedPlan(*torch.split_with_sizes(buf, (max_new, B + 1, B, 1, 4)))
     else:
         sizes = (max_new, B + 1, B, 1, 4)
@@ -569,7 +582,7 @@ def kv_plan_paged(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table
             if _on(dev, t, "out." + name, _I32).numel() != n:
                 raise ValueError(f"out.{name} must hold {n} values")
     _check(_call_on(dev, L.pqb_kv_plan_paged, cached_lens.data_ptr(), new_lens.data_ptr(), B,
-                    block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(),
+                    block_table.data_ptr(), shape[1], free_pages.data_ptr(),
                     free_pages.numel(), free_used.data_ptr(), page_size, max_new,
                     out.slots.data_ptr(), out.q_starts.data_ptr(), out.kv_lens.data_ptr(),
                     out.free_used.data_ptr(), out.status.data_ptr(), _ptr(ws), need),
@@ -583,20 +596,22 @@ def kv_append_paged(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache
     outside the cache (-1) are skipped.  `slots` may hold more entries than
     there are tokens (a plan's slots are max_new long)."""
     dev = _gpu_of(k, "k")
-    for t, name in ((k, "k"), (v, "v")):
-        _on(dev, t, name, (torch.float32, torch.bfloat16), contiguous=False)
+    _on(dev, k, "k", _FLOATS, contiguous=False)
+    _on(dev, v, "v", _FLOATS, contiguous=False)
     _on(dev, slots, "slots", _I32)
     c = _pages_struct(cache, dev)
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or shape != v.shape or dtype != v.dtype:
         raise ValueError("k and v must be [tokens, heads, head_dim] of one shape and dtype")
-    if k.shape[1] != c.heads or k.shape[2] != c.head_dim:
+    T = shape[0]
+    if shape[1] != c.heads or shape[2] != c.head_dim:
         raise ValueError("k and v must have the cache's heads and head_dim")
-    if slots.numel() < k.shape[0]:
+    if slots.numel() < T:
         raise ValueError("slots must hold an entry per token")
-    k, k_ld = _token_rows(k)
-    v, v_ld = _token_rows(v)
+    k, k_ld = _token_rows(k, shape)
+    v, v_ld = _token_rows(v, shape)
     _check(_call_on(dev, lib().pqb_kv_append_paged, k.data_ptr(), v.data_ptr(),
-                    BF16 if k.dtype == torch.bfloat16 else F32, k.shape[0], k_ld, v_ld,
+                    BF16 if dtype == torch.bfloat16 else F32, T, k_ld, v_ld,
                     slots.data_ptr(), ctypes.byref(c)), "kv_append_paged")
 
 
@@ -614,39 +629,40 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     of one request where the caller knows it (a hint for speed and workspace).
     Rows outside every request are left as they were in `out`."""
     dev = _gpu_of(q, "q")
-    _on(dev, q, "q", (torch.float32, torch.bfloat16), contiguous=False)
+    _on(dev, q, "q", _FLOATS, contiguous=False)
     c = _pages_struct(cache, dev)
-    _on(dev, block_table, "block_table", _I32)
-    _on(dev, q_starts, "q_starts", _I32)
-    _on(dev, kv_lens, "kv_lens", _I32)
-    if q.dim() != 3 or q.shape[2] != c.head_dim or q.shape[1] % max(c.heads, 1):
+    _all_on(dev, _I32, "block_table q_starts kv_lens", block_table, q_starts, kv_lens)
+    shape, dtype, rows = q.shape, BF16 if q.dtype == torch.bfloat16 else F32, block_table.shape
+    if len(shape) != 3 or shape[2] != c.head_dim or shape[1] % max(c.heads, 1):
         raise ValueError("q must be [tokens, q_heads, head_dim] with q_heads a multiple of the cache's heads")
+    T, Hq, D = shape
     B = kv_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or q_starts.numel() != B + 1:
+    if len(rows) != 2 or rows[0] != B or q_starts.numel() != B + 1:
         raise ValueError("block_table must be [batch, width] and q_starts [batch + 1]")
     if max_q_len is not None and max_q_len < 1:
         raise ValueError("max_q_len must be positive")
-    T, Hq, D = q.shape
-    q, ld = _token_rows(q)
+    width, hint = rows[1], max_q_len or 0
+    q, ld = _token_rows(q, shape)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    elif _on(dev, out, "out", (q.dtype,)).shape != (T, Hq, D):
+        out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
+    elif _on(dev, out, "out", (q.dtype,)).shape != shape:
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     if T == 0 or B == 0:
         return out
     L = lib()
-    hint, dtype = max_q_len or 0, BF16 if q.dtype == torch.bfloat16 else F32
-    need = L.pqb_kv_attend_workspace_bytes(dtype, T, Hq, c.heads, D, B, block_table.shape[1], c.page_size, hint)
+    need = L.pqb_kv_attend_workspace_bytes(dtype, T, Hq, c.heads, D, B, width, c.page_size, hint)
     if workspace is None:
+        have = need
         if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _on(dev, workspace, "workspace", (workspace.dtype,))
-    have = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(_call_on(dev, L.pqb_kv_attend_paged, q.data_ptr(), dtype, T, Hq, ld, ctypes.byref(c), block_table.data_ptr(), block_table.shape[1],
-                    q_starts.data_ptr(), kv_lens.data_ptr(), B, int(causal),
-                    1.0 / math.sqrt(D) if scale is None else scale, hint, out.data_ptr(),
-                    _ptr(workspace), have), "kv_attend_paged")
+        have = workspace.numel() * workspace.element_size()
+    _check(_call_on(dev, L.pqb_kv_attend_paged, q.data_ptr(), dtype, T, Hq, ld, ctypes.byref(c),
+                    block_table.data_ptr(), width, q_starts.data_ptr(), kv_lens.data_ptr(), B,
+                    int(causal), 1.0 / math.sqrt(D) if scale is None else scale, hint,
+                    out.data_ptr(), None if workspace is None else workspace.data_ptr(), have),
+           "kv_attend_paged")
     return out
 
 

@@ -213,14 +213,38 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
   return e4m3_bytes4(lo[0] * f, lo[1] * f, hi[0] * f, hi[1] * f);
 }
 
+// Rows r0 .. r3 of four bytes -> columns c0 .. c3.
+__device__ __forceinline__ void transpose4(const uint32_t r[4], uint32_t c[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), b = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
+  const uint32_t d = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u), e = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+  c[0] = __builtin_amdgcn_perm(d, a, 0x05040100u);
+  c[1] = __builtin_amdgcn_perm(d, a, 0x07060302u);
+  c[2] = __builtin_amdgcn_perm(e, b, 0x05040100u);
+  c[3] = __builtin_amdgcn_perm(e, b, 0x07060302u);
+}
+
+// Eight values times inv, as codes.
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Raw8& raw, const T* tag, float inv) {
+  float v[8];
+  widen8(raw, tag, v);
+  return make_uint2(e4m3_bytes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    e4m3_bytes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+
+// One workgroup: a window of tokens, one head of K or V; every run that starts in
+// the window, to its end.  Its loads come in two rounds, the slots of the window
+// and of one page behind it, then the values and the held scale.
 template <typename T, int kD>
 __global__ __launch_bounds__(kAppThreads) void k_append(const AppendArgs a) {
   constexpr int kUnits = kD / 8;                             // 8-channel units of a token
   constexpr int kKeep = kAppRows * kUnits / kAppThreads;     // units a thread keeps
   constexpr int kLd = kD + 8;                                // LDS row: 8-byte steps, spread banks
-  __shared__ int run_at[kAppThreads], nruns;
+  constexpr int kMaxPage = 256;
+  __shared__ int run_at[kMaxPage], nruns;
+  __shared__ int32_t slot[2 * kMaxPage + 1];                 // of tokens t0 - 1, t0, ...
   __shared__ uint32_t red[kAppThreads / kWave];
-  __shared__ int red_n[kAppThreads / kWave];
+  __shared__ int red_n[kAppThreads / kWave], held_x;
   __shared__ __align__(16) uint8_t tile[kAppRows * kLd];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int head = blockIdx.y >> 1;
@@ -232,23 +256,27 @@ __global__ __launch_bounds__(kAppThreads) void k_append(const AppendArgs a) {
   uint8_t* codes = is_v ? a.v_codes : a.k_codes;
   uint8_t* scales = is_v ? a.v_scales : a.k_scales;
 
+  // a slot of -2 follows nothing and is followed by nothing
+  for (int i = tid; i < a.window + ps + 1; i += kAppThreads) {
+    const int64_t t = t0 - 1 + i;
+    slot[i] = t >= 0 && t < a.tokens ? a.slots[t] : -2;
+  }
   if (tid == 0) nruns = 0;
   __syncthreads();
-  if (tid < a.window && t0 + tid < a.tokens) {
-    const int64_t t = t0 + tid;
-    const int32_t s = a.slots[t];
-    const bool starts = t == 0 || (s & (ps - 1)) == 0 || (int64_t)a.slots[t - 1] + 1 != s;
+  if (tid < a.window) {
+    const int32_t s = slot[tid + 1];
+    const bool starts = (s & (ps - 1)) == 0 || (int64_t)slot[tid] + 1 != s;
     if (s >= 0 && s < nslots && starts) run_at[atomicAdd(&nruns, 1)] = tid;
   }
   __syncthreads();
   const int runs = nruns;
   for (int r = 0; r < runs; ++r) {
-    const int64_t t = t0 + run_at[r];
-    const int32_t s = a.slots[t];
+    const int first = run_at[r];
+    const int32_t s = slot[first + 1];
+    const int64_t t = t0 + first;
     const int off = s & (ps - 1);
     // the run's length: the first i >= 1 whose slot does not follow
-    const bool on = tid < ps - off && t + tid < a.tokens && (int64_t)a.slots[t + tid] == (int64_t)s + tid;
-    const uint64_t m = __ballot(on);
+    const uint64_t m = __ballot(tid < ps - off && (int64_t)slot[first + 1 + tid] == (int64_t)s + tid);
     if (lane == 0) red_n[wave] = m == ~0ull ? kWave : __builtin_ctzll(~m);
     __syncthreads();
     int n = 0;
@@ -262,17 +290,20 @@ __global__ __launch_bounds__(kAppThreads) void k_append(const AppendArgs a) {
     const T* src = x + t * ld;
     // tokens of the run up to the next multiple of kAppRows in the page are kept
     const int n0 = min(n, kAppRows - (off & (kAppRows - 1)));
+    if (tid == 0) held_x = (int)scales[tile_id] - kE8m0Bias;
     Raw8 keep[kKeep];
-    uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
       const int u = tid + i * kAppThreads, row = u / kUnits, col = u % kUnits;
-      if (row < n0) {
-        keep[i] = load_raw8(src + row * ld + col * 8);
-        float v[8];
-        widen8(keep[i], src, v);
-        amax = max(amax, as_u(absmax8(v)));
-      }
+      keep[i] = Raw8{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (row < n0) keep[i] = load_raw8(src + row * ld + col * 8);
+    }
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+      float v[8];
+      widen8(keep[i], src, v);
+      amax = max(amax, as_u(absmax8(v)));
     }
     for (int u = n0 * kUnits + tid; u < n * kUnits; u += kAppThreads) {
       float v[8];
@@ -281,10 +312,10 @@ __global__ __launch_bounds__(kAppThreads) void k_append(const AppendArgs a) {
     }
     amax = wave_umax(amax);
     if (lane == 0) red[wave] = amax;
-    const int xold = (int)scales[tile_id] - kE8m0Bias;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kAppThreads / kWave; ++w) amax = max(amax, red[w]);
+    const int xold = held_x;
     int xp = page_exponent(amax);
     if (off) xp = max(xp, xold);
     const bool grown = off && xp > xold;
@@ -299,81 +330,63 @@ __global__ __launch_bounds__(kAppThreads) void k_append(const AppendArgs a) {
           const uint4 w = *p;
           *p = make_uint4(rescale4(w.x, f), rescale4(w.y, f), rescale4(w.z, f), rescale4(w.w, f));
         }
+      uint2* out = reinterpret_cast<uint2*>(dst + (int64_t)off * kD);
 #pragma unroll
       for (int i = 0; i < kKeep; ++i) {
         const int u = tid + i * kAppThreads;
-        if (u / kUnits < n0) {
-          float v[8];
-          widen8(keep[i], src, v);
-          *reinterpret_cast<uint2*>(dst + (int64_t)off * kD + u * 8) =
-              make_uint2(e4m3_bytes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                         e4m3_bytes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-        }
+        if (u / kUnits < n0) out[u] = codes8(keep[i], src, inv);
       }
-      for (int u = n0 * kUnits + tid; u < n * kUnits; u += kAppThreads) {
-        float v[8];
-        widen8(load_raw8(src + (u / kUnits) * ld + (u % kUnits) * 8), src, v);
-        *reinterpret_cast<uint2*>(dst + (int64_t)off * kD + u * 8) =
-            make_uint2(e4m3_bytes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                       e4m3_bytes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-      }
+      for (int u = n0 * kUnits + tid; u < n * kUnits; u += kAppThreads)
+        out[u] = codes8(load_raw8(src + (u / kUnits) * ld + (u % kUnits) * 8), src, inv);
     } else {
       // kAppRows page offsets at a time: the run's codes into LDS by token, then
-      // dwords of four tokens of one channel out.  A dword is written by one
-      // thread, which keeps the bytes of tokens outside the run (held before it,
-      // rescaled if the exponent rose; untouched behind it).
-      const int groups = min(ps, kAppRows) / 4;
-      for (int c0 = 0; c0 < off + n; c0 += kAppRows) {
+      // blocks of four tokens by four channels turned and written along the tokens.
+      // A dword is written by one thread, which keeps the bytes of tokens outside
+      // the run (held before it, rescaled if the exponent rose; untouched behind it).
+      for (int c0 = grown ? 0 : off & -kAppRows; c0 < off + n; c0 += kAppRows) {
         const int lo = max(off, c0), hi = min(off + n, c0 + kAppRows);
-        if (hi <= lo && !grown) continue;
-        if (hi > lo) {
-          const int rows = hi - lo;
-          if (lo == off) {
+        if (lo == off && hi > lo) {
 #pragma unroll
-            for (int i = 0; i < kKeep; ++i) {
-              const int u = tid + i * kAppThreads, row = u / kUnits;
-              if (row < rows) {
-                float v[8];
-                widen8(keep[i], src, v);
-                *reinterpret_cast<uint2*>(tile + row * kLd + (u % kUnits) * 8) =
-                    make_uint2(e4m3_bytes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                               e4m3_bytes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-              }
-            }
-          } else {
-            for (int u = tid; u < rows * kUnits; u += kAppThreads) {
-              float v[8];
-              widen8(load_raw8(src + (int64_t)(lo - off + u / kUnits) * ld + (u % kUnits) * 8), src, v);
-              *reinterpret_cast<uint2*>(tile + (u / kUnits) * kLd + (u % kUnits) * 8) =
-                  make_uint2(e4m3_bytes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                             e4m3_bytes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-            }
+          for (int i = 0; i < kKeep; ++i) {
+            const int u = tid + i * kAppThreads, row = u / kUnits;
+            if (row < hi - lo) *reinterpret_cast<uint2*>(tile + row * kLd + (u % kUnits) * 8) = codes8(keep[i], src, inv);
           }
+        } else {
+          for (int u = tid; u < (hi - lo) * kUnits; u += kAppThreads)
+            *reinterpret_cast<uint2*>(tile + (u / kUnits) * kLd + (u % kUnits) * 8) =
+                codes8(load_raw8(src + (int64_t)(lo - off + u / kUnits) * ld + (u % kUnits) * 8), src, inv);
         }
         __syncthreads();
-        for (int i = tid; i < kD * groups; i += kAppThreads) {
-          const int d = i / groups, o = c0 + (i % groups) * 4;
-          const bool any_new = o < hi && o + 4 > lo, all_new = o >= lo && o + 4 <= hi;
-          if (!any_new && !(grown && o < off)) continue;
+        const int from = (grown ? c0 : lo) >> 2, groups = ((hi + 3) >> 2) - from;
+        for (int i = tid; i < groups * (kD / 4); i += kAppThreads) {
+          const int d = i / groups * 4, o = (from + i % groups) * 4;
           uint32_t* p = reinterpret_cast<uint32_t*>(dst + (d << a.shift) + o);
-          const uint32_t was = all_new ? 0 : *p, up = grown && o < off ? rescale4(was, f) : was;
-          uint32_t w = 0;
+          uint32_t rows[4], cols[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int at = o + j;
-            uint32_t byte;
-            if (at >= lo && at < hi)
-              byte = tile[(at - lo) * kLd + d];
-            else
-              byte = ((at < off ? up : was) >> (8 * j)) & 0xFFu;
-            w |= byte << (8 * j);
+          for (int k = 0; k < 4; ++k)
+            rows[k] = o + k >= lo && o + k < hi ? *reinterpret_cast<const uint32_t*>(tile + (o + k - lo) * kLd + d) : 0;
+          transpose4(rows, cols);
+          if (o < lo || o + 4 > hi) {
+            // bytes of the run, and of what is held before it
+            const int b0 = min(max(lo - o, 0), 4), b1 = min(max(hi - o, 0), 4);
+            const uint32_t below = b0 == 4 ? ~0u : (1u << (8 * b0)) - 1;
+            const uint32_t fresh = (b1 == 4 ? ~0u : (1u << (8 * b1)) - 1) & ~below;
+            uint32_t was[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) was[k] = p[(k << a.shift) / 4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t held = grown ? (rescale4(was[k], f) & below) | (was[k] & ~below) : was[k];
+              cols[k] = (cols[k] & fresh) | (held & ~fresh);
+            }
           }
-          *p = w;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) p[(k << a.shift) / 4] = cols[k];
         }
         __syncthreads();
       }
     }
-    __syncthreads();  // red, red_n and the tile are free for the next run
+    __syncthreads();  // red, red_n, held_x and the tile are free for the next run
   }
 }
 
@@ -388,7 +401,7 @@ void append_d(const AppendArgs& a, int head_dim, dim3 grid, hipStream_t st) {
 }
 
 // About this many workgroups before a window takes more than one token.
-constexpr int64_t kAppendGroups = 8192;
+constexpr int64_t kAppendGroups = 4096;
 
 }  // namespace
 

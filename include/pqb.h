@@ -352,7 +352,7 @@ typedef struct pqb_kv_pages {
  * kv_lens may be cached_lens and free_used_out may be free_used (a step in
  * place); no other arrays may overlap.  The lengths stay on the GPU, so a
  * captured step can be replayed.  Workspace: pqb_kv_plan_workspace_bytes(), 4-
- * byte aligned (0 bytes for up to 2048 requests and 4096 slots).
+ * byte aligned (0 bytes for up to 2048 requests and 1024 slots).
  * Shape rules: batch, table_width, free_total and max_new in [0, 2^31), and
  * table_width * page_size < 2^31 - 256.  All arrays 4-byte aligned.  Errors,
  * before any launch: PQB_ERR_SHAPE, PQB_ERR_NULL, PQB_ERR_ALIGN,

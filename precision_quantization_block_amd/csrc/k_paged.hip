@@ -7,9 +7,12 @@
 //   slots[S_b + i] = table[b, (c_b + i) / ps] ps + (c_b + i) % ps   0 <= i < n_b.
 // A few hundred bytes to a few hundred kilobytes move, so the time is launch and
 // dependent-load latency: one workgroup takes both sums in one scan (a 64-bit
-// word holds n below and need above) and, up to kPlanOneMax slots, fills the
-// slots too.  Beyond that a second launch fills them with one thread per slot,
-// each finding its request by bisection of S.
+// word holds n below and need above) and fills the slots too, each thread finding
+// its slot's request by bisection of S in LDS.  More than kPlanOneMax slots take a
+// workgroup for each kPlanOneMax: every one repeats the sums rather than wait for
+// them, and the first writes them.  That needs inputs that no output overlaps;
+// a step in place, or more requests than LDS holds, fills its slots in a
+// second launch.
 //
 // Append.  One workgroup per run (consecutive slots inside one page), head and
 // tensor.  The page's exponent is X = the smallest integer with
@@ -19,6 +22,8 @@
 // codes before the run are decoded, scaled and encoded again.  The input is
 // read once (the first 64 tokens of a run stay in registers between the maximum
 // and the codes) and V goes through LDS to be written along its tokens.
+#include <algorithm>
+
 #include "../../include/pqb.h"
 #include "launch.h"
 #include "paged.h"
@@ -31,7 +36,7 @@ namespace {
 // ---------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / kWave;
-constexpr int64_t kPlanOneMax = 4096;  // slots filled by the planning workgroup itself
+constexpr int64_t kPlanOneMax = 1024;  // slots that a planning workgroup fills
 constexpr int kPlanOneBatch = 2048;    // requests whose sums it then keeps in LDS
 
 __device__ __forceinline__ uint64_t wave_incl_sum(uint64_t v) {
@@ -87,6 +92,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const PlanArgs a) {
   __shared__ int32_t first[kFill ? kPlanOneBatch + 1 : 1], held[kFill ? kPlanOneBatch : 1],
       base[kFill ? kPlanOneBatch : 1];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const bool writer = blockIdx.x == 0;
   if (tid == 0) flags = 0;
   __syncthreads();
   const int64_t used = *a.free_used, room = a.width << a.shift;
@@ -124,12 +130,14 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const PlanArgs a) {
   if (tokens > a.max_new) bad |= PQB_PLAN_SLOTS;
   if (used >= 0 && need > a.free_total - used) bad |= PQB_PLAN_PAGES;
   if (tid == 0) {
-    a.status[0] = (int32_t)bad;
-    a.status[1] = (int32_t)min(need, (int64_t)INT32_MAX);
-    a.status[2] = (int32_t)min(tokens, (int64_t)INT32_MAX);
-    a.status[3] = 0;
-    *a.free_used_out = (int32_t)(bad ? used : used + need);
-    a.starts[a.batch] = bad ? 0 : (int32_t)tokens;
+    if (writer) {
+      a.status[0] = (int32_t)bad;
+      a.status[1] = (int32_t)min(need, (int64_t)INT32_MAX);
+      a.status[2] = (int32_t)min(tokens, (int64_t)INT32_MAX);
+      a.status[3] = 0;
+      *a.free_used_out = (int32_t)(bad ? used : used + need);
+      a.starts[a.batch] = bad ? 0 : (int32_t)tokens;
+    }
     if constexpr (kFill) first[a.batch] = bad ? 0 : (int32_t)tokens;
   }
   uint64_t run = 0;  // sums of the chunks before this one: tokens below, pages above
@@ -155,8 +163,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const PlanArgs a) {
     if (b < a.batch) {
       const uint64_t ex = before + incl - v;
       const int32_t s0 = (int32_t)(uint32_t)ex, p0 = (int32_t)used + (int32_t)(ex >> 32);
-      a.starts[b] = s0;
-      a.kv_lens[b] = c + n;
+      if (writer) {
+        a.starts[b] = s0;
+        a.kv_lens[b] = c + n;
+      }
       if constexpr (kFill) {
         first[b] = s0;
         held[b] = c;
@@ -169,7 +179,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(const PlanArgs a) {
   }
   if constexpr (kFill) {
     const int64_t total = bad ? 0 : tokens;
-    for (int64_t t = tid; t < a.max_new; t += kPlanThreads) {
+    const int64_t t0 = (int64_t)blockIdx.x * kPlanOneMax, t1 = min(t0 + kPlanOneMax, a.max_new);
+    for (int64_t t = t0 + tid; t < t1; t += kPlanThreads) {
       int32_t slot = -1;
       if (t < total) {
         const int64_t b = find_row(first, a.batch, t);
@@ -405,13 +416,20 @@ constexpr int64_t kAppendGroups = 4096;
 
 }  // namespace
 
+// Whether the second launch is what fills the slots.
+static bool plan_two_launches(int64_t batch, int64_t max_new, bool in_place) {
+  return batch > kPlanOneBatch || (in_place && max_new > kPlanOneMax);
+}
+
 size_t plan_workspace_bytes(int64_t batch, int64_t max_new) {
-  return max_new <= kPlanOneMax && batch <= kPlanOneBatch ? 0 : 4 * (size_t)batch;
+  return plan_two_launches(batch, max_new, true) ? 4 * (size_t)batch : 0;
 }
 
 hipError_t launch_plan(const PlanArgs& a, hipStream_t st) {
-  if (plan_workspace_bytes(a.batch, a.max_new) == 0) {
-    hipLaunchKernelGGL((k_plan<true>), dim3(1), dim3(kPlanThreads), 0, st, a);
+  const bool in_place = a.kv_lens == a.cached || a.free_used_out == a.free_used;
+  if (!plan_two_launches(a.batch, a.max_new, in_place)) {
+    const int64_t groups = std::max<int64_t>(1, (a.max_new + kPlanOneMax - 1) / kPlanOneMax);
+    hipLaunchKernelGGL((k_plan<true>), dim3((unsigned)groups), dim3(kPlanThreads), 0, st, a);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((k_plan<false>), dim3(1), dim3(kPlanThreads), 0, st, a);

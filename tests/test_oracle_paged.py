@@ -102,7 +102,7 @@ def test_status_has_a_text():
     (dict(page=512), -4), (dict(cached=None), -1), (dict(status=None), -1), (dict(slots=None), -1),
     (dict(free_pages=None), -1), (dict(table=None), -1), (dict(used=None), -1), (dict(starts=None), -1),
     (dict(table=ctypes.c_void_p((1 << 20) + 2)), -5), (dict(slots=ctypes.c_void_p((1 << 20) + 1)), -5),
-    (dict(max_new=4097), -6), (dict(batch=2049), -6), (dict(max_new=4097, ws=None, wsb=1 << 20), -1)])
+    (dict(max_new=1025), -6), (dict(batch=2049), -6), (dict(max_new=1025, ws=None, wsb=1 << 20), -1)])
 def test_plan_refuses(kw, status):
     d = dict(cached=FAKE, new=FAKE, batch=3, table=FAKE, width=8, free_pages=FAKE, free=9, used=FAKE, page=16,
              max_new=9, slots=FAKE, starts=FAKE, kv=FAKE, out=FAKE, status=FAKE, ws=FAKE, wsb=0) | kw
@@ -158,7 +158,7 @@ def test_workspaces():
     assert ws(width=8) == 0 < ws(width=9)                  # 512 tokens: one item each
     assert ws() <= ws(hint=0) and ws(dtype=0) <= ws(dtype=0, hint=0)
     assert ws(heads=7) == ws(rows=0) == ws(batch=0) == ws(dtype=2) == ws(page=8) == ws(batch=1 << 20) == 0
-    assert L.pqb_kv_plan_workspace_bytes(2048, 4096) == 0 and L.pqb_kv_plan_workspace_bytes(7, 4097) == 28
+    assert L.pqb_kv_plan_workspace_bytes(2048, 1024) == 0 and L.pqb_kv_plan_workspace_bytes(7, 1025) == 28
 
 
 def test_binding_refuses_host_tensors():

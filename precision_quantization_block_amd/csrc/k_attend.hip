@@ -36,8 +36,7 @@ constexpr int kMetaUnits = 64;   // units whose pages are looked up at a time
 constexpr int kMinUnits = 2 * kWaves;             // fewest units of a split
 constexpr int kMaxPartRows = 64;                  // rows of a float32 request that may be split
 constexpr int64_t kGroupsWanted = 1536;           // workgroups a split aims at
-constexpr int64_t kMaxGridYZ = 65535;
-constexpr int64_t kMaxGroups = 1 << 23;            // workgroups of a join
+constexpr int64_t kMaxGroups = 1 << 23;            // workgroups that splits or joins lead to
 constexpr int kMinWideUnits = 8;                  // the same for the wide kernel
 constexpr int64_t kMaxWideSplits = 32, kWideGroupsWanted = 512;
 
@@ -288,24 +287,24 @@ struct RowsLds {
   int pg[kWaves][kMetaUnits * kGroups], xs[kWaves][kMetaUnits * kGroups];
 };
 
+// Item x for KV head h, row tiles z, z + nz, ...
 template <int kD, bool kF32, bool kWholePages>
-__global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
+__device__ __forceinline__ void attend_rows(const AttendArgs& a, int64_t x, int h, int z, int nz,
+                                            RowsLds<kD, kWholePages>& lds) {
   constexpr int kKC = kD / 64;       // 16-byte key reads of a lane per 16-row tile
   constexpr int kDT = kD / 16;       // 16-channel tiles of O; also the DMA steps of a unit's keys, or V
   constexpr int kKeyChunks = kD / 16;
   constexpr int kParts = kF32 ? 3 : 1;
   constexpr int kGroups = RowsLds<kD, kWholePages>::kGroups;
-  __shared__ __align__(16) RowsLds<kD, kWholePages> lds;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int col = lane & 15, g4 = lane >> 4;
-  const int h = blockIdx.y;
   uint8_t *kb = lds.in.k[wave], *vb = lds.in.v[wave];
   int *pg = lds.pg[wave], *xs = lds.xs[wave];
 
   const Request first = lane_request(a, 0);
   const int C = split_units(a, first);
-  const Item it = find_item<false>(a, blockIdx.x, C, first);
+  const Item it = find_item<false>(a, x, C, first);
   if (it.b < 0) return;
   const Request rq = it.rq;
   const int32_t rows = rq.n * a.group;
@@ -330,8 +329,8 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
   voff = (uint32_t)(((lane >> 2) << a.shift) + (kWholePages ? 16 * vg : 0));
   constexpr uint32_t kFlip = kD % 128 == 0 ? 64 : 32;         // row_swizzle(16), in bytes
 
-  for (int rt = blockIdx.z; rt * kTile < rows; rt += gridDim.z) {
-    if (rt != (int)blockIdx.z) __syncthreads();  // the last tile's reads of LDS are done
+  for (int rt = z; rt * kTile < rows; rt += nz) {
+    if (rt != z) __syncthreads();  // the last tile's reads of LDS are done
     const int row = rt * kTile + col;
     const bool valid = row < rows;
     const int tok = row / a.group, hq = h * a.group + row % a.group;
@@ -573,7 +572,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
         store_row<kF32, kD / 16>(a.out, ((int64_t)(rq.start + grow_row / a.group) * a.heads * a.group +
                                          h * a.group + grow_row % a.group) * kD + d0, acc);
       } else {
-        const int64_t slot = ((int64_t)blockIdx.x * a.heads + h) * a.part_rows + grow_row;
+        const int64_t slot = (x * a.heads + h) * a.part_rows + grow_row;
         store_row<true, kD / 16>(a.part_o, slot * kD + d0, acc);
         if (tid % 16 == 0) {
           a.part_ml[2 * slot] = M;
@@ -582,6 +581,12 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
       }
     }
   }
+}
+
+template <int kD, bool kF32, bool kWholePages>
+__global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
+  __shared__ __align__(16) RowsLds<kD, kWholePages> lds;
+  attend_rows<kD, kF32, kWholePages>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -663,19 +668,27 @@ __device__ __forceinline__ WideSplit wide_split(const AttendArgs& a, int end) {
 }
 
 template <int kD, bool kWholePages>
-__global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(const AttendArgs a) {
+struct WideLds {
+  static constexpr int kGroups = kWholePages ? 1 : 4;   // pages that a unit may lie in
+  uint8_t kbuf[kStages][kUnit * kD], vbuf[kStages][kUnit * kD];
+  // page (-1: none) and scales (K's byte, V's << 8) of the units ahead
+  int pg[2 * kMetaUnits * kGroups], xs[2 * kMetaUnits * kGroups];
+};
+
+// Row tile y of KV head h, one of its splits.
+template <int kD, bool kWholePages>
+__device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t y, int split,
+                                            WideLds<kD, kWholePages>& lds) {
   constexpr int kKS = kD / 64;    // 64-deep steps of S^T; also the DMA steps of a wave and tensor
   constexpr int kDT = kD / 32;    // 32-channel tiles of O^T
   constexpr int kKeyChunks = kD / 16;
-  constexpr int kGroups = kWholePages ? 1 : 4;   // pages that a unit may lie in
-  __shared__ __align__(16) uint8_t kbuf[kStages][kUnit * kD], vbuf[kStages][kUnit * kD];
-  // page and scales of the units ahead: pg -1 if there is none, xs K's byte and V's << 8
-  __shared__ __align__(16) int pg[2 * kMetaUnits * kGroups], xs[2 * kMetaUnits * kGroups];
+  constexpr int kGroups = WideLds<kD, kWholePages>::kGroups;
+  auto &kbuf = lds.kbuf, &vbuf = lds.vbuf;
+  auto &pg = lds.pg, &xs = lds.xs;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n = lane & 31, half = lane >> 5;
-  const int h = blockIdx.x;
-  const WideTile wt = find_wide(a, a.wide_first + blockIdx.y);
+  const WideTile wt = find_wide(a, y);
   if (wt.b < 0) return;
   const Request rq = wt.rq;
   const int rows = rq.n * a.group, row0 = wt.tile * kWideTile + wave * kWideRows, row = row0 + n;
@@ -686,7 +699,6 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   const int first_limit = a.causal ? ahead + row0 / a.group : rq.kv;
   const int wave_end = row0 >= rows ? 0 : a.causal ? ahead + (min(row0 + kWideRows, rows) - 1) / a.group : rq.kv;
   const int tile_end = a.causal ? ahead + (min((wt.tile + 1) * kWideTile, rows) - 1) / a.group : rq.kv;
-  const int split = blockIdx.z;
   const WideSplit ws = wide_split(a, tile_end);
   if (split >= ws.count) return;
   const int u0 = __builtin_amdgcn_readfirstlane(split * ws.per);
@@ -1025,6 +1037,25 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_wide(con
   }
 }
 
+// Both kinds in one launch, for calls whose requests may have many rows: the wide
+// tiles first, the few-row items behind them, where they fill the places that the
+// last tiles leave.  Head by head: where the KV heads divide by 8, a head's tiles
+// keep to one XCD and share its L2.
+template <int kD, bool kWholePages>
+__global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_both(const AttendArgs a, int64_t tiles,
+                                                                             int64_t wide_groups) {
+  __shared__ __align__(16) union Lds {
+    RowsLds<kD, kWholePages> rows;
+    WideLds<kD, kWholePages> wide;
+  } lds;
+  const int64_t x = blockIdx.x, item = x / a.heads;
+  const int h = (int)(x % a.heads);
+  if (x < wide_groups)
+    attend_wide<kD, kWholePages>(a, h, item % tiles, (int)(item / tiles), lds.wide);
+  else
+    attend_rows<kD, false, kWholePages>(a, item - wide_groups / a.heads, h, 0, 1, lds.rows);
+}
+
 // Joins what was split: workgroups below `row_groups` take one request, KV head and
 // row (z, strided) of the row kernel's items; the others kGroups rows of the wide
 // kernel's each.  D / 4 threads cover a row.
@@ -1143,6 +1174,8 @@ struct Plan {
   size_t part_o, part_ml, wide_o, wide_ml, bytes;   // floats before each part, and all bytes
 };
 
+int64_t wide_tiles(int64_t q_rows, int64_t batch, int64_t group) { return q_rows * group / kWideTile + batch; }
+
 Plan plan_of(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_t max_rows, int64_t width,
              int shift, int head_dim, bool bf16) {
   Plan p{};
@@ -1153,7 +1186,8 @@ Plan plan_of(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_
   p.wide_splits = 1;
   if (p.wide && (width << shift) > (int64_t)kMinWideUnits * kUnit) {
     const int64_t groups = (q_rows * group + kWideTile - 1) / kWideTile * heads;
-    p.wide_splits = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxWideSplits, kWideGroupsWanted / groups));
+    const int64_t most = kMaxGroups / (wide_tiles(q_rows, batch, group) * heads);
+    p.wide_splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxWideSplits, kWideGroupsWanted / groups, most}));
   }
   const size_t rows = (size_t)p.items * heads * p.part_rows;
   const size_t wide = p.wide_splits > 1 ? (size_t)p.wide_splits * q_rows * heads * group : 0;
@@ -1164,36 +1198,29 @@ Plan plan_of(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_
   return p;
 }
 
-template <int kD>
-hipError_t run_wide(AttendArgs a, const Plan& p, hipStream_t st) {
-  const int64_t tiles = a.q_rows * a.group / kWideTile + a.batch;
-  for (a.wide_first = 0; a.wide_first < tiles; a.wide_first += kMaxGridYZ) {
-    const int64_t left = tiles - a.wide_first;
-    const dim3 grid((unsigned)a.heads, (unsigned)(left < kMaxGridYZ ? left : kMaxGridYZ), (unsigned)p.wide_splits);
-    if ((1 << a.shift) >= kUnit)
-      hipLaunchKernelGGL((k_attend_wide<kD, true>), grid, dim3(kThreads), 0, st, a);
-    else
-      hipLaunchKernelGGL((k_attend_wide<kD, false>), grid, dim3(kThreads), 0, st, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+template <int kD, bool kF32, bool kWholePages>
+void run_parts(const AttendArgs& a, const Plan& p, int64_t max_rows, hipStream_t st) {
+  const int64_t items = p.items ? p.items : a.batch;
+  if constexpr (!kF32) {
+    if (p.wide) {
+      const int64_t tiles = wide_tiles(a.q_rows, a.batch, a.group), wide_groups = tiles * p.wide_splits * a.heads;
+      hipLaunchKernelGGL((k_attend_both<kD, kWholePages>), dim3((unsigned)(wide_groups + items * a.heads)),
+                         dim3(kThreads), 0, st, a, tiles, wide_groups);
+      return;
+    }
   }
-  return hipSuccess;
+  const int64_t tiles = (max_rows + kTile - 1) / kTile;
+  hipLaunchKernelGGL((k_attend_rows<kD, kF32, kWholePages>),
+                     dim3((unsigned)items, (unsigned)a.heads, (unsigned)(tiles < 64 ? tiles : 64)), dim3(kThreads), 0,
+                     st, a);
 }
 
 template <int kD, bool kF32>
 hipError_t run(const AttendArgs& a, const Plan& p, int64_t max_rows, hipStream_t st) {
-  if constexpr (!kF32) {
-    if (p.wide) {
-      const hipError_t e = run_wide<kD>(a, p, st);
-      if (e != hipSuccess) return e;
-    }
-  }
-  const int64_t tiles = p.wide ? 1 : (max_rows + kTile - 1) / kTile;
-  const dim3 grid((unsigned)(p.items ? p.items : a.batch), (unsigned)a.heads, (unsigned)(tiles < 64 ? tiles : 64));
   if ((1 << a.shift) >= kUnit)
-    hipLaunchKernelGGL((k_attend_rows<kD, kF32, true>), grid, dim3(kThreads), 0, st, a);
+    run_parts<kD, kF32, true>(a, p, max_rows, st);
   else
-    hipLaunchKernelGGL((k_attend_rows<kD, kF32, false>), grid, dim3(kThreads), 0, st, a);
+    run_parts<kD, kF32, false>(a, p, max_rows, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!p.items && p.wide_splits == 1)) return e;
   constexpr int64_t kJoinRows = kThreads / (kD / 4);

@@ -232,7 +232,6 @@ struct AttendArgs {
   int32_t part_rows;                          // rows of a request that may be split
   int32_t wide;                               // requests of more rows go to the wide kernel
   int32_t wide_splits;
-  int64_t wide_first;
 };
 // The workspace for at most max_rows = max_q_len * group rows per request.
 size_t attend_workspace_bytes(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_t max_rows,

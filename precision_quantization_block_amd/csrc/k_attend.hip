@@ -740,8 +740,8 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
     }
   };
 
-  // Staging, kStages - 1 units ahead of V's use and one more for keys: S^T of unit
-  // u + 1 is formed under the softmax of unit u.  A wave's DMA takes the keys of
+  // Staging.  While unit u has its O^T formed, u + 1 has its P and u + 2 its S^T: V is
+  // staged kStages - 1 units ahead of u and keys two more.  A wave's DMA takes the keys of
   // 16-token group `wave` and a quarter of V's channels; this lane's V bytes are
   // of group vg.  A key group lies in one page, so its address is uniform.
   const int vg = (lane & 3) ^ ((lane >> 3) & 3);
@@ -778,8 +778,8 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
         dma16(vp + voff[i], to);
     }
   };
-  // Waits until at most `steps` of this wave's newest staging steps (keys of a
-  // unit and V of the one before: 2 kKS loads) are in flight.
+  // Waits until at most `steps` of this wave's newest staging steps (V of a unit and
+  // keys of the second behind it: 2 kKS loads) are in flight.
   auto wait_steps = [&](int steps) {
     static_assert(kStages == 4, "one wait for each number of steps");
     if (steps >= 3)
@@ -796,13 +796,14 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   const uint8_t *k_next = nullptr, *v_next = nullptr;   // where the next staging step reads
   if (u0 < units) {
     stage_k(u0, k_from(u0));
+    stage_k(u0 + 1, k_from(u0 + 1));   // behind the last unit: page 0's bytes, unused
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i)
       if (u0 + i < units) {
         stage_v(u0 + i, v_from(u0 + i));
-        stage_k(u0 + i + 1, k_from(u0 + i + 1));   // behind the last unit: page 0's bytes, unused
+        // (of the fourth unit's keys, in the first's place, only when those are used up)
+        if (i < kStages - 2) stage_k(u0 + i + 2, k_from(u0 + i + 2));
       }
-    k_next = k_from(u0 + kStages), v_next = v_from(u0 + kStages - 1);
   }
   load_scales(u0);
 
@@ -887,59 +888,28 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
       }
     return sum;
   };
-
-  // The unit's largest V exponent, negative lo where some page is none, and the V
-  // exponents of this lane's two token groups.
-  int xr_next = 1, lo_next = 0, xv_next[2] = {1, 1};
+  // What unit u's pages say: its largest V exponent, negative `lo` where some page
+  // is none, and the V exponents of this lane's two token groups.
+  struct Scales {
+    int xr, lo, xv[2];
+  };
   auto scales_of = [&](int u) {
+    Scales c;
     if constexpr (kWholePages) {
-      xr_next = __builtin_amdgcn_readfirstlane(xs[meta_at(u, 0)]) >> 8;
-      lo_next = __builtin_amdgcn_readfirstlane(pg[meta_at(u, 0)]);
-      xv_next[0] = xv_next[1] = xr_next;
+      c.xr = __builtin_amdgcn_readfirstlane(xs[meta_at(u, 0)]) >> 8;
+      c.lo = __builtin_amdgcn_readfirstlane(pg[meta_at(u, 0)]);
+      c.xv[0] = c.xv[1] = c.xr;
     } else {
       const int4 x = *reinterpret_cast<const int4*>(&xs[meta_at(u, 0)]), p = *reinterpret_cast<const int4*>(&pg[meta_at(u, 0)]);
-      xr_next = max(max(x.x, x.y), max(x.z, x.w)) >> 8;
-      lo_next = min(min(p.x, p.y), min(p.z, p.w));
-      xv_next[0] = (half ? x.z : x.x) >> 8;
-      xv_next[1] = (half ? x.w : x.y) >> 8;
+      c.xr = max(max(x.x, x.y), max(x.z, x.w)) >> 8;
+      c.lo = min(min(p.x, p.y), min(p.z, p.w));
+      c.xv[0] = (half ? x.z : x.x) >> 8;
+      c.xv[1] = (half ? x.w : x.y) >> 8;
     }
+    return c;
   };
-
-  // One unit: s holds its S^T, next receives the following unit's.
-  auto unit = [&](int u, f32x16* s, f32x16* next) {
-    const int buf = u % kStages;
-    wait_steps(min(kStages - 2, units - 1 - u));  // this wave's DMA: keys of u + 1, V of u
-    __syncthreads();
-    if (u + kStages - 1 < units) {
-      stage_v(u + kStages - 1, v_next);
-      stage_k(u + kStages, k_next);
-      if (((u + kStages + 1 - u0) & (kMetaUnits - 1)) == 0) {
-        load_pages(u + kStages + 1);
-        load_scales(u + kStages + 1);
-        __syncthreads();
-      }
-    }
-    const int xr = xr_next, lo = lo_next;
-    int xv[2] = {xv_next[0], xv_next[1]};
-    if (lo < 0 || (u + 1) * kUnit > rq.kv) {
-      // codes behind the last token, or of no page, may be anything: V's become 0
-      for (int i = tid; i < 4 * kD; i += kThreads) {
-        const int d = i >> 2, g = (i & 3) ^ ((d >> 1) & 3);
-        const int held = pg[meta_at(u, g)] < 0 ? 0 : min(max(rq.kv - (u * kUnit + 16 * g), 0), 16);
-        uint32_t* p = reinterpret_cast<uint32_t*>(&vbuf[buf][i * 16]);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int nb = min(max(held - 4 * w, 0), 4);
-          if (nb < 4) p[w] &= (1u << (8 * nb)) - 1;
-        }
-      }
-      __syncthreads();
-    }
-    // for the next unit, ahead of its barrier
-    scales_of(u + 1);
-    k_next = k_from(u + kStages + 1), v_next = v_from(u + kStages);
-    if (u * kUnit >= wave_end) return;
-
+  // -inf for what unit u's rows do not see
+  auto mask = [&](int u, int lo, f32x16* s) {
     if (lo < 0 || (u + 1) * kUnit > first_limit) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -949,14 +919,13 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
           if (j >= cnt) s[t][j] = -INFINITY;
       }
     }
-    // The next unit's S^T (of whatever LDS holds behind the last unit: unused)
-    // beside this unit's P.
-    scores(u + 1, next);
-    uint32_t pw[2][8];
-    float sum = weights(s, r, pw);
-    // No maximum is taken while P fits f16: what does not, or the first unit's
-    // infinite r, shows in the sum.
+  };
+  // No maximum is taken while P fits f16: what does not, or the first unit's
+  // infinite r, shows in the sum.  Then the reference moves to the maximum, and O
+  // and l with it; and to a larger V exponent.
+  auto settle = [&](int xr, const f32x16* s, const f32x16* later, uint32_t (*pw)[8], float sum) {
     if (__ballot(!(sum <= 65000.0f)) || xr > R) {
+      asm volatile("" ::"v"(later[0]), "v"(later[1]));   // keeps their products above this branch
       float mx = s[0][0];
 #pragma unroll
       for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[0][j]);
@@ -979,6 +948,9 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
       R = R_new;
     }
     l += sum;
+  };
+  // O^T += V^T P^T of unit u
+  auto values = [&](int u, const int* xv, const uint32_t (*pw)[8]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const float sv = as_f((uint32_t)(127 - min(max(R - xv[t], 0), 60)) << 23);
@@ -987,23 +959,87 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
 #pragma unroll
       for (int i = 0; i < kDT; ++i) {
         const int d = 32 * i + n;
-        const uint4 w = *reinterpret_cast<const uint4*>(&vbuf[buf][d * 64 + (((2 * half + t) ^ ((d >> 1) & 3)) << 4)]);
+        const uint4 w = *reinterpret_cast<const uint4*>(&vbuf[u % kStages][d * 64 + (((2 * half + t) ^ ((d >> 1) & 3)) << 4)]);
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.x, w.y, sv), p0, o[i], 0, 0, 0);
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.z, w.w, sv), p1, o[i], 0, 0, 0);
       }
     }
   };
+  // Waits for unit u's V and unit u + 2's keys, sends the next staging step out, and
+  // clears the V codes of unit u behind the last token or of no page (they may be
+  // anything).
+  auto advance = [&](int u, int lo) {
+    wait_steps(min(kStages - 2, units - 1 - u));
+    __syncthreads();
+    if (u + kStages - 1 < units) {
+      stage_v(u + kStages - 1, v_next);
+      stage_k(u + kStages + 1, k_next);
+      if (((u + kStages + 2 - u0) & (kMetaUnits - 1)) == 0) {
+        load_pages(u + kStages + 2);
+        load_scales(u + kStages + 2);
+        __syncthreads();
+      }
+    }
+    if (lo < 0 || (u + 1) * kUnit > rq.kv) {
+      for (int i = tid; i < 4 * kD; i += kThreads) {
+        const int d = i >> 2, g = (i & 3) ^ ((d >> 1) & 3);
+        const int held = pg[meta_at(u, g)] < 0 ? 0 : min(max(rq.kv - (u * kUnit + 16 * g), 0), 16);
+        uint32_t* p = reinterpret_cast<uint32_t*>(&vbuf[u % kStages][i * 16]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int nb = min(max(held - 4 * w, 0), 4);
+          if (nb < 4) p[w] &= (1u << (8 * nb)) - 1;
+        }
+      }
+      __syncthreads();
+    }
+    k_next = k_from(u + kStages + 2), v_next = v_from(u + kStages);
+  };
+
+  // One unit that has a next: O^T of unit u, P of u + 1 and S^T of u + 2 (of whatever
+  // LDS holds behind the last: unused), three independent things in one block.
+  Scales now, ahead1;
+  auto unit = [&](int u, uint32_t (*pw)[8], f32x16* s1, uint32_t (*pw1)[8], f32x16* s2) {
+    advance(u, now.lo);
+    const Scales then = scales_of(u + 2);
+    if (u * kUnit < wave_end) {
+      mask(u + 1, ahead1.lo, s1);
+      scores(u + 2, s2);
+      const float sum = weights(s1, r, pw1);
+      values(u, now.xv, pw);
+      settle(ahead1.xr, s1, s2, pw1, sum);
+    }
+    now = ahead1;
+    ahead1 = then;
+  };
 
   f32x16 sa[2], sb[2];
+  uint32_t pa[2][8], pb[2][8];
   if (u0 < units) {
-    wait_steps(min(kStages - 1, units - u0));
+    wait_steps(min(kStages - 2, units - u0));   // the keys of the first two units
     __syncthreads();
-    scales_of(u0);
+    now = scales_of(u0);
+    ahead1 = scales_of(u0 + 1);
     scores(u0, sa);
+    scores(u0 + 1, sb);
+    mask(u0, now.lo, sa);
+    settle(now.xr, sa, sb, pa, INFINITY);
+    __syncthreads();                  // the first unit's keys are used up
+    if (u0 + kStages - 2 < units) stage_k(u0 + kStages, k_from(u0 + kStages));
+    k_next = k_from(u0 + kStages + 1), v_next = v_from(u0 + kStages - 1);
   }
-  for (int u = u0; u < units; u += 2) {
-    unit(u, sa, sb);
-    if (u + 1 < units) unit(u + 1, sb, sa);
+  int u = u0;
+  for (; u + 2 < units; u += 2) {
+    unit(u, pa, sb, pb, sa);
+    unit(u + 1, pb, sa, pa, sb);
+  }
+  if (u + 1 < units) {
+    unit(u, pa, sb, pb, sa);
+    advance(u + 1, now.lo);
+    if ((u + 1) * kUnit < wave_end) values(u + 1, now.xv, pb);
+  } else if (u < units) {
+    advance(u, now.lo);
+    if (u * kUnit < wave_end) values(u, now.xv, pa);
   }
 
   if (!valid) return;

@@ -1150,30 +1150,48 @@ __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t group) {
   constexpr int kQuads = kD / 4, kGroups = kThreads / kQuads;
   const int tid = threadIdx.x, quad = tid % kQuads, grp = tid / kQuads, q_heads = a.heads * a.group;
   const int64_t total = a.q_rows * q_heads, at = group * kGroups + grp;
-  if (grp >= kGroups || at >= total) return;
-  const int t = (int)(at / q_heads), g = (int)(at % q_heads) % a.group;
-  int64_t lo = 0, hi = a.batch;   // the request of query row t
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (a.starts[mid] <= t)
-      lo = mid;
-    else
-      hi = mid;
+  const bool inside = grp < kGroups && at < total;
+  const int t = inside ? (int)(at / q_heads) : -1, g = (int)(at % q_heads) % a.group;
+  // the request of each row's query token, all of the wave's at once
+  Request rq{0, 0, 0};
+  for (int64_t b0 = 0; b0 < a.batch; b0 += kWave) {
+    const Request r = lane_request(a, b0);
+    uint64_t left = __ballot(inside);
+    while (left) {   // one token a turn
+      const int ts = __builtin_amdgcn_readlane(t, __builtin_ctzll(left));
+      const uint64_t m = __ballot(ts >= r.start && ts < r.start + r.n);
+      if (m && t == ts) rq = from_lane(r, __builtin_ctzll(m));
+      left &= ~__ballot(t == ts);
+    }
   }
-  const Request rq = request(a, lo);
   const int rows = rq.n * a.group, tok = t - rq.start;
-  if (rows <= a.part_rows || tok < 0 || tok >= rq.n) return;
+  if (!inside || rows <= a.part_rows) return;
   const int last = min((tok * a.group + g) / kWideTile * kWideTile + kWideTile, rows) - 1;
   const int n = wide_split(a, a.causal ? rq.kv - rq.n + 1 + last / a.group : rq.kv).count;
   if (n < 2) return;
   float M = -INFINITY, L = 0;
   f32x4 acc = {0, 0, 0, 0};
-  for (int i = 0; i < n; ++i) M = fmaxf(M, a.wide_ml[2 * (i * total + at)]);
-  for (int i = 0; i < n; ++i) {
-    const int64_t slot = i * total + at;
-    const float mi = a.wide_ml[2 * slot], wt = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mi - M) * a.c);
-    L += a.wide_ml[2 * slot + 1] * wt;
-    acc += *reinterpret_cast<const f32x4*>(a.wide_o + slot * kD + 4 * quad) * wt;
+  for (int i0 = 0; i0 < n; i0 += 4) {   // four parts' loads at a time
+    float mi[4], li[4];
+    f32x4 oi[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t slot = (int64_t)min(i0 + k, n - 1) * total + at;
+      mi[k] = i0 + k < n ? a.wide_ml[2 * slot] : -INFINITY;
+      li[k] = a.wide_ml[2 * slot + 1];
+      oi[k] = *reinterpret_cast<const f32x4*>(a.wide_o + slot * kD + 4 * quad);
+    }
+    const float top = fmaxf(M, fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])));
+    const float keep = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((M - top) * a.c);
+    L *= keep;
+    acc *= keep;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float wt = mi[k] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mi[k] - top) * a.c);
+      L += li[k] * wt;
+      acc += oi[k] * wt;
+    }
+    M = top;
   }
   const float inv = L > 0 ? 1.0f / L : 0.0f;
   const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};

@@ -396,7 +396,8 @@ pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, in
 /* Attention of new tokens over their requests' pages:
  *   out[t, g] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * (q[t, g] . k_j) - max).
  * q: `dtype` [q_rows, q_heads, head_dim], a token's heads and channels contiguous,
- * tokens q_stride elements apart; out: the same type, contiguous.  Request b owns
+ * tokens q_stride elements apart; out: the same type, contiguous, not overlapping
+ * q.  Request b owns
  * rows q_starts[b] .. q_starts[b + 1] - 1 (i32 [batch + 1], rising) and kv_lens[b]
  * tokens (i32), its pages in block_table[b] (i32 [batch, table_width]); query
  * head g reads KV head g / (q_heads / heads).  With causal != 0, query i of n sees

@@ -645,8 +645,8 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     q, ld = _token_rows(q, shape)
     if out is None:
         out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
-    elif _on(dev, out, "out", (q.dtype,)).shape != shape:
-        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    elif _on(dev, out, "out", (q.dtype,)).shape != shape or out.data_ptr() == q.data_ptr() and T:
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype, apart from q")
     if T == 0 or B == 0:
         return out
     L = lib()

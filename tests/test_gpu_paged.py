@@ -394,7 +394,7 @@ def test_binding_refuses():
            lambda: pqb.kv_append_paged(x, x, i, pqb.PagedKV(c.k_codes, c.k_codes, c.k_scales, c.v_scales)),
            lambda: pqb.kv_append_paged(x, x, i, pqb.PagedKV(c.k_codes, c.v_codes, c.k_scales.float(), c.v_scales)),
            lambda: pqb.kv_attend_paged(x[:, :1], c, t, s, i), lambda: pqb.kv_attend_paged(x, c, t, i, i),
-           lambda: pqb.kv_attend_paged(x, c, t, s, i, out=x.float()), lambda: pqb.kv_attend_paged(x, c, t, s, i, max_q_len=0),
+           lambda: pqb.kv_attend_paged(x, c, t, s, i, out=x.float()), lambda: pqb.kv_attend_paged(x, c, t, s, i, out=x), lambda: pqb.kv_attend_paged(x, c, t, s, i, max_q_len=0),
            lambda: pqb.kv_attend_paged(x, c, t.cpu(), s, i)]
     for n, call in enumerate(bad):
         with pytest.raises(ValueError):

@@ -445,7 +445,7 @@ def kv_read_kivi(k_parts, v_parts, shape, bits: int = 2, out_dtype=torch.bfloat1
 # paged 8-bit KV cache
 # --------------------------------------------------------------------------
 
-@dataclass
+@dataclass(slots=True)
 class PagedKV:
     """One layer's paged 8-bit KV cache: E4M3 codes with a power-of-two scale
     (E8M0 byte X + 127) per page and head; V is transposed inside its page."""
@@ -465,7 +465,7 @@ def kv_paged_cache(pages: int, heads: int, page_size: int, head_dim: int, device
                    torch.empty((pages, heads), dtype=torch.uint8, device=dev))
 
 
-@dataclass
+@dataclass(slots=True)
 class PagedPlan:
     """What kv_plan_paged wrote (all int32 on the GPU)."""
     slots: torch.Tensor      # [max_new] slot of each new token, -1 behind the last
@@ -478,53 +478,57 @@ class PagedPlan:
 PLAN_FLAGS = {"pages": 1, "table": 2, "slots": 4, "negative": 8}
 
 
-def _on(dev, t, name, dtypes, contiguous=True):
-    """t, checked to be a contiguous tensor of `dev` (in-place arguments are never copied)."""
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+_I32, _U8, _BF16, _F32 = torch.int32, torch.uint8, torch.bfloat16, torch.float32
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _all_on(dev, dtypes, names, *ts):
-    """_on for several contiguous tensors at the price of one call."""
+def _refuse(dev, dtypes, names, *ts, contiguous=True):
+    """Raises for the first of ts that is not a (contiguous) tensor of `dev` and of one of dtypes."""
+    for t, name in zip(ts, names.split()):
+        if not isinstance(t, torch.Tensor) or t.device != dev or dev.type != "cuda":
+            where = dev if dev is not None and dev.type == "cuda" else "a GPU"
+            raise ValueError(f"{name} must be a GPU tensor on {where}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _ready(dev, dtype, *ts) -> bool:
+    """Whether all of ts are contiguous tensors of `dev` and dtype (in-place arguments
+    are never copied).  One loop: these checks are a third of a small call's time."""
     try:
         for t in ts:
-            if t.device != dev or t.dtype not in dtypes or not t.is_contiguous():
-                break
-        else:
-            return
+            if t.device != dev or t.dtype is not dtype or not t.is_contiguous():
+                return False
     except AttributeError:
-        pass
-    for t, name in zip(ts, names.split()):
-        _on(dev, t, name, dtypes)
+        return False
+    return True
 
 
-def _gpu_of(t, name):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        raise ValueError(f"{name} must be a GPU tensor")
-    return t.device
+def _device_of(t, name):
+    """The GPU of a float32 or bf16 tensor, of any strides."""
+    dev = t.device if isinstance(t, torch.Tensor) else None
+    if dev is None or dev.type != "cuda" or (t.dtype is not _BF16 and t.dtype is not _F32):
+        _refuse(dev, (_F32, _BF16), name, t, contiguous=False)
+    return dev
 
 
 def _call_on(dev, fn, *args):
     """fn(*args, the device's current stream), with `dev` the current device.
     (The raw stream handle: torch.cuda.current_stream() builds an object, 1.8 of
     the 14 us that a small call took.)"""
-    if dev.index == torch._C._cuda_getDevice():
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    index = dev.index
+    if index == _current_device():
+        return fn(*args, _raw_stream(index))
     with torch.cuda.device(dev):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
-
-
-_I32, _U8, _FLOATS = (torch.int32,), (torch.uint8,), (torch.bfloat16, torch.float32)
+        return fn(*args, _raw_stream(index))
 
 
 def _pages_struct(cache: PagedKV, dev) -> _KvPages:
     kc, vc, ks, vs = cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales
-    _all_on(dev, _U8, "k_codes v_codes k_scales v_scales", kc, vc, ks, vs)
+    if not _ready(dev, _U8, kc, vc, ks, vs):
+        _refuse(dev, (_U8,), "k_codes v_codes k_scales v_scales", kc, vc, ks, vs)
     shape, per_head = kc.shape, ks.shape
     if len(shape) != 4:
         raise ValueError("k_codes must be [pages, heads, page_size, head_dim]")
@@ -534,17 +538,18 @@ def _pages_struct(cache: PagedKV, dev) -> _KvPages:
     return _KvPages(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), N, H, D, S, 0)
 
 
-def _token_rows(x: torch.Tensor, shape):
+def _token_rows(x: torch.Tensor, shape, es: int):
     """x [tokens, heads, head_dim] with a token's values contiguous and tokens a
     16-byte multiple apart (copied if they are not), and the tokens' stride."""
     T, H, D = shape
     ld, head, one = x.stride()
+    row = H * D
     if T < 2:
-        ld = H * D
-    if not x.numel() or (one == 1 and (head == D or H == 1) and ld >= H * D and not ld * x.element_size() % 16
-                         and not x.data_ptr() % 16):
-        return x, max(ld, H * D)
-    return x.clone(memory_format=torch.contiguous_format), H * D
+        ld = row
+    if one == 1 and (head == D or H == 1) and ld >= row and not ld * es % 16 and not x.data_ptr() % 16 \
+            or not T:
+        return x, ld if ld > row else row
+    return x.clone(memory_format=torch.contiguous_format), row
 
 
 def kv_plan_paged(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -557,10 +562,12 @@ def kv_plan_paged(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     status[0] is not 0 (PLAN_FLAGS), nothing was handed out, the slots are -1 and
     there are no query rows.  `out`: a plan of the same sizes to write into; its
     kv_lens may be cached_lens and its free_used may be free_used."""
-    dev = _gpu_of(cached_lens, "cached_lens")
+    dev = cached_lens.device if isinstance(cached_lens, torch.Tensor) else None
+    if dev is None or dev.type != "cuda" or not _ready(dev, _I32, cached_lens, new_lens, block_table, free_pages,
+                                                       free_used):
+        _refuse(dev, (_I32,), "cached_lens new_lens block_table free_pages free_used", cached_lens, new_lens,
+                block_table, free_pages, free_used)
     B = cached_lens.numel()
-    _all_on(dev, _I32, "cached_lens new_lens block_table free_pages free_used", cached_lens, new_lens,
-            block_table, free_pages, free_used)
     shape = block_table.shape
     if new_lens.numel() != B or len(shape) != 2 or shape[0] != B:
         raise ValueError("new_lens must be [batch] and block_table [batch, width]")
@@ -578,9 +585,10 @@ def kv_plan_paged(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     else:
         sizes = (max_new, B + 1, B, 1, 4)
         parts = (out.slots, out.q_starts, out.kv_lens, out.free_used, out.status)
-        for t, n, name in zip(parts, sizes, ("slots", "q_starts", "kv_lens", "free_used", "status")):
-            if _on(dev, t, "out." + name, _I32).numel() != n:
-                raise ValueError(f"out.{name} must hold {n} values")
+        if not _ready(dev, _I32, *parts):
+            _refuse(dev, (_I32,), "out.slots out.q_starts out.kv_lens out.free_used out.status", *parts)
+        if any(t.numel() != n for t, n in zip(parts, sizes)):
+            raise ValueError(f"out must hold {sizes} values in slots, q_starts, kv_lens, free_used and status")
     _check(_call_on(dev, L.pqb_kv_plan_paged, cached_lens.data_ptr(), new_lens.data_ptr(), B,
                     block_table.data_ptr(), shape[1], free_pages.data_ptr(),
                     free_pages.numel(), free_used.data_ptr(), page_size, max_new,
@@ -595,24 +603,26 @@ def kv_append_paged(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache
     tokens at any stride) into their slots of the cache; tokens of a slot
     outside the cache (-1) are skipped.  `slots` may hold more entries than
     there are tokens (a plan's slots are max_new long)."""
-    dev = _gpu_of(k, "k")
-    _on(dev, k, "k", _FLOATS, contiguous=False)
-    _on(dev, v, "v", _FLOATS, contiguous=False)
-    _on(dev, slots, "slots", _I32)
+    dev, dtype = _device_of(k, "k"), k.dtype
+    if _device_of(v, "v") != dev or not _ready(dev, _I32, slots):
+        _refuse(dev, (_F32, _BF16), "v", v, contiguous=False)
+        _refuse(dev, (_I32,), "slots", slots)
     c = _pages_struct(cache, dev)
-    shape, dtype = k.shape, k.dtype
-    if len(shape) != 3 or shape != v.shape or dtype != v.dtype:
+    shape = k.shape
+    if len(shape) != 3 or shape != v.shape or dtype is not v.dtype:
         raise ValueError("k and v must be [tokens, heads, head_dim] of one shape and dtype")
     T = shape[0]
     if shape[1] != c.heads or shape[2] != c.head_dim:
         raise ValueError("k and v must have the cache's heads and head_dim")
     if slots.numel() < T:
         raise ValueError("slots must hold an entry per token")
-    k, k_ld = _token_rows(k, shape)
-    v, v_ld = _token_rows(v, shape)
-    _check(_call_on(dev, lib().pqb_kv_append_paged, k.data_ptr(), v.data_ptr(),
-                    BF16 if dtype == torch.bfloat16 else F32, T, k_ld, v_ld,
-                    slots.data_ptr(), ctypes.byref(c)), "kv_append_paged")
+    es = 2 if dtype is _BF16 else 4
+    k, k_ld = _token_rows(k, shape, es)
+    v, v_ld = _token_rows(v, shape, es)
+    status = _call_on(dev, lib().pqb_kv_append_paged, k.data_ptr(), v.data_ptr(), BF16 if es == 2 else F32, T,
+                      k_ld, v_ld, slots.data_ptr(), ctypes.byref(c))
+    if status:
+        raise PqbError(status, "kv_append_paged")
 
 
 def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
@@ -628,11 +638,11 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     scale: 1 / sqrt(head_dim) unless given.  max_q_len: the most query tokens
     of one request where the caller knows it (a hint for speed and workspace).
     Rows outside every request are left as they were in `out`."""
-    dev = _gpu_of(q, "q")
-    _on(dev, q, "q", _FLOATS, contiguous=False)
+    dev = _device_of(q, "q")
     c = _pages_struct(cache, dev)
-    _all_on(dev, _I32, "block_table q_starts kv_lens", block_table, q_starts, kv_lens)
-    shape, dtype, rows = q.shape, BF16 if q.dtype == torch.bfloat16 else F32, block_table.shape
+    if not _ready(dev, _I32, block_table, q_starts, kv_lens):
+        _refuse(dev, (_I32,), "block_table q_starts kv_lens", block_table, q_starts, kv_lens)
+    shape, dtype, rows = q.shape, BF16 if q.dtype is _BF16 else F32, block_table.shape
     if len(shape) != 3 or shape[2] != c.head_dim or shape[1] % max(c.heads, 1):
         raise ValueError("q must be [tokens, q_heads, head_dim] with q_heads a multiple of the cache's heads")
     T, Hq, D = shape
@@ -642,11 +652,11 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     if max_q_len is not None and max_q_len < 1:
         raise ValueError("max_q_len must be positive")
     width, hint = rows[1], max_q_len or 0
-    q, ld = _token_rows(q, shape)
     if out is None:
         out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
-    elif _on(dev, out, "out", (q.dtype,)).shape != shape or out.data_ptr() == q.data_ptr() and T:
+    elif not _ready(dev, q.dtype, out) or out.shape != shape or out.data_ptr() == q.data_ptr() and T:
         raise ValueError("out must be a contiguous tensor of q's shape and dtype, apart from q")
+    q, ld = _token_rows(q, shape, 2 if dtype == BF16 else 4)
     if T == 0 or B == 0:
         return out
     L = lib()
@@ -655,14 +665,16 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
         have = need
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    else:
-        _on(dev, workspace, "workspace", (workspace.dtype,))
+    elif _ready(dev, workspace.dtype, workspace):
         have = workspace.numel() * workspace.element_size()
-    _check(_call_on(dev, L.pqb_kv_attend_paged, q.data_ptr(), dtype, T, Hq, ld, ctypes.byref(c),
-                    block_table.data_ptr(), width, q_starts.data_ptr(), kv_lens.data_ptr(), B,
-                    int(causal), 1.0 / math.sqrt(D) if scale is None else scale, hint,
-                    out.data_ptr(), None if workspace is None else workspace.data_ptr(), have),
-           "kv_attend_paged")
+    else:
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    status = _call_on(dev, L.pqb_kv_attend_paged, q.data_ptr(), dtype, T, Hq, ld, ctypes.byref(c),
+                      block_table.data_ptr(), width, q_starts.data_ptr(), kv_lens.data_ptr(), B, causal,
+                      D ** -0.5 if scale is None else scale, hint, out.data_ptr(),
+                      None if workspace is None else workspace.data_ptr(), have)
+    if status:
+        raise PqbError(status, "kv_attend_paged")
     return out
 
 

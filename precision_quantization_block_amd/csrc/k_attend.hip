@@ -34,7 +34,7 @@ constexpr int kTile = 16;        // query rows of a tile
 constexpr int kWaves = 4, kThreads = kWaves * kWave;
 constexpr int kMetaUnits = 64;   // units whose pages are looked up at a time
 constexpr int kMinUnits = 2 * kWaves;             // fewest units of a split
-constexpr int kMaxPartRows = 64;                  // rows of a float32 request that may be split
+constexpr int kMaxPartRows = 64;                  // rows of a request that the row kernel may split
 constexpr int64_t kGroupsWanted = 1536;           // workgroups a split aims at
 constexpr int64_t kMaxGroups = 1 << 23;            // workgroups that splits or joins lead to
 constexpr int kMinWideUnits = 8;                  // the same for the wide kernel
@@ -249,7 +249,7 @@ __device__ __forceinline__ float swap_sum(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Few query rows: single tokens (and float32 rows of any number), 16 rows a tile.
+// Few query rows: single tokens, 16 rows a tile.
 // Bound by the bytes of the cache.
 //
 // One workgroup takes an item's units for one KV head, its waves every fourth
@@ -287,7 +287,8 @@ struct RowsLds {
   int pg[kWaves][kMetaUnits * kGroups], xs[kWaves][kMetaUnits * kGroups];
 };
 
-// Item x for KV head h, row tiles z, z + nz, ...
+// Item x for KV head h, row tiles z, z + nz, ... (more than one where the wide kernel
+// does not go, or the hint of the most query tokens was wrong).
 template <int kD, bool kF32, bool kWholePages>
 __device__ __forceinline__ void attend_rows(const AttendArgs& a, int64_t x, int h, int z, int nz,
                                             RowsLds<kD, kWholePages>& lds) {
@@ -590,7 +591,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many query rows: prompts and chunks (bf16).
+// Many query rows: prompts and chunks.
 //
 // A workgroup takes 128 rows of one KV head, 32 a wave, over its request's
 // units of 64 tokens; both tiles of a unit (64 D bytes each) go straight into
@@ -602,6 +603,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 // significant bits and lo holds the other 4, exact down to 2^-14 of the row's
 // largest and within 2^-23 of it below.  Two products of twice the bf16 rate
 // cost what one bf16 product would, and half the LDS bytes.
+// A float32 q stays in its three bf16 parts, against keys decoded to bf16.
 // O^T: V is decoded to f16 beside the products (v_cvt_scalef32_pk_f16_fp8).
 //
 // Key row m = 8 a + 4 h + b of tile t stands for token 32 h + 16 t + 4 a + b: a
@@ -616,6 +618,10 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 constexpr float kPExp = 9.0f;      // p is held times 2^9
 constexpr int kStages = 4;        // units in LDS at a time
 constexpr int kWideRows = 32, kWideTile = kWaves * kWideRows;
+
+// The wide kernel's head dimensions.  Three parts of a wider float32 q do not fit its
+// registers beside O; such rows stay with the row kernel, 16 at a time.
+constexpr bool wide_takes(int head_dim, bool bf16) { return bf16 || head_dim <= 128; }
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -684,12 +690,13 @@ struct WideLds {
 };
 
 // Row tile y of KV head h, one of its splits.
-template <int kD, bool kWholePages>
+template <int kD, bool kF32, bool kWholePages>
 __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t y, int split,
                                             WideLds<kD, kWholePages>& lds) {
   constexpr int kKS = kD / 64;    // 64-deep steps of S^T; also the DMA steps of a wave and tensor
   constexpr int kDT = kD / 32;    // 32-channel tiles of O^T
   constexpr int kKeyChunks = kD / 16;
+  constexpr int kPParts = kF32 ? 2 : 1;   // f16 parts of P
   constexpr int kGroups = WideLds<kD, kWholePages>::kGroups;
   auto &kbuf = lds.kbuf, &vbuf = lds.vbuf;
   auto &pg = lds.pg, &xs = lds.xs;
@@ -715,17 +722,21 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   const int64_t page_bytes = (int64_t)kD << a.shift;
   const int ps1 = (1 << a.shift) - 1;
 
-  // q's loads go out first: they return under the page lookups and the first DMA
-  uint4 raw[kKS][4];
-  {
-    const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(rq.start + tok) * a.q_stride +
-                         (int64_t)(h * a.group + row % a.group) * kD + half * 32;
+  // q's loads go out first: they return under the page lookups and the first DMA.
+  // This lane's 32 channels of each 64.
+  const int64_t q_at = (int64_t)(rq.start + tok) * a.q_stride + (int64_t)(h * a.group + row % a.group) * kD + half * 32;
+  uint4 raw[kF32 ? 1 : kKS][4];
+  bf16x8 qf[kF32 ? kKS : 1][4][3];
 #pragma unroll
-    for (int s = 0; s < kKS; ++s)
+  for (int s = 0; s < kKS; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        raw[s][i] = valid ? *reinterpret_cast<const uint4*>(qp + s * 64 + i * 8) : make_uint4(0, 0, 0, 0);
-  }
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kF32)
+        load_q8<true>(a.q, q_at + s * 64 + i * 8, valid, qf[s][i]);
+      else
+        raw[s][i] = valid ? *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + q_at + s * 64 + i * 8)
+                          : make_uint4(0, 0, 0, 0);
+    }
 
   // What the units lie in: kMetaUnits units' pages and scales at a time.
   auto meta_at = [&](int u, int group) { return (u & (2 * kMetaUnits - 1)) * kGroups + (kWholePages ? 0 : group); };
@@ -816,9 +827,9 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   load_scales(u0);
 
   // q as 2^e (hi + lo / 16)
-  v8i qh[kKS], ql[kKS];
-  int eh;
-  {
+  v8i qh[kF32 ? 1 : kKS], ql[kF32 ? 1 : kKS];
+  int eh = 0;
+  if constexpr (!kF32) {
     float mx = 0;
 #pragma unroll
     for (int s = 0; s < kKS; ++s)
@@ -875,14 +886,26 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
         const int ch = ks * 4 + half * 2;
         const uint4 lo = *reinterpret_cast<const uint4*>(&kbuf[u % kStages][token * kD + ((ch ^ key) << 4)]);
         const uint4 hi = *reinterpret_cast<const uint4*>(&kbuf[u % kStages][token * kD + (((ch + 1) ^ key) << 4)]);
-        const v8i kf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-        to[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, ql[ks], to[t], 0, 0, 0, sk, 0, el);
-        to[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qh[ks], to[t], 0, 0, 0, sk, 0, eh);
+        if constexpr (kF32) {
+          const uint32_t kw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bf16x8 kf = codes_bf16(kw[2 * i], kw[2 * i + 1], as_f((uint32_t)sk << 23));
+#pragma unroll
+            for (int p = 2; p >= 0; --p)
+              to[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks][i][p], to[t], 0, 0, 0);
+          }
+        } else {
+          const v8i kf = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+          to[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, ql[ks], to[t], 0, 0, 0, sk, 0, el);
+          to[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(kf, qh[ks], to[t], 0, 0, 0, sk, 0, eh);
+        }
       }
     }
   };
-  // P of one unit as f16 pairs, and this lane's sum
-  auto weights = [&](const f32x16* s, float r, uint32_t (*pw)[8]) {
+  // P of one unit as f16 pairs (float32: and what they leave over), and this lane's sum
+  typedef uint32_t Weights[kPParts][2][8];
+  auto weights = [&](const f32x16* s, float r, Weights& pw) {
     float sum = 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -892,7 +915,11 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
         const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][2 * j + 1], c, r));
         sum += p0;
         sum += p1;
-        pw[t][j] = cvt_f16x2(p0, p1);
+        pw[0][t][j] = cvt_f16x2(p0, p1);
+        if constexpr (kF32) {
+          const f16x2 b = __builtin_bit_cast(f16x2, pw[0][t][j]);
+          pw[kPParts - 1][t][j] = cvt_f16x2(p0 - (float)b[0], p1 - (float)b[1]);
+        }
       }
     return sum;
   };
@@ -931,7 +958,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   // No maximum is taken while P fits f16: what does not, or the first unit's
   // infinite r, shows in the sum.  Then the reference moves to the maximum, and O
   // and l with it; and to a larger V exponent.
-  auto settle = [&](int xr, const f32x16* s, const f32x16* later, uint32_t (*pw)[8], float sum) {
+  auto settle = [&](int xr, const f32x16* s, const f32x16* later, Weights& pw, float sum) {
     if (__ballot(!(sum <= 65000.0f)) || xr > R) {
       asm volatile("" ::"v"(later[0]), "v"(later[1]));   // keeps their products above this branch
       float mx = s[0][0];
@@ -958,18 +985,30 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
     l += sum;
   };
   // O^T += V^T P^T of unit u
-  auto values = [&](int u, const int* xv, const uint32_t (*pw)[8]) {
+  auto values = [&](int u, const int* xv, const Weights& pw) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const float sv = as_f((uint32_t)(127 - min(max(R - xv[t], 0), 60)) << 23);
-      const f16x8 p0 = __builtin_bit_cast(f16x8, make_uint4(pw[t][0], pw[t][1], pw[t][2], pw[t][3]));
-      const f16x8 p1 = __builtin_bit_cast(f16x8, make_uint4(pw[t][4], pw[t][5], pw[t][6], pw[t][7]));
+      f16x8 pf[kPParts][2];
+#pragma unroll
+      for (int k = 0; k < kPParts; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          pf[k][e] = __builtin_bit_cast(f16x8, make_uint4(pw[k][t][4 * e], pw[k][t][4 * e + 1], pw[k][t][4 * e + 2], pw[k][t][4 * e + 3]));
 #pragma unroll
       for (int i = 0; i < kDT; ++i) {
         const int d = 32 * i + n;
         const uint4 w = *reinterpret_cast<const uint4*>(&vbuf[u % kStages][d * 64 + (((2 * half + t) ^ ((d >> 1) & 3)) << 4)]);
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.x, w.y, sv), p0, o[i], 0, 0, 0);
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.z, w.w, sv), p1, o[i], 0, 0, 0);
+        if constexpr (kF32) {
+          const f16x8 v0 = codes_f16(w.x, w.y, sv), v1 = codes_f16(w.z, w.w, sv);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, pf[kPParts - 1][0], o[i], 0, 0, 0);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, pf[kPParts - 1][1], o[i], 0, 0, 0);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, pf[0][0], o[i], 0, 0, 0);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, pf[0][1], o[i], 0, 0, 0);
+        } else {
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.x, w.y, sv), pf[0][0], o[i], 0, 0, 0);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(codes_f16(w.z, w.w, sv), pf[0][1], o[i], 0, 0, 0);
+        }
       }
     }
   };
@@ -1007,14 +1046,14 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   // One unit that has a next: O^T of unit u, P of u + 1 and S^T of u + 2 (of whatever
   // LDS holds behind the last: unused), three independent things in one block.
   Scales now, ahead1;
-  auto unit = [&](int u, uint32_t (*pw)[8], f32x16* s1, uint32_t (*pw1)[8], f32x16* s2) {
+  auto unit = [&](int u, const Weights& pw, f32x16* s1, Weights& pw1, f32x16* s2) {
     advance(u, now.lo);
     const Scales then = scales_of(u + 2);
     if (u * kUnit < wave_end) {
       mask(u + 1, ahead1.lo, s1);
       scores(u + 2, s2);
-      const float sum = weights(s1, r, pw1);
       values(u, now.xv, pw);
+      const float sum = weights(s1, r, pw1);
       settle(ahead1.xr, s1, s2, pw1, sum);
     }
     now = ahead1;
@@ -1022,7 +1061,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   };
 
   f32x16 sa[2], sb[2];
-  uint32_t pa[2][8], pb[2][8];
+  Weights pa, pb;
   if (u0 < units) {
     wait_steps(min(kStages - 2, units - u0));   // the keys of the first two units
     __syncthreads();
@@ -1061,7 +1100,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
       for (int j = 0; j < 4; ++j) {
         const float v[4] = {o[i][4 * j] * scale, o[i][4 * j + 1] * scale, o[i][4 * j + 2] * scale,
                             o[i][4 * j + 3] * scale};
-        store_row<false, 4>(a.out, out_row * kD + 4 * half + 32 * i + 8 * j, v);
+        store_row<kF32, 4>(a.out, out_row * kD + 4 * half + 32 * i + 8 * j, v);
       }
   } else {
     const int64_t slot = (int64_t)split * a.q_rows * a.heads * a.group + out_row;
@@ -1075,7 +1114,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
         store_row<true, 4>(a.wide_o, slot * kD + 4 * half + 32 * i + 8 * j, v);
       }
     if (half == 0) {
-      a.wide_ml[2 * slot] = m;
+      a.wide_ml[2 * slot] = m == -INFINITY ? m : kPExp - r;   // the reference that O and l have, in powers of 2
       a.wide_ml[2 * slot + 1] = l * 0x1p-9f;
     }
   }
@@ -1088,8 +1127,8 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
 // the others they hold places while the dispatcher deals out, and leave some CUs
 // with three workgroups and some with one.  Head by head: where the KV heads
 // divide by 8, a head's tiles keep to one XCD and share its L2.
-template <int kD, bool kWholePages>
-__global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_both(const AttendArgs a,
+template <int kD, bool kF32, bool kWholePages>
+__global__ __launch_bounds__(kThreads, kD <= 128 && !kF32 ? 2 : 1) void k_attend_both(const AttendArgs a,
                                                                              int64_t wide_groups) {
   __shared__ __align__(16) union Lds {
     RowsLds<kD, kWholePages> rows;
@@ -1098,9 +1137,9 @@ __global__ __launch_bounds__(kThreads, kD <= 128 ? 2 : 1) void k_attend_both(con
   const int64_t x = blockIdx.x, item = x / a.heads;
   const int h = (int)(x % a.heads);
   if (x < wide_groups)
-    attend_wide<kD, kWholePages>(a, h, item / a.wide_splits, (int)(item % a.wide_splits), lds.wide);
+    attend_wide<kD, kF32, kWholePages>(a, h, item / a.wide_splits, (int)(item % a.wide_splits), lds.wide);
   else
-    attend_rows<kD, false, kWholePages>(a, item - wide_groups / a.heads, h, 0, 1, lds.rows);
+    attend_rows<kD, kF32, kWholePages>(a, item - wide_groups / a.heads, h, 0, 1, lds.rows);
 }
 
 // Joins what was split: workgroups below `row_groups` take one request, KV head and
@@ -1156,7 +1195,7 @@ __device__ __forceinline__ void join_items(const AttendArgs& a, int64_t b, int h
   }
 }
 
-template <int kD>
+template <int kD, bool kF32>
 __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t group) {
   constexpr int kQuads = kD / 4, kGroups = kThreads / kQuads;
   const int tid = threadIdx.x, quad = tid % kQuads, grp = tid / kQuads, q_heads = a.heads * a.group;
@@ -1193,12 +1232,12 @@ __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t group) {
       oi[k] = *reinterpret_cast<const f32x4*>(a.wide_o + slot * kD + 4 * quad);
     }
     const float top = fmaxf(M, fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])));
-    const float keep = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((M - top) * a.c);
+    const float keep = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(M - top);
     L *= keep;
     acc *= keep;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float wt = mi[k] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mi[k] - top) * a.c);
+      const float wt = mi[k] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi[k] - top);
       L += li[k] * wt;
       acc += oi[k] * wt;
     }
@@ -1206,7 +1245,7 @@ __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t group) {
   }
   const float inv = L > 0 ? 1.0f / L : 0.0f;
   const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
-  store_row<false, 4>(a.out, at * kD + 4 * quad, v);
+  store_row<kF32, 4>(a.out, at * kD + 4 * quad, v);
 }
 
 template <int kD, bool kF32>
@@ -1215,8 +1254,8 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, in
   if (x < row_groups) {
     const int64_t bh = x / nz;
     join_items<kD, kF32>(a, bh / a.heads, (int)(bh % a.heads), (int)(x % nz), nz);
-  } else if constexpr (!kF32) {
-    join_wide<kD>(a, x - row_groups);
+  } else if constexpr (wide_takes(kD, !kF32)) {
+    join_wide<kD, kF32>(a, x - row_groups);
   }
 }
 
@@ -1233,7 +1272,7 @@ bool may_split(int64_t width, int shift) { return (width << shift) > (int64_t)kM
 // How a call is laid out; the workspace query and the launch agree on it.
 struct Plan {
   bool wide;
-  int part_rows;       // most rows of a request for the row kernel's splits
+  int part_rows;       // most rows of a request that the row kernel splits
   int64_t items;       // of the row kernel (0: nothing can be split)
   int wide_splits;
   size_t part_o, part_ml, wide_o, wide_ml, bytes;   // floats before each part, and all bytes
@@ -1247,8 +1286,8 @@ int64_t wide_tiles(int64_t q_rows, int64_t batch, int64_t group) {
 Plan plan_of(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_t max_rows, int64_t width,
              int shift, int head_dim, bool bf16) {
   Plan p{};
-  p.wide = bf16 && max_rows > kTile;
-  const int64_t most = bf16 ? kTile : kMaxPartRows;
+  p.wide = max_rows > kTile && wide_takes(head_dim, bf16);
+  const int64_t most = p.wide ? kTile : kMaxPartRows;
   p.part_rows = (int)((max_rows < most ? max_rows + kTile - 1 : most) / kTile * kTile);
   p.items = may_split(width, shift) ? most_items(batch, heads, width, shift) : 0;
   p.wide_splits = 1;
@@ -1269,10 +1308,10 @@ Plan plan_of(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_
 template <int kD, bool kF32, bool kWholePages>
 void run_parts(const AttendArgs& a, const Plan& p, int64_t max_rows, hipStream_t st) {
   const int64_t items = p.items ? p.items : a.batch;
-  if constexpr (!kF32) {
+  if constexpr (wide_takes(kD, !kF32)) {
     if (p.wide) {
       const int64_t wide_groups = wide_tiles(a.q_rows, a.batch, a.group) * p.wide_splits * a.heads;
-      hipLaunchKernelGGL((k_attend_both<kD, kWholePages>), dim3((unsigned)(wide_groups + items * a.heads)),
+      hipLaunchKernelGGL((k_attend_both<kD, kF32, kWholePages>), dim3((unsigned)(wide_groups + items * a.heads)),
                          dim3(kThreads), 0, st, a, wide_groups);
       return;
     }

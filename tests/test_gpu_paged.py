@@ -267,7 +267,8 @@ def test_attend_ragged_queries(dtype, causal, hint):
 
 
 @pytest.mark.parametrize("dtype,dim,heads,group,page", [
-    (BF, 128, 2, 4, 64), (BF, 64, 3, 1, 16), (BF, 256, 1, 2, 32), (F32, 128, 1, 2, 64), (BF, 192, 1, 4, 128)])
+    (BF, 128, 2, 4, 64), (BF, 64, 3, 1, 16), (BF, 256, 1, 2, 32), (F32, 128, 1, 2, 64), (BF, 192, 1, 4, 128),
+    (F32, 64, 2, 3, 128), (F32, 128, 1, 4, 16), (F32, 256, 1, 2, 32), (F32, 192, 1, 2, 64), (BF, 256, 1, 8, 256)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_attend_prompts(dtype, dim, heads, group, page, causal):
     rng = np.random.default_rng(12)
@@ -278,6 +279,30 @@ def test_attend_prompts(dtype, dim, heads, group, page, causal):
 def test_attend_splits_long_requests(dtype):
     rng = np.random.default_rng(13)
     check_attend(rng, [1, 1, 1, 6], [9001, 40, 300, 5000], 2, 4, 128, 64, dtype, spare=5)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF, 128), (F32, 128), (BF, 256), (F32, 64), (F32, 256)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_attend_splits_long_prompts(dtype, dim, page):
+    """A few rows over many tokens: tiles cut along the tokens, and more units than
+    are looked up at a time (64)."""
+    rng = np.random.default_rng(23)
+    check_attend(rng, [20, 3, 70], [5000, 4500, 4200], 1, 2, dim, page, dtype)
+    check_attend(rng, [33], [9000], 1, 1, dim, page, dtype, causal=False, spare=3)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_attend_with_a_wrong_hint_over_many_tokens(page):
+    """More rows than the hint allows are not cut: a wave walks over 64 units of its own."""
+    rng = np.random.default_rng(25)
+    check_attend(rng, [20, 1], [17000, 70], 1, 1, 64, page, BF, hint=1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attend_of_one_long_row_tile(dtype):
+    """Enough heads that nothing is cut: one workgroup walks 150 units."""
+    rng = np.random.default_rng(24)
+    check_attend(rng, [130] * 10, [9600] + [140] * 9, 16, 1, 64, 64, dtype)
 
 
 def test_attend_of_many_requests():

@@ -409,12 +409,16 @@ pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, in
  * not seen.
  * max_q_len: a hint, the most query tokens of one request (0: unknown).  It
  * decides workspace and launch shapes; results hold whatever it is.
- * Numbers: float32 sums, maxima and outputs before one rounding to `dtype`;
- * q . k exact products (float32 q in three bf16 parts); p rounded to 11 bits
- * relative to its value down to 2^-23 of the largest (22 bits for float32 q).
+ * Numbers: float32 sums, maxima and outputs before one rounding to `dtype`.
+ * q . k takes exact products of q: float32 q in three bf16 parts; bf16 q as it
+ * is, but for more than 16 rows of a request and KV head, where it is exact down
+ * to 2^-14 of the row's largest |q| and within 2^-23 of that below.  p is rounded
+ * to 11 bits relative to its value down to 2^-23 of the largest (22 bits for
+ * float32 q).  q, q . k and scale * (q . k) must be finite in float32; a row that
+ * breaks this spoils no other row.
  * Shape rules: q_heads a multiple of heads; q_rows * q_heads < 2^30;
  * table_width * page_size < 2^31 - 256; batch * heads < 2^21; q_stride in
- * [q_heads * head_dim, 2^40).  scale: finite and >= 0 (else PQB_ERR_VALUE).  Workspace:
+ * [q_heads * head_dim, 2^40).  scale in [0, 2^127] (else PQB_ERR_VALUE).  Workspace:
  * pqb_kv_attend_workspace_bytes(), its contents on entry do not matter; calls
  * that overlap in time need one each.  Alignment: q, out and workspace 16 bytes,
  * q_stride a multiple of 16 bytes, the int arrays 4.  Errors, before any launch:

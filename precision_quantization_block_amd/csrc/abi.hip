@@ -781,7 +781,7 @@ pqb_status pqb_kv_attend_paged(const void* q, pqb_dtype dtype, int64_t q_rows, i
   if (!attend_dims_ok(q_rows, q_heads, cache->heads, cache->head_dim, batch, table_width, shift))
     return PQB_ERR_SHAPE;
   if (q_stride < q_heads * cache->head_dim || q_stride >= kPagedMaxStride) return PQB_ERR_SHAPE;
-  if (!(scale >= 0.0f) || scale > 3.0e38f) return PQB_ERR_VALUE;
+  if (!(scale >= 0.0f && scale <= 0x1p127f)) return PQB_ERR_VALUE;  // times log2(e) still finite
   if (q_rows == 0 || batch == 0) return PQB_OK;
   if (!q || !out || !q_starts || !kv_lens || (table_width > 0 && !block_table)) return PQB_ERR_NULL;
   const int64_t es = dtype == PQB_BF16 ? 2 : 4;

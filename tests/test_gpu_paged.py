@@ -379,6 +379,24 @@ def test_attend_repeats_bit_for_bit(new, kv):
         assert torch.equal(pqb.kv_attend_paged(*args, workspace=ws), first)
 
 
+@pytest.mark.parametrize("dtype,dim", [(BF, 64), (BF, 128), (F32, 64), (F32, 256)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_a_row_that_is_not_finite_spoils_no_other(dtype, dim, page):
+    rng = np.random.default_rng(dim + page)
+    new, kv, bad = [3, 50, 1], [100, 650, 9], [(1, 1), (10, 0), (40, 3), (53, 2)]
+    table, pages = tiles(rng, [-(-n // page) for n in kv], 50)
+    cache, host = filled(rng, pages, 2, page, dim)
+    starts = np.concatenate([[0], np.cumsum(new)])
+    q = torch.from_numpy(rng.standard_normal((sum(new), 4, dim)) * 1.5).to(dtype)
+    want, bound = paged.attend(q.double().numpy(), *host, table, starts, kv, True, 1 / np.sqrt(dim), dtype == F32)
+    for (t, g), x in zip(bad, (float("nan"), float("inf"), float("-inf"), float("nan"))):
+        q[t, g, 5:9] = x
+    got = pqb.kv_attend_paged(q.to(DEV), cache, ints(table), ints(starts), ints(kv)).double().cpu().numpy()
+    keep = np.ones(got.shape[:2], bool)
+    keep[tuple(zip(*bad))] = False
+    assert (np.abs(got - want) <= bound)[keep].all()
+
+
 def test_offsets_past_32_bits():
     """Pages whose codes lie beyond 2^32 bytes: append, then attend, at both ends of the cache."""
     heads, page, dim = 8, 256, 256

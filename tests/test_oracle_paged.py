@@ -142,6 +142,13 @@ def test_attend_refuses(kw, cache, status):
         d["kv"], d["batch"], 1, d["scale"], 0, d["out"], d["ws"], d["wsb"], None) == status
 
 
+@pytest.mark.parametrize("scale,status", [(2.0 ** 127, 0), (2.5e38, -9), (3e38, -9), (3.4e38, -9), (0.0, 0)])
+def test_scale_stays_finite_in_powers_of_two(scale, status):
+    """scale * log2(e) is what the kernels multiply by."""
+    assert pqb.lib().pqb_kv_attend_paged(FAKE, 1, 0, 2, 128, pages(), FAKE, 1, FAKE, FAKE, 1, 1, scale, 0, FAKE, FAKE,
+                                         0, None) == status
+
+
 def test_null_cache_is_refused():
     L = pqb.lib()
     assert L.pqb_kv_append_paged(FAKE, FAKE, 1, 1, 128, 128, FAKE, None, None) == -1

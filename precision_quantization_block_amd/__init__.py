@@ -4,8 +4,8 @@ FP8 E4M3 and E5M2 (per tensor, per row, 1x128, 128x128), symmetric INT8 (per
 tensor, per row), MXFP4, MXFP8, NVFP4, INT4 group-128 asymmetric and the FP8
 KV-cache write (per layer, per head or static scale) and the KIVI-style
 2/4-bit KV cache (K per channel, V per token), a paged 8-bit KV cache (a
-scale per page and head) with its page planning, appends and attention, plus the block-scaled FP8
-GEMM that consumes 1x128 / 128x128 codes on the matrix cores, the MXFP4
+scale per page and head) with its page planning, appends and attention, plus
+the block-scaled FP8 GEMM that consumes 1x128 / 128x128 codes on the matrix cores, the MXFP4
 product, and the W4A16 product on INT4 codes (decode rows on the vector
 units, any number of rows on the matrix cores), as HIP kernels behind
 the C ABI in include/pqb.h.  The binding is loaded on first use so that the input

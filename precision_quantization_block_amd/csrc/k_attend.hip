@@ -12,7 +12,7 @@
 //
 // Numbers: a key is dec(c) 2^X, exact in bf16, times q's bf16 (float32 q is taken
 // as the exact sum of three bf16 parts).  The maximum, the sum and O are float32.
-// P is rounded to f16 as 2^15 p: 11 significant bits for every p >= 2^-29, three
+// The row kernel rounds P to f16 as 2^15 p: 11 significant bits for every p >= 2^-29, three
 // more than bf16 has, and below that to 2^-40 of the largest (float32 rows add
 // the rounding's remainder as a second f16 part).  V enters as dec(c) 2^(X - R),
 // exact in f16 unless X is over 15 below R, the largest V exponent met so far; O
@@ -613,6 +613,12 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 // sum of its 32 p of a unit passes 65000, so that no p passes f16's 65504.  Just
 // after a move that sum is 2^14 at most, however flat the row, so a move is rare;
 // 11 significant bits reach down to 2^-23 of the reference.
+//
+// Bound by the issue of vector and matrix instructions together: three units are
+// in the pipeline (O^T of one, P of the next, S^T of the one behind it), so that
+// the matrix core works under the exponentials and conversions.  Two prompts of
+// 4096 tokens (32 heads over 8, 128 wide, bf16): 271 us, 1.03 PFLOP/s, where the
+// library's bf16 product of 8192^3 reaches 1.19; one unit at a time took 330.
 // ---------------------------------------------------------------------------
 
 constexpr float kPExp = 9.0f;      // p is held times 2^9

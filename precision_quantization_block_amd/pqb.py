@@ -637,6 +637,8 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     of them (cross attention over an encoder's states, of any other length).
     scale: 1 / sqrt(head_dim) unless given.  max_q_len: the most query tokens
     of one request where the caller knows it (a hint for speed and workspace).
+    workspace: memory to use instead of an allocation per call (any contiguous
+    tensor of pqb_kv_attend_workspace_bytes; calls that overlap need one each).
     Rows outside every request are left as they were in `out`."""
     dev = _device_of(q, "q")
     c = _pages_struct(cache, dev)

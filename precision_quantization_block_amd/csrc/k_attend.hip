@@ -21,6 +21,7 @@
 
 #include "launch.h"
 #include "paged.h"
+#include "units.h"
 
 namespace pqb {
 namespace {
@@ -29,10 +30,8 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kUnit = 64;        // tokens a wave takes at a time
 constexpr int kTile = 16;        // query rows of a tile
-constexpr int kWaves = 4, kThreads = kWaves * kWave;
-constexpr int kMetaUnits = 64;   // units whose pages are looked up at a time
+constexpr int kWaves = kUnitWaves, kThreads = kWaves * kWave;
 constexpr int kMinUnits = 2 * kWaves;             // fewest units of a split
 constexpr int kMaxPartRows = 64;                  // rows of a request that the row kernel may split
 constexpr int64_t kGroupsWanted = 1536;           // workgroups a split aims at
@@ -347,8 +346,8 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, int64_t x, int 
     auto load_pages = [&](int u) {
 #pragma unroll
       for (int i = lane; i < kMetaUnits * kGroups; i += kWave) {
-        const int t = (u + i / kGroups * kWaves) * kUnit + 16 * (i % kGroups);
-        const int p = t < rq.kv ? table[t >> a.shift] : -1;
+        const int at = table_column(u + i / kGroups * kWaves, i % kGroups, rq.kv, a.shift);
+        const int p = at >= 0 ? table[at] : -1;
         pg[i] = (uint32_t)p < (uint64_t)a.pages ? p : -1;
       }
     };
@@ -726,7 +725,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   const int units = __builtin_amdgcn_readfirstlane(min(ws.units, u0 + ws.per));
   const int32_t* table = a.table + wt.b * a.width;
   const int64_t page_bytes = (int64_t)kD << a.shift;
-  const int ps1 = (1 << a.shift) - 1;
+  const uint32_t ps1 = (1u << a.shift) - 1;
 
   // q's loads go out first: they return under the page lookups and the first DMA.
   // This lane's 32 channels of each 64.
@@ -748,8 +747,8 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   auto meta_at = [&](int u, int group) { return (u & (2 * kMetaUnits - 1)) * kGroups + (kWholePages ? 0 : group); };
   auto load_pages = [&](int first) {
     for (int i = tid; i < kMetaUnits * kGroups; i += kThreads) {
-      const int u = first + i / kGroups, t = u * kUnit + 16 * (i % kGroups);
-      const int p = u < units && t < rq.kv ? table[t >> a.shift] : -1;
+      const int u = first + i / kGroups, at = table_column(u, i % kGroups, rq.kv, a.shift);
+      const int p = u < units && at >= 0 ? table[at] : -1;
       pg[meta_at(u, i % kGroups)] = (uint32_t)p < (uint64_t)a.pages ? p : -1;
     }
   };
@@ -782,12 +781,12 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   const uint32_t page_step = (uint32_t)(a.heads * page_bytes);   // at most 4096 heads of 64 KiB
   auto k_from = [&](int u) {
     const uint32_t p = (uint32_t)max(__builtin_amdgcn_readfirstlane(pg[meta_at(u, wave)]), 0);
-    return k_head + (uint64_t)p * page_step + (uint32_t)(((u * kUnit + 16 * wave) & ps1) * kD);
+    return k_head + (uint64_t)p * page_step + ((((uint32_t)u * kUnit + 16 * wave) & ps1) * kD);
   };
   auto v_from = [&](int u) {
     int p = pg[meta_at(u, vg)];
     if constexpr (kWholePages) p = __builtin_amdgcn_readfirstlane(p);
-    return v_head + (uint64_t)(uint32_t)max(p, 0) * page_step + ((u * kUnit + (kWholePages ? 0 : 16 * vg)) & ps1);
+    return v_head + (uint64_t)(uint32_t)max(p, 0) * page_step + (((uint32_t)u * kUnit + (kWholePages ? 0 : 16 * vg)) & ps1);
   };
   auto stage_k = [&](int u, const uint8_t* kp) {
 #pragma unroll

@@ -32,9 +32,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 16;        // query rows of a tile
 constexpr int kWaves = kUnitWaves, kThreads = kWaves * kWave;
-constexpr int kMinUnits = 2 * kWaves;             // fewest units of a split
 constexpr int kMaxPartRows = 64;                  // rows of a request that the row kernel may split
-constexpr int64_t kGroupsWanted = 1536;           // workgroups a split aims at
 constexpr int64_t kMaxGroups = 1 << 23;            // workgroups that splits or joins lead to
 constexpr int kMinWideUnits = 8;                  // the same for the wide kernel
 constexpr int64_t kMaxWideSplits = 32, kWideGroupsWanted = 512;
@@ -67,7 +65,7 @@ __device__ __forceinline__ int items_of(const AttendArgs& a, const Request& r, i
   const int64_t rows = (int64_t)r.n * a.group;
   if (rows == 0) return 0;
   if (rows > a.part_rows) return a.wide ? 0 : 1;  // the wide kernel's, or not cut
-  return max(1, (units_of(r.kv) + C - 1) / C);
+  return items_of_units(units_of(r.kv), C);
 }
 
 __device__ __forceinline__ int64_t wave_sum64(int64_t v) {
@@ -94,9 +92,7 @@ __device__ __forceinline__ int split_units(const AttendArgs& a, const Request& f
     const int64_t rows = (int64_t)r.n * a.group;
     if (rows > 0 && rows <= a.part_rows) total += units_of(r.kv);
   }
-  total = wave_sum64(total) * a.heads;
-  const int64_t c = (total + kGroupsWanted - 1) / kGroupsWanted;
-  return __builtin_amdgcn_readfirstlane((int)((max(c, (int64_t)kMinUnits) + kWaves - 1) / kWaves * kWaves));
+  return __builtin_amdgcn_readfirstlane(units_an_item(wave_sum64(total) * a.heads));
 }
 
 struct Item {
@@ -1262,14 +1258,6 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(const AttendArgs a, in
   } else if constexpr (wide_takes(kD, !kF32)) {
     join_wide<kD, kF32>(a, x - row_groups);
   }
-}
-
-// Items that the lengths can lead to: their number is bounded by what a split
-// aims at, and by the table's width.
-int64_t most_items(int64_t batch, int64_t heads, int64_t width, int shift) {
-  const int64_t wanted = (kGroupsWanted + heads - 1) / heads + batch;
-  const int64_t each = ((width << shift) + kMinUnits * kUnit - 1) / (kMinUnits * kUnit);
-  return each * batch < wanted ? each * batch : wanted;
 }
 
 bool may_split(int64_t width, int shift) { return (width << shift) > (int64_t)kMinUnits * kUnit; }

@@ -416,8 +416,8 @@ pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, in
  * to 11 bits relative to its value down to 2^-23 of the largest (22 bits for
  * float32 q).  v_j is exact, but for pages whose X is over 15 below the largest V
  * exponent R of the request's pages and head, where it is within 2^(R - 25).
- * q, q . k and scale * (q . k) must be finite in float32; a row that breaks this
- * spoils no other row.
+ * q, q . k and scale * log2(e) * (q . k) must be at most 2^126 in magnitude; a row
+ * that breaks this spoils no other row.
  * Shape rules: q_heads a multiple of heads; q_rows * q_heads < 2^30;
  * table_width * page_size < 2^31 - 256; batch * heads < 2^21; q_stride in
  * [q_heads * head_dim, 2^40).  scale in [0, 2^127] (else PQB_ERR_VALUE).  Workspace:

@@ -333,7 +333,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, int64_t x, int 
     // what this lane's row, the tile's first row and its last row see
     const int ahead = rq.kv - rq.n + 1;
     const int limit = !valid ? 0 : a.causal ? ahead + tok : rq.kv;
-    const int first_limit = a.causal ? ahead + rt * kTile / a.group : rq.kv;
+    const int first_limit = a.flat ? 0 : a.causal ? ahead + rt * kTile / a.group : rq.kv;
     const int last_limit = a.causal ? ahead + (min(rt * kTile + kTile, rows) - 1) / a.group : rq.kv;
     const int u0 = unit0 + wave;
     const int end = __builtin_amdgcn_readfirstlane(min(unit_end, last_limit > 0 ? units_of(last_limit) : 0));
@@ -450,7 +450,8 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, int64_t x, int 
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the key reads have returned
       if (more) stage_k(u + kWaves);
 
-      // Tokens outside the row's view, and tokens of a page id outside the cache.
+      // Tokens outside the row's view, and tokens of a page id outside the cache
+      // (first_limit 0: every unit, if scores are all 0).
       const bool whole = (u + 1) * kUnit <= first_limit && __ballot(!okv) == 0;
       uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
       if (!whole) {
@@ -458,8 +459,10 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, int64_t x, int 
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i) {
+            if (a.flat) s[t][i] = 0;
             if (4 * t + i >= cnt) s[t][i] = -INFINITY;
+          }
         // codes behind the last token may be anything (NaN times p = 0 is NaN)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -712,7 +715,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   const int tok = row / a.group;
   const int ahead = rq.kv - rq.n + 1;
   const int limit = a.causal && valid ? ahead + tok : rq.kv;
-  const int first_limit = a.causal ? ahead + row0 / a.group : rq.kv;
+  const int first_limit = a.flat ? 0 : a.causal ? ahead + row0 / a.group : rq.kv;
   const int wave_end = row0 >= rows ? 0 : a.causal ? ahead + (min(row0 + kWideRows, rows) - 1) / a.group : rq.kv;
   const int tile_end = a.causal ? ahead + (min((wt.tile + 1) * kWideTile, rows) - 1) / a.group : rq.kv;
   const WideSplit ws = wide_split(a, tile_end);
@@ -944,15 +947,17 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
     }
     return c;
   };
-  // -inf for what unit u's rows do not see
+  // -inf for what unit u's rows do not see (all of them pass here if scores are all 0)
   auto mask = [&](int u, int lo, f32x16* s) {
     if (lo < 0 || (u + 1) * kUnit > first_limit) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int g = 2 * half + t, cnt = pg[meta_at(u, g)] < 0 ? 0 : limit - (u * kUnit + 16 * g);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 16; ++j) {
+          if (a.flat) s[t][j] = 0;
           if (j >= cnt) s[t][j] = -INFINITY;
+        }
       }
     }
   };
@@ -1366,9 +1371,12 @@ hipError_t launch_attend(AttendArgs a, bool bf16, int head_dim, int64_t max_rows
   a.wide_splits = p.wide_splits;
   a.wide_o = ws + p.wide_o;
   a.wide_ml = ws + p.wide_ml;
-  // scale 0 (all tokens alike) as a scale too small to matter, so that a masked
-  // -inf stays -inf through the product
-  if (a.c < 1e-37f) a.c = 1e-37f;
+  // Scale 0: all scores 0, set before the mask, whose -inf has to stay -inf through the
+  // product.
+  if (a.c == 0) {
+    a.flat = 1;
+    a.c = 1;
+  }
   return bf16 ? run_d<false>(a, p, head_dim, max_rows, st) : run_d<true>(a, p, head_dim, max_rows, st);
 }
 

@@ -232,6 +232,7 @@ struct AttendArgs {
   int32_t part_rows;                          // rows of a request that may be split
   int32_t wide;                               // requests of more rows go to the wide kernel
   int32_t wide_splits;
+  int flat;                                   // scale 0: every token that is seen counts alike
 };
 // The workspace for at most max_rows = max_q_len * group rows per request.
 size_t attend_workspace_bytes(int64_t q_rows, int64_t batch, int64_t heads, int64_t group, int64_t max_rows,

@@ -6,7 +6,7 @@ import torch
 
 import precision_quantization_block_amd as pqb
 from oracle import paged
-from test_gpu_paged import BF, DEV, F32, filled, ints
+from test_gpu_paged import BF, DEV, F32, check_attend, filled, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +26,14 @@ def test_attend_at_the_largest_length(dtype):
     got = pqb.kv_attend_paged(q.to(DEV), cache, table, ints([0, 1]), ints([width * page]), scale=8.0)
     want, bound = paged.attend(q.double().numpy(), *host, np.array([[1]]), [0, 1], [page], True, 8.0, dtype == F32)
     assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("new,kv", [([1, 2, 1], [100, 90, 3000]), ([70, 1, 33], [100, 90, 3000])])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -124, 2.0 ** -127, 2.0 ** -140])
+def test_attend_scales_next_to_zero(dtype, new, kv, scale):
+    """Products q.k of about 2^121, up to the largest allowed: scale 0 makes all tokens
+    alike, and the smallest normal and subnormal scales leave them apart."""
+    rng = np.random.default_rng(27)
+    for page in (16, 64):
+        check_attend(rng, new, kv, 2, 2, 64, page, dtype, scale=scale, qscale=1.5 * 2.0 ** 112, lo=127, hi=127)

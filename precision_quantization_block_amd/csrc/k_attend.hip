@@ -204,6 +204,22 @@ __device__ __forceinline__ void store_row(void* out, int64_t at, const float* o)
   }
 }
 
+// What a part of a row counts beside one with the maximum M.
+__device__ __forceinline__ float part_weight(float m, float M, float c) {
+  return m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - M) * c);
+}
+
+// Sums of p v in units of 2^R (biased), and l of p, to averages.  A part keeps its
+// average and its l: the sum of p v may pass float32's range where no average does, and
+// 2^R / l its smallest normal.  (l holds the p of the row's reference, 1 times 2^9 or
+// 2^15, and of at most 2^31 tokens more: well inside recip_rn's range.)
+template <int kN>
+__device__ __forceinline__ void average(float* o, float l, int R) {
+  const float inv = l > 0 ? recip_rn(l) : 0.0f, unit = as_f((uint32_t)R << 23);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) o[i] = o[i] * inv * unit;
+}
+
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
 }
@@ -243,6 +259,17 @@ __device__ __forceinline__ float swap_sum(float x) {
   return as_f(r[0]) + as_f(r[1]);
 }
 
+// Over the whole wave, in one order whatever the lane.
+template <typename F>
+__device__ __forceinline__ float wave_fold(float x, F f) {
+  x = f(x, as_f(dpp<kDppXor1>(as_u(x))));
+  x = f(x, as_f(dpp<kDppXor2>(as_u(x))));
+  x = f(x, as_f(dpp<kDppHalfMirror>(as_u(x))));
+  x = f(x, as_f(dpp<kDppMirror>(as_u(x))));
+  x = f(x, __shfl_xor(x, 16));
+  return f(x, __shfl_xor(x, 32));
+}
+
 // ---------------------------------------------------------------------------
 // Few query rows: single tokens, 16 rows a tile.
 // Bound by the bytes of the cache.
@@ -278,6 +305,7 @@ struct RowsLds {
     float o[kWaves][kTile][kD + 4];
   };
   float m[kWaves][kTile], l[kWaves][kTile];
+  int R[kWaves];
   // page (-1: none) and scales (K's byte, V's << 8) of a wave's next units
   int pg[kWaves][kMetaUnits * kGroups], xs[kWaves][kMetaUnits * kGroups];
 };
@@ -538,36 +566,39 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, int64_t x, int 
 
     l += __shfl_xor(l, 16);
     l = swap_sum(l);
-    const float unit = as_f((uint32_t)R << 23) * 0x1p-15f;  // O and l in units of 1 from here on
     __syncthreads();  // every wave is done with its K and V, whose LDS O takes
 #pragma unroll
-    for (int i = 0; i < kDT; ++i)
-      *reinterpret_cast<f32x4*>(&lds.o[wave][col][16 * i + 4 * g4]) = o[i] * unit;
+    for (int i = 0; i < kDT; ++i) *reinterpret_cast<f32x4*>(&lds.o[wave][col][16 * i + 4 * g4]) = o[i];
     if (g4 == 0) {
       lds.m[wave][col] = m;
-      lds.l[wave][col] = l * 0x1p-15f;
+      lds.l[wave][col] = l;
     }
+    if (lane == 0) lds.R[wave] = R;
     __syncthreads();
     // 16 threads a row, kD / 16 channels each
     const int r = tid / 16, d0 = (tid % 16) * (kD / 16), grow_row = rt * kTile + r;
     if (grow_row < rows) {
       float M = lds.m[0][r];
+      int top = lds.R[0];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) M = fmaxf(M, lds.m[w][r]);
+      for (int w = 1; w < kWaves; ++w) {
+        M = fmaxf(M, lds.m[w][r]);
+        top = max(top, lds.R[w]);
+      }
       float L = 0, acc[kD / 16];
 #pragma unroll
       for (int j = 0; j < kD / 16; ++j) acc[j] = 0;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float mw = lds.m[w][r], wt = mw == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mw - M) * a.c);
+        const float wt = part_weight(lds.m[w][r], M, a.c);
+        const int down = top - lds.R[w];
+        const float wo = down > 126 ? 0.0f : wt * as_f((uint32_t)(127 - down) << 23);
         L += lds.l[w][r] * wt;
 #pragma unroll
-        for (int j = 0; j < kD / 16; ++j) acc[j] += lds.o[w][r][d0 + j] * wt;
+        for (int j = 0; j < kD / 16; ++j) acc[j] += lds.o[w][r][d0 + j] * wo;
       }
+      average<kD / 16>(acc, L, top);
       if (it.count == 1) {
-        const float inv = L > 0 ? 1.0f / L : 0.0f;
-#pragma unroll
-        for (int j = 0; j < kD / 16; ++j) acc[j] *= inv;
         store_row<kF32, kD / 16>(a.out, ((int64_t)(rq.start + grow_row / a.group) * a.heads * a.group +
                                          h * a.group + grow_row % a.group) * kD + d0, acc);
       } else {
@@ -1098,27 +1129,21 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   if (!valid) return;
   l = swap_sum(l);
   const int64_t out_row = (int64_t)(rq.start + tok) * a.heads * a.group + h * a.group + row % a.group;
-  if (ws.count == 1) {
-    const float scale = l > 0 ? as_f((uint32_t)R << 23) / l : 0.0f;
+  const bool whole = ws.count == 1;
+  const int64_t slot = whole ? out_row : (int64_t)split * a.q_rows * a.heads * a.group + out_row;
 #pragma unroll
-    for (int i = 0; i < kDT; ++i)
+  for (int i = 0; i < kDT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v[4] = {o[i][4 * j] * scale, o[i][4 * j + 1] * scale, o[i][4 * j + 2] * scale,
-                            o[i][4 * j + 3] * scale};
-        store_row<kF32, 4>(a.out, out_row * kD + 4 * half + 32 * i + 8 * j, v);
-      }
-  } else {
-    const int64_t slot = (int64_t)split * a.q_rows * a.heads * a.group + out_row;
-    const float scale = as_f((uint32_t)R << 23) * 0x1p-9f;
-#pragma unroll
-    for (int i = 0; i < kDT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v[4] = {o[i][4 * j] * scale, o[i][4 * j + 1] * scale, o[i][4 * j + 2] * scale,
-                            o[i][4 * j + 3] * scale};
-        store_row<true, 4>(a.wide_o, slot * kD + 4 * half + 32 * i + 8 * j, v);
-      }
+    for (int j = 0; j < 4; ++j) {
+      float v[4] = {o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+      average<4>(v, l, R);
+      const int64_t at = slot * kD + 4 * half + 32 * i + 8 * j;
+      if (whole)
+        store_row<kF32, 4>(a.out, at, v);
+      else
+        store_row<true, 4>(a.wide_o, at, v);
+    }
+  if (!whole) {
     if (half == 0) {
       a.wide_ml[2 * slot] = m == -INFINITY ? m : kPExp - r;   // the reference that O and l have, in powers of 2
       a.wide_ml[2 * slot + 1] = l * 0x1p-9f;
@@ -1154,7 +1179,7 @@ __global__ __launch_bounds__(kThreads, kD <= 128 && !kF32 ? 2 : 1) void k_attend
 template <int kD, bool kF32>
 __device__ __forceinline__ void join_items(const AttendArgs& a, int64_t b, int h, int z, int nz) {
   constexpr int kQuads = kD / 4, kGroups = kThreads / kQuads;
-  __shared__ float red_m[kWaves], red_l[kGroups];
+  __shared__ float red_m[kWaves], red_l[kWaves];
   __shared__ f32x4 red_o[kGroups][kQuads];
   const Request first = lane_request(a, 0);
   const Item it = find_item<true>(a, b, split_units(a, first), first);
@@ -1165,36 +1190,42 @@ __device__ __forceinline__ void join_items(const AttendArgs& a, int64_t b, int h
   const int64_t step = (int64_t)a.heads * a.part_rows;
   for (int row = z; row < rows; row += nz) {
     const int64_t slot0 = (it.first * a.heads + h) * a.part_rows + row;
-    float M = -INFINITY;
-    for (int i = tid; i < it.count; i += kThreads) M = fmaxf(M, a.part_ml[2 * (slot0 + i * step)]);
-#pragma unroll
-    for (int d = kWave / 2; d; d >>= 1) M = fmaxf(M, __shfl_xor(M, d));
+    float M = -INFINITY, L = 0;
+    for (int i = tid; i < it.count; i += kThreads) {
+      const int64_t slot = slot0 + i * step;
+      const float mi = a.part_ml[2 * slot], top = fmaxf(M, mi);
+      L = L * part_weight(M, top, a.c) + a.part_ml[2 * slot + 1] * part_weight(mi, top, a.c);
+      M = top;
+    }
+    const float mine = M;
+    M = wave_fold(M, [](float x, float y) { return fmaxf(x, y); });
+    L = wave_fold(L * part_weight(mine, M, a.c), [](float x, float y) { return x + y; });
     __syncthreads();  // the last row's reads of LDS are done
-    if (lane == 0) red_m[tid / kWave] = M;
+    if (lane == 0) {
+      red_m[tid / kWave] = M;
+      red_l[tid / kWave] = L;
+    }
     __syncthreads();
+    L = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) M = fmaxf(M, red_m[w]);
-    float L = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) L += red_l[w] * part_weight(red_m[w], M, a.c);
+    const float inv = L > 0 ? recip_rn(L) : 0.0f;
     f32x4 acc = {0, 0, 0, 0};
     if (grp < kGroups) {
       for (int i = grp; i < it.count; i += kGroups) {
         const int64_t slot = slot0 + i * step;
-        const float mi = a.part_ml[2 * slot], wt = mi == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((mi - M) * a.c);
-        L += a.part_ml[2 * slot + 1] * wt;
+        const float wt = a.part_ml[2 * slot + 1] * inv * part_weight(a.part_ml[2 * slot], M, a.c);
         acc += *reinterpret_cast<const f32x4*>(a.part_o + slot * kD + 4 * quad) * wt;
       }
       red_o[grp][quad] = acc;
-      if (quad == 0) red_l[grp] = L;
     }
     __syncthreads();
     if (grp == 0) {
 #pragma unroll
-      for (int g = 1; g < kGroups; ++g) {
-        acc += red_o[g][quad];
-        L += red_l[g];
-      }
-      const float inv = L > 0 ? 1.0f / L : 0.0f;
-      const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+      for (int g = 1; g < kGroups; ++g) acc += red_o[g][quad];
+      const float v[4] = {acc[0], acc[1], acc[2], acc[3]};
       store_row<kF32, 4>(a.out, ((int64_t)(rq.start + row / a.group) * a.heads * a.group + h * a.group +
                                  row % a.group) * kD + 4 * quad, v);
     }
@@ -1238,19 +1269,21 @@ __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t group) {
       oi[k] = *reinterpret_cast<const f32x4*>(a.wide_o + slot * kD + 4 * quad);
     }
     const float top = fmaxf(M, fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])));
-    const float keep = M == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(M - top);
-    L *= keep;
-    acc *= keep;
+    // the average so far, and the parts', by their shares of p
+    const float keep = L * part_weight(M, top, 1.0f);
+    L = keep;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float wt = mi[k] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi[k] - top);
-      L += li[k] * wt;
-      acc += oi[k] * wt;
+      li[k] *= part_weight(mi[k], top, 1.0f);
+      L += li[k];
     }
+    const float inv = L > 0 ? recip_rn(L) : 0.0f;
+    acc *= keep * inv;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc += oi[k] * (li[k] * inv);
     M = top;
   }
-  const float inv = L > 0 ? 1.0f / L : 0.0f;
-  const float v[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+  const float v[4] = {acc[0], acc[1], acc[2], acc[3]};
   store_row<kF32, 4>(a.out, at * kD + 4 * quad, v);
 }
 

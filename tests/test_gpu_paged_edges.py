@@ -6,7 +6,7 @@ import torch
 
 import precision_quantization_block_amd as pqb
 from oracle import paged
-from test_gpu_paged import BF, DEV, F32, check_attend, filled, ints
+from test_gpu_paged import BF, DEV, F32, check_attend, filled, ints, tiles
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,31 @@ def test_attend_scales_next_to_zero(dtype, new, kv, scale):
     rng = np.random.default_rng(27)
     for page in (16, 64):
         check_attend(rng, new, kv, 2, 2, 64, page, dtype, scale=scale, qscale=1.5 * 2.0 ** 112, lo=127, hi=127)
+
+
+def check_values(rng, new, kv, heads, group, dim, page, dtype, v_scale, **more):
+    """Attention over positive V of one page exponent (its byte v_scale), within the oracle's bound."""
+    counts = [-(-n // page) for n in kv]
+    table, pages = tiles(rng, counts, max(counts))
+    cache, host = filled(rng, pages, heads, page, dim)
+    cache.v_codes &= 0x7F
+    cache.v_scales.fill_(v_scale)
+    host[1][:], host[3][:] = host[1] & 0x7F, v_scale
+    starts = np.concatenate([[0], np.cumsum(new)])
+    q = torch.from_numpy(rng.standard_normal((int(starts[-1]), heads * group, dim))).to(dtype)
+    got = pqb.kv_attend_paged(q.to(DEV), cache, ints(table), ints(starts), ints(kv), max_q_len=max(new), **more)
+    want, bound = paged.attend(q.double().numpy(), *host, table, starts, kv, True, dim ** -0.5, dtype == F32)
+    assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF, 64), (BF, 128), (F32, 64), (F32, 256)])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("v_scale", [246, 1])
+def test_attend_values_at_the_ends_of_float32(dtype, dim, page, v_scale):
+    """V of up to 448 * 2^119 = 2.98e38, whose sums pass float32, and of down to 2^-126,
+    for which 2^X / l is no normal number: both kernels, whole and split."""
+    rng = np.random.default_rng(28)
+    check_values(rng, [1, 2, 1], [100, 333, 3], 2, 2, dim, page, dtype, v_scale)
+    check_values(rng, [1, 1], [5000, 700], 1, 2, dim, page, dtype, v_scale)
+    check_values(rng, [40, 1, 200], [100, 333, 200], 2, 2, dim, page, dtype, v_scale)
+    check_values(rng, [20, 33, 1], [5000, 2100, 3000], 1, 2, dim, page, dtype, v_scale)

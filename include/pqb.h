@@ -410,11 +410,9 @@ pqb_status pqb_kv_append_paged(const void* k, const void* v, pqb_dtype dtype, in
  * max_q_len: a hint, the most query tokens of one request (0: unknown).  It
  * decides workspace and launch shapes; results hold whatever it is.
  * Numbers: float32 sums, maxima and outputs before one rounding to `dtype`.
- * q . k takes exact products of q: float32 q in three bf16 parts; bf16 q as it
- * is, but for more than 16 rows of a request and KV head, where it is exact down
- * to 2^-14 of the row's largest |q| and within 2^-23 of that below.  p is rounded
- * to 11 bits relative to its value down to 2^-23 of the largest (22 bits for
- * float32 q).  v_j is exact, but for pages whose X is over 15 below the largest V
+ * q . k takes exact products: a key is exact in bf16, and so is bf16 q; float32 q
+ * enters as three bf16 parts.  p is rounded to 11 bits relative to its value down
+ * to 2^-23 of the largest (22 bits for float32 q).  v_j is exact, but for pages whose X is over 15 below the largest V
  * exponent R of the request's pages and head, where it is within 2^(R - 25).
  * q, q . k and scale * log2(e) * (q . k) must be at most 2^126 in magnitude; a row
  * that breaks this spoils no other row.

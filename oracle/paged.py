@@ -104,8 +104,6 @@ def attend(q, k_codes, v_codes, k_scales, v_scales, table, starts, kv_lens, caus
         float32 q), so |ds| <= (3 D + 8) 2^-24 scale sum |k||q|; the exponent's
         argument is rounded twice more, 3 |s - max| 2^-24, and exp2 is within
         2^-22; p moves by at most that factor, above and below the line: 2 ds A;
-        a bf16 q may be taken as two E4M3 parts, each value within 2^-23 of the
-        row's largest |q|, so 2^-22 max |q| sum |k| scale more;
       p rounded to f16, 2^-11 of itself (float32: remainder kept, 2^-22), and
         2^-34 of the largest below 2^-23; V to 2^-25 of its request's largest
         scale;
@@ -145,8 +143,6 @@ def attend(q, k_codes, v_codes, k_scales, v_scales, table, starts, kv_lens, caus
                 o = p @ v / safe
                 u = 2.0 ** -24
                 mag = np.abs(x) @ np.abs(k).T * scale
-                if not f32:
-                    mag = mag + 4.0 / (3 * D + 8) * np.abs(x).max(1, keepdims=True) * np.abs(k).sum(1) * scale
                 ds = (3 * D + 8) * u * mag + 3 * u * np.where(see, np.where(np.isinf(big), 0, big) - np.where(see, s, 0), 0) + 2.0 ** -22
                 ds = np.expm1(np.where(see, ds, 0))
                 A = p @ np.abs(v) / safe

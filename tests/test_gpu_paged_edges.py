@@ -65,3 +65,47 @@ def test_attend_values_at_the_ends_of_float32(dtype, dim, page, v_scale):
     check_values(rng, [1, 1], [5000, 700], 1, 2, dim, page, dtype, v_scale)
     check_values(rng, [40, 1, 200], [100, 333, 200], 2, 2, dim, page, dtype, v_scale)
     check_values(rng, [20, 33, 1], [5000, 2100, 3000], 1, 2, dim, page, dtype, v_scale)
+
+
+def check_whole_scores(dtype, dim, page, base, unit, new, kv):
+    """Scores unit * (base + a whole number up to 189), exact in float32 and equal for many
+    tokens: with unit 1 their differences count, far beyond it the largest of a row alone.
+    So, with A = sum p |v| / sum p: p is off by 2^-22 (exp2) and by the rounding of an
+    exponent that counts (under 64: 2^-18 and half that from log2(e)); f16 by 2^-11
+    (float32: 2^-22); sums by (2 n + 64) 2^-24."""
+    rng = np.random.default_rng(29)
+    heads, group = 1, 2
+    table, pages = tiles(rng, [-(-n // page) for n in kv], -(-max(kv) // page))
+    cache, host = filled(rng, pages, heads, page, dim)
+    k = np.zeros((pages, heads, page, dim))
+    k[..., 0] = 2.0 ** 8 if base else 0
+    k[..., 1:22] = rng.integers(0, 4, k[..., 1:22].shape)      # q of 0 .. 3 against them: up to 189
+    codes = torch.from_numpy(k).to(torch.float8_e4m3fn).view(torch.uint8)
+    cache.k_codes.copy_(codes)
+    cache.k_scales.fill_(127)
+    host[0][:], host[2][:] = codes.numpy(), 127
+    starts = np.concatenate([[0], np.cumsum(new)])
+    q = np.zeros((int(starts[-1]), heads * group, dim))
+    q[..., 0] = base / 2.0 ** 8
+    q[..., 1:22] = rng.integers(0, 4, q[..., 1:22].shape)
+    qt = torch.from_numpy(q * unit).to(dtype)
+    got = pqb.kv_attend_paged(qt.to(DEV), cache, ints(table), ints(starts), ints(kv), scale=1.0, max_q_len=max(new))
+    got = got.double().cpu().numpy()
+    want, _ = paged.attend(qt.double().numpy(), *host, table, starts, kv, True, 1.0, dtype == F32)
+    host[1] &= 0x7F
+    A, _ = paged.attend(qt.double().numpy(), *host, table, starts, kv, True, 1.0, dtype == F32)
+    tol = A * (2.0 ** -17 + (2.0 ** -22 if dtype == F32 else 2.0 ** -11) + (2 * max(kv) + 64) * 2.0 ** -24)
+    tol += (2.0 ** -24 if dtype == F32 else 2.0 ** -8) * (np.abs(want) + tol)
+    assert not np.isnan(got).any() and (np.abs(got - want) <= tol).all()
+
+
+FEW, MANY, LONG = ([1, 3, 1], [100, 333, 2600]), ([40, 1, 200], [100, 70, 200]), ([20, 33, 2], [2500, 1100, 600])
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF, 64), (BF, 128), (BF, 192), (BF, 256), (F32, 64), (F32, 128), (F32, 256)])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("base", [2.0 ** 9, 2.0 ** 12, 2.0 ** 15])
+@pytest.mark.parametrize("new,kv", [FEW, MANY, LONG])
+def test_attend_where_one_channel_stands_out(dtype, dim, page, base, new, kv):
+    """One product of the sum q.k is up to 2^15 times the others, which alone tell the tokens apart."""
+    check_whole_scores(dtype, dim, page, base, 1.0, new, kv)

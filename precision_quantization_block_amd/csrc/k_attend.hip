@@ -650,6 +650,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 // ---------------------------------------------------------------------------
 
 constexpr float kPExp = 9.0f;      // p is held times 2^9
+constexpr float kFar = 0x1p20f;   // |r| up to here is right to 2^-5
 constexpr int kStages = 4;        // units in LDS at a time
 constexpr int kWideRows = 32, kWideTile = kWaves * kWideRows;
 
@@ -857,7 +858,11 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   const float c = a.c;
   // m: the row's reference (the maximum when it was last moved), r = 9 - m c; O
   // and l hold 2^9 p' relative to it.  r starts infinite: the first unit moves it.
+  // It is rounded, so exactly they hold 2^e p', e = m c + r.  Where m c passes kFar and
+  // that is no longer close to 9, r stays infinite: every unit then settles its row anew,
+  // from s - m and with e = 9.
   float m = -INFINITY, r = INFINITY, l = 0;
+  auto held_exp = [&](float m, float r) { return r == INFINITY ? kPExp : __builtin_fmaf(m, c, r); };
   int R = 1;
   f32x16 o[kDT];
 #pragma unroll
@@ -945,7 +950,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
   // No maximum is taken while P fits f16: what does not, or the first unit's
   // infinite r, shows in the sum.  Then the reference moves to the maximum, and O
   // and l with it; and to a larger V exponent.
-  auto settle = [&](int xr, const f32x16* s, const f32x16* later, Weights& pw, float sum) {
+  auto settle = [&](int xr, f32x16* s, const f32x16* later, Weights& pw, float sum) {
     if (__ballot(!(sum <= 65000.0f)) || xr > R) {
       asm volatile("" ::"v"(later[0]), "v"(later[1]));   // keeps their products above this branch
       float mx = s[0][0];
@@ -956,7 +961,11 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
       const float m_new = fmaxf(m, swap_max(mx));
       const bool none = m_new == -INFINITY;
       const float r_new = none ? kPExp : __builtin_fmaf(-m_new, c, kPExp);
-      const float alpha = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(r_new - r);
+      const bool far = fabsf(r_new) > kFar;
+      const float at = far ? kPExp : r_new, off = far ? m_new : 0.0f;
+      const float held = far ? kPExp : __builtin_fmaf(m_new, c, r_new);
+      const float alpha =
+          m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(m - m_new, c, held - held_exp(m, r)));
       const int R_new = max(R, xr);
       const float f = R_new - R > 126 ? 0.0f : alpha * as_f((uint32_t)(127 - (R_new - R)) << 23);
       l *= alpha;
@@ -964,9 +973,13 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
       for (int i = 0; i < kDT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] *= f;
-      sum = weights(s, r_new, pw);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[t][j] -= off;
+      sum = weights(s, at, pw);
       m = m_new;
-      r = none ? INFINITY : r_new;
+      r = none || far ? INFINITY : r_new;
       R = R_new;
     }
     l += sum;
@@ -1095,8 +1108,8 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, int h, int64_t 
     }
   if (!whole) {
     if (half == 0) {
-      a.wide_ml[2 * slot] = m == -INFINITY ? m : kPExp - r;   // the reference that O and l have, in powers of 2
-      a.wide_ml[2 * slot + 1] = l * 0x1p-9f;
+      a.wide_ml[2 * slot] = m;
+      a.wide_ml[2 * slot + 1] = l * __builtin_amdgcn_exp2f(-held_exp(m, r));
     }
   }
 }
@@ -1220,11 +1233,11 @@ __device__ __forceinline__ void join_wide(const AttendArgs& a, int64_t group) {
     }
     const float top = fmaxf(M, fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])));
     // the average so far, and the parts', by their shares of p
-    const float keep = L * part_weight(M, top, 1.0f);
+    const float keep = L * part_weight(M, top, a.c);
     L = keep;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      li[k] *= part_weight(mi[k], top, 1.0f);
+      li[k] *= part_weight(mi[k], top, a.c);
       L += li[k];
     }
     const float inv = L > 0 ? recip_rn(L) : 0.0f;

@@ -552,6 +552,13 @@ def _token_rows(x: torch.Tensor, shape, es: int):
     return x.clone(memory_format=torch.contiguous_format), row
 
 
+def _rows_meet(rows: int, step: int, size: int, count: int, other: int) -> bool:
+    """Whether `count` rows of `size` bytes, `step` >= size bytes apart from address `rows`,
+    share a byte with the count * size bytes at address `other`."""
+    first = max((other - size - rows) // step + 1, 0)       # the first row that ends behind `other`
+    return first < count and rows + first * step < other + count * size
+
+
 def kv_plan_paged(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
                   free_pages: torch.Tensor, free_used: torch.Tensor, page_size: int, max_new: int,
                   out: PagedPlan | None = None) -> PagedPlan:
@@ -639,7 +646,8 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     of one request where the caller knows it (a hint for speed and workspace).
     workspace: memory to use instead of an allocation per call (any contiguous
     tensor of pqb_kv_attend_workspace_bytes; calls that overlap need one each).
-    Rows outside every request are left as they were in `out`."""
+    Rows outside every request are left as they were in `out`, which may share no
+    memory with q."""
     dev = _device_of(q, "q")
     c = _pages_struct(cache, dev)
     if not _ready(dev, _I32, block_table, q_starts, kv_lens):
@@ -654,11 +662,14 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     if max_q_len is not None and max_q_len < 1:
         raise ValueError("max_q_len must be positive")
     width, hint = rows[1], max_q_len or 0
+    es = 2 if dtype == BF16 else 4
+    if out is not None and (not _ready(dev, q.dtype, out) or out.shape != shape or out.data_ptr() == q.data_ptr() and T):
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype, apart from q")
+    q, ld = _token_rows(q, shape, es)
     if out is None:
         out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
-    elif not _ready(dev, q.dtype, out) or out.shape != shape or out.data_ptr() == q.data_ptr() and T:
-        raise ValueError("out must be a contiguous tensor of q's shape and dtype, apart from q")
-    q, ld = _token_rows(q, shape, 2 if dtype == BF16 else 4)
+    elif T and Hq and _rows_meet(q.data_ptr(), ld * es, Hq * D * es, T, out.data_ptr()):
+        raise ValueError("out must not share memory with q")
     if T == 0 or B == 0:
         return out
     L = lib()

@@ -1,5 +1,7 @@
 """The paged 8-bit KV cache at the ends of what a call may hold: the largest lengths,
 values and scores, many requests with everything split, and workspaces in use."""
+import contextlib
+
 import numpy as np
 import pytest
 import torch
@@ -121,3 +123,23 @@ def test_attend_scores_far_from_zero(dtype, dim, page, base, unit, new, kv):
     """Scores whose rounding to float32 is coarser than what tells them apart, or that pass
     what an exponent may be: only differences of scores may enter p."""
     check_whole_scores(dtype, dim, page, base, unit, new, kv)
+
+
+def test_attend_refuses_an_out_that_shares_memory_with_q():
+    """The same projection's buffer: parts of it that lie over q's rows are refused, its
+    free rows and the gaps between q's rows are not."""
+    cache = filled(np.random.default_rng(30), 2, 2, 16, 64)[0]
+    buf = torch.randn((12, 8, 64), dtype=BF, device=DEV)
+    args = (cache, ints([[0, 1]]), ints([0, 4]), ints([20]))
+    q = buf[:4, 2:6]
+    want = pqb.kv_attend_paged(q, *args)
+    for at in (0, 64, 128, 1920):                                # q's rows end at 384, 896, 1408, 1920
+        out = buf.view(-1)[at:at + 1024].view(4, 4, 64)
+        with pytest.raises(ValueError) if at < 1920 else contextlib.nullcontext():
+            pqb.kv_attend_paged(q, *args, out=out)
+    free = buf.view(-1)[4 * 512:4 * 512 + 1024].view(4, 4, 64)
+    assert torch.equal(pqb.kv_attend_paged(q, *args, out=free), want)
+    wide = torch.randn((2, 12, 64), dtype=BF, device=DEV)        # a gap of 8 heads holds 2 rows of 4
+    one = (cache, ints([[0, 1]]), ints([0, 2]), ints([20]))
+    got = pqb.kv_attend_paged(wide[:, :4], *one, out=wide.view(-1)[256:768].view(2, 4, 64))
+    assert torch.equal(got, pqb.kv_attend_paged(wide[:, :4], *one))

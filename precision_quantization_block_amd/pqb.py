@@ -479,7 +479,9 @@ PLAN_FLAGS = {"pages": 1, "table": 2, "slots": 4, "negative": 8}
 
 
 _I32, _U8, _BF16, _F32 = torch.int32, torch.uint8, torch.bfloat16, torch.float32
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# (a torch without GPU support has neither of the two quick ones; the binding still imports)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _refuse(dev, dtypes, names, *ts, contiguous=True):

@@ -8,7 +8,7 @@ import torch
 
 import precision_quantization_block_amd as pqb
 from oracle import paged
-from test_gpu_paged import BF, DEV, F32, check_attend, filled, ints, tiles
+from test_gpu_paged import BF, DEV, F32, Server, check_attend, filled, ints, tiles
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,117 @@ def test_attend_refuses_an_out_that_shares_memory_with_q():
     one = (cache, ints([[0, 1]]), ints([0, 2]), ints([20]))
     got = pqb.kv_attend_paged(wide[:, :4], *one, out=wide.view(-1)[256:768].view(2, 4, 64))
     assert torch.equal(got, pqb.kv_attend_paged(wide[:, :4], *one))
+
+
+# ---------------------------------------------------------------------------
+# many requests, and workspaces in use
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("batch,hint", [(130, "max"), (200, "max"), (200, None), (200, 1)])
+def test_attend_of_many_requests_that_are_cut(dtype, page, batch, hint):
+    """More requests than a wave looks at in one round (64): single tokens over thousands
+    (cut into items), prompts (wide tiles, some cut along their tokens) and requests
+    without queries on both sides of requests 63/64 and 127/128 and behind them."""
+    rng = np.random.default_rng(31)
+    new = (np.arange(batch) % 3 != 0).astype(int)             # every third has no query
+    kv = rng.integers(0, 200, batch)
+    for b in (2, 62, 63, 64, 127, 128, 129):
+        new[b], kv[b] = 1, 1500 + 7 * b
+    for b in (5, 61, 65, 66, 126, batch - 2, batch - 1):
+        new[b], kv[b] = 17 + b % 50, 900 + 5 * b
+    new[60], kv[60], new[67], kv[67] = 150, 150, 9, 2000
+    new[68], kv[68] = 0, 2500
+    check_attend(rng, new.tolist(), kv.tolist(), 2, 2, 64, page, dtype, hint=hint)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("page", [16, 64])
+def test_attend_of_many_single_tokens_that_are_cut(dtype, page):
+    """Decoding alone (the row kernel, its items and their join), over 300 requests."""
+    rng = np.random.default_rng(32)
+    kv = rng.integers(0, 700, 300)
+    kv[[0, 63, 64, 200, 255, 256, 299]] = [3000, 2500, 2600, 5000, 600, 2048, 4097]
+    check_attend(rng, [1] * 300, kv.tolist(), 1, 4, 64, page, dtype, spare=3)
+
+
+class Filled(Server):
+    """A server whose requests hold thousands of tokens already."""
+
+    def __init__(self, lens, seed, heads, group, dim, page, width, max_new, dtype):
+        super().__init__(len(lens), heads, group, dim, page, width, len(lens) * width, max_new, dtype)
+        rng = np.random.default_rng(seed)
+        self.cache, self.host = filled(rng, len(lens) * width, heads, page, dim)
+        self.new.copy_(ints(lens))
+        big = pqb.PagedPlan(ints([0] * sum(lens)), ints([0] * (len(lens) + 1)), self.lens, self.used, ints([0] * 4))
+        pqb.kv_plan_paged(self.lens, self.new, self.table, self.free, self.used, page, sum(lens), out=big)
+        assert big.status[0].item() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_two_streams_use_their_workspaces_at_once(dtype):
+    """Two servers of other data on two streams: single tokens over thousands and a chunk,
+    all cut, so that every call writes and joins parts; each as it does alone."""
+    lens, kw = [4000, 2500, 3000], dict(heads=2, group=4, dim=128, page=64, width=80, max_new=64, dtype=dtype)
+
+    def make(k):
+        s = Filled(lens, 40 + k, **kw)
+        s.qkv.copy_(torch.randn(s.qkv.shape, generator=torch.Generator().manual_seed(50 + k)))
+        s.new.copy_(ints([1, 1, 40]))
+        return s
+
+    need = pqb.pqb.lib().pqb_kv_attend_workspace_bytes(0 if dtype == F32 else 1, 64, 8, 2, 128, 3, 80, 64, 0)
+    assert need > 1 << 20
+    servers, streams = [make(0), make(1)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for k, (s, st) in enumerate(zip(servers, streams)):
+            with torch.cuda.stream(st):
+                s.step()
+                outs[k].append(s.out.clone())
+    torch.cuda.synchronize()
+    for k in range(2):
+        alone = make(k)
+        for got in outs[k]:
+            alone.step()
+            assert torch.equal(got, alone.out)
+        assert alone.plan.status[0].item() == 0
+    assert not torch.equal(outs[0][0], outs[1][0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_replays_cross_into_cuts(dtype):
+    """One captured step replayed while lengths pass 512 tokens, where items and tiles
+    begin to be cut, and from nothing to a chunk and back; every replay against the plain form."""
+    heads, group, dim, page, width = 2, 2, 64, 16, 200
+    s = Filled([509, 2000, 30, 511], 60, heads, group, dim, page, width, 64, dtype)
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        s.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.step()
+    rng = np.random.default_rng(61)
+    codes = [s.host[0].copy(), np.ascontiguousarray(s.host[1].transpose(0, 1, 3, 2))]
+    scales = [s.host[2].copy(), s.host[3].copy()]
+    table, free, lens, used = s.table.cpu().numpy(), s.free.cpu().numpy(), s.lens.tolist(), s.used.item()
+    hq = heads * group
+    for new in ([1, 1, 1, 1], [2, 1, 0, 0], [1, 30, 1, 1], [1, 1, 1, 20], [0, 0, 40, 0], [1, 1, 1, 1], [25, 1, 1, 1]):
+        x = torch.from_numpy(rng.standard_normal(tuple(s.qkv.shape))).to(dtype)
+        s.qkv.copy_(x)
+        s.new.copy_(ints(new))
+        s.out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        flags, table, slots, starts, lens, used, _ = paged.plan(lens, new, table, free, used, page, 64)
+        lens = lens.tolist()
+        assert flags == 0 and s.lens.tolist() == lens
+        xd = x.double().numpy()
+        paged.append(xd[:, hq:hq + heads], slots, codes[0], scales[0])
+        paged.append(xd[:, hq + heads:], slots, codes[1], scales[1])
+        T = int(starts[-1])
+        want, bound = paged.attend(xd[:T, :hq], codes[0], codes[1].transpose(0, 1, 3, 2), *scales,
+                                   np.where(table < 0, 0, table), starts, lens, True, dim ** -0.5, dtype == F32)
+        got = s.out.double().cpu().numpy()
+        assert (got[T:] == 7).all() and (np.abs(got[:T] - want) <= bound).all(), new

@@ -34,7 +34,9 @@ constexpr int kTile = 16;        // query rows of a tile
 constexpr int kWaves = kUnitWaves, kThreads = kWaves * kWave;
 constexpr int kMaxPartRows = 64;                  // rows of a request that the row kernel may split
 constexpr int64_t kMaxGroups = 1 << 23;            // workgroups that splits or joins lead to
-constexpr int kMinWideUnits = 8;                  // the same for the wide kernel
+constexpr int kMinWideUnits = 8;                  // fewest units of a split of the wide kernel
+// 512: the places of bf16 and heads up to 128 wide, two workgroups a CU, for which it was
+// measured best of 256 to 1024.  The other forms have 256 places and share the number.
 constexpr int64_t kMaxWideSplits = 32, kWideGroupsWanted = 512;
 
 // ---------------------------------------------------------------------------
@@ -630,8 +632,9 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 // against q's bf16 (or a float32 q's three parts).  The FP8 products would take the
 // codes as they are, but sum eight products at a time with 13 bits below the largest
 // (beside 2^16 one of 2^3 counts, one of 2^2 is lost): where a channel of the keys stands
-// out, that drops what the others say.  The bf16 products keep float32's 24 bits.  The
-// two prompts below took 275 us with FP8 products and q in two E4M3 parts.
+// out, that drops what the others say.  The bf16 products keep float32's 24 bits and
+// cost what two FP8 ones would (q in two E4M3 parts), but for 64 conversions more a
+// wave and unit (D = 128): the two prompts below took 265-280 us with FP8 products.
 // O^T: V is decoded to f16 beside the products (v_cvt_scalef32_pk_f16_fp8).
 //
 // Key row m = 8 a + 4 h + b of tile t stands for token 32 h + 16 t + 4 a + b: a
@@ -645,8 +648,8 @@ __global__ __launch_bounds__(kThreads) void k_attend_rows(const AttendArgs a) {
 // Bound by the issue of vector and matrix instructions together: three units are
 // in the pipeline (O^T of one, P of the next, S^T of the one behind it), so that
 // the matrix core works under the exponentials and conversions.  Two prompts of
-// 4096 tokens (32 heads over 8, 128 wide, bf16): 271 us, 1.03 PFLOP/s, where the
-// library's bf16 product of 8192^3 reaches 1.19; one unit at a time took 330.
+// 4096 tokens (32 heads over 8, 128 wide, bf16): 295-305 us, 0.92 PFLOP/s, where the
+// library's bf16 product of 8192^3 reaches 1.19.
 // ---------------------------------------------------------------------------
 
 constexpr float kPExp = 9.0f;      // p is held times 2^9

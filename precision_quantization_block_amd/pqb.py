@@ -645,7 +645,9 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     causal: query i of n sees the tokens up to kv_lens[b] - n + i; otherwise all
     of them (cross attention over an encoder's states, of any other length).
     scale: 1 / sqrt(head_dim) unless given.  max_q_len: the most query tokens
-    of one request where the caller knows it (a hint for speed and workspace).
+    of one request where the caller knows it (a hint for speed and workspace:
+    without it a step of single tokens is launched as if prompts might be
+    among them, 141 instead of 104 us for 64 requests of 269 K tokens).
     workspace: memory to use instead of an allocation per call (any contiguous
     tensor of pqb_kv_attend_workspace_bytes; calls that overlap need one each).
     Rows outside every request are left as they were in `out`, which may share no

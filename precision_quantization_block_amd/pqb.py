@@ -682,7 +682,7 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
         have = need
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif _ready(dev, workspace.dtype, workspace):
+    elif isinstance(workspace, torch.Tensor) and _ready(dev, workspace.dtype, workspace):
         have = workspace.numel() * workspace.element_size()
     else:
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")

@@ -145,6 +145,16 @@ def test_attend_refuses_an_out_that_shares_memory_with_q():
     assert torch.equal(got, pqb.kv_attend_paged(wide[:, :4], *one))
 
 
+def test_attend_refuses_a_workspace_that_is_no_tensor_there():
+    cache = filled(np.random.default_rng(33), 2, 2, 16, 64)[0]
+    q = torch.zeros((1, 4, 64), dtype=BF, device=DEV)
+    ws = torch.empty((64, 64), dtype=torch.uint8, device=DEV)
+    for bad in (1 << 20, ws.data_ptr(), ws.cpu(), ws[:, :32]):
+        with pytest.raises(ValueError):
+            pqb.kv_attend_paged(q, cache, ints([[0, 1]]), ints([0, 1]), ints([20]), workspace=bad)
+    pqb.kv_attend_paged(q, cache, ints([[0, 1]]), ints([0, 1]), ints([20]), workspace=ws)
+
+
 # ---------------------------------------------------------------------------
 # many requests, and workspaces in use
 # ---------------------------------------------------------------------------

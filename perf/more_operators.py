@@ -1,0 +1,419 @@
+"""Cases of the INT8 layer: the 8-bit integer product and what a decoder layer does around it.
+
+  gemm   C[m, n] = sa[m] sb[n] sum_k a[m, k] b[n, k] + bias[n] of int8 codes with a
+         float32 scale per token (row of a) and per channel (row of b)
+  norm   h = gate * N(x; post) + c * residual, rounded to the input's type, then
+         RMS or layer norm of h, as it is or as codes with a scale per row
+         (INT8, E4M3) or per 1x128 block (E4M3)
+  act    act(g) * u (or act(g) alone), as it is or as codes with their scales
+  rope   q and k turned by their positions' angles: half or interleaved pairs,
+         the whole head or its first part
+  down   an MLP's second half: silu(g) * u to INT8 codes, then the product
+"""
+import math
+
+import torch
+
+own = False
+
+E4M3 = torch.float8_e4m3fn
+AMAX_FLOOR = 1e-12
+
+
+# ---------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------
+
+def listed():
+    return [
+        # one decoded token through an attention output projection of Llama-3.1-8B's size
+        dict(name="gemm_one_bf16", op="gemm", m=1, n=4096, k=4096, bias=False, dtype="bf16"),
+        # a decode step of 64 requests through its gate projection
+        dict(name="gemm_step64_bf16", op="gemm", m=64, n=14336, k=4096, bias=False, dtype="bf16"),
+        # odd rows and channels, a ragged inner size, a bias, float32 out
+        dict(name="gemm_odd_f32", op="gemm", m=777, n=1001, k=2064, bias=True, dtype="f32"),
+        # a prefill batch on the repository's FP8 product's shape
+        dict(name="gemm_prefill_bf16", op="gemm", m=8192, n=7168, k=2048, bias=False, dtype="bf16"),
+        # a chunk of a prompt through an MLP's second half, the inputs parts of one fused projection
+        dict(name="down_chunk_bf16", op="down", m=512, n=4096, k=14336, dtype="bf16"),
+        # between two products of a decode step: residual, RMS norm, INT8 codes per token
+        dict(name="norm_step64_int8", op="norm", rows=64, cols=4096, kind="rms", form="int8",
+             residual=True, scale=1.0, gates=0, post=False, dtype="bf16"),
+        # the same for a prefill batch, E4M3 codes per 1x128 block for the FP8 product
+        dict(name="norm_prefill_blk", op="norm", rows=8192, cols=7168, kind="rms", form="fp8_blk",
+             residual=True, scale=1.0, gates=0, post=False, dtype="bf16"),
+        # layer norms before and after a block, a gate per sequence, a scaled residual, odd width
+        dict(name="norm_gated_f32", op="norm", rows=1500, cols=1005, kind="layer", form="none",
+             residual=True, scale=0.7071, gates=4, post=True, dtype="f32"),
+        # SwiGLU of a prefill batch to E4M3 per 1x128 block
+        dict(name="act_prefill_blk", op="act", rows=4096, cols=14336, act="silu", gated=True,
+             form="fp8_blk", dtype="bf16"),
+        # an encoder's GELU over 1500 states, odd width, E4M3 per row
+        dict(name="act_gelu_f32", op="act", rows=1500, cols=1285, act="gelu_erf", gated=False,
+             form="fp8_row", dtype="f32"),
+        # a decode step of 64 requests far into long conversations
+        dict(name="rope_step64_bf16", op="rope", tokens=64, heads=32, kv_heads=8, dim=128, rot=128,
+             interleaved=False, far=131072, factor=8.0, dtype="bf16"),
+        # a prefill batch, interleaved pairs on the first half of each head
+        dict(name="rope_prefill_f32", op="rope", tokens=8192, heads=32, kv_heads=8, dim=128, rot=64,
+             interleaved=True, far=8192, factor=1.0, dtype="f32"),
+    ]
+
+
+def _between(rng, lo, hi):
+    """An integer spread over the logarithm of [lo, hi]."""
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["gemm", "gemm", "gemm", "norm", "norm", "act", "rope", "down"])
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    if op == "gemm":
+        m, k = _between(rng, 1, 8192), 16 * _between(rng, 1, 896)
+        n = _between(rng, 1, max(1, min(16384, 10 ** 11 // (m * k))))
+        return dict(op=op, m=m, n=n, k=k, bias=rng.random() < 0.3, dtype=dtype)
+    if op == "down":
+        return dict(op=op, m=_between(rng, 1, 512), n=_between(rng, 16, 4096),
+                    k=16 * _between(rng, 4, 896), dtype=dtype)
+    if op == "norm":
+        form = rng.choice(["int8", "fp8_row", "fp8_blk", "none"])
+        rows = _between(rng, 1, 16384)
+        cols = _between(rng, 16, max(17, min(16384, 40_000_000 // rows)))
+        cols = 128 * max(1, cols // 128) if form == "fp8_blk" else cols
+        plain = form == "int8"      # codes of whole numbers: forms whose codes no sum enters
+        gates = rng.choice([0, 0, 1, rows]) if not plain else 0
+        return dict(op=op, rows=rows, cols=cols, kind="rms" if plain else rng.choice(["rms", "layer"]),
+                    form=form, residual=rng.random() < 0.75, scale=rng.choice([1.0, 1.0, 0.22]),
+                    gates=gates, post=not plain and rng.random() < 0.3, dtype=dtype)
+    if op == "act":
+        form = rng.choice(["fp8_row", "fp8_blk", "none"])
+        rows = _between(rng, 1, 16384)
+        cols = _between(rng, 16, max(17, min(28672, 40_000_000 // rows)))
+        cols = 128 * max(1, cols // 128) if form == "fp8_blk" else cols
+        return dict(op=op, rows=rows, cols=cols, act=rng.choice(["silu", "gelu_tanh", "gelu_erf"]),
+                    gated=rng.random() < 0.7, form=form, dtype=dtype)
+    dim = rng.choice([64, 80, 96, 128, 128, 256])
+    kv_heads = rng.choice([1, 2, 4, 8])
+    heads = kv_heads * rng.choice([1, 2, 4, 5])
+    tokens = _between(rng, 1, max(1, min(16384, 30_000_000 // ((heads + kv_heads) * dim))))
+    return dict(op=op, tokens=tokens, heads=heads, kv_heads=kv_heads, dim=dim,
+                rot=rng.choice([dim, dim, dim // 2, 20]), interleaved=rng.random() < 0.4,
+                far=_between(rng, 100, 10_000_000), factor=rng.choice([1.0, 4.0, 8.0]), dtype=dtype)
+
+
+def _width(dtype):
+    return 2 if dtype == "bf16" else 4
+
+
+def _form_bytes(form, rows, cols, es):
+    """Bytes of the codes and scales (or plain values) of [rows, cols]."""
+    if form == "none":
+        return rows * cols * es
+    return rows * cols + 4 * rows * (cols // 128 if form == "fp8_blk" else 1)
+
+
+def work(case):
+    es, op = _width(case["dtype"]), case["op"]
+    if op in ("gemm", "down"):
+        m, n, k = case["m"], case["n"], case["k"]
+        a = m * k + 4 * m if op == "gemm" else 2 * m * k * es
+        return {"bytes": a + n * k + 4 * n + m * n * es + (4 * n if case.get("bias") else 0),
+                "flops": 2 * m * n * k}
+    if op == "norm":
+        rows, cols = case["rows"], case["cols"]
+        adds = case["residual"] or case["gates"] or case["post"]
+        reads = rows * cols * (2 if case["residual"] else 1) + cols * (
+            1 + case["gates"] + (1 if case["post"] else 0) + (1 if case["kind"] == "layer" else 0))
+        return {"bytes": es * (reads + (rows * cols if adds else 0))
+                + _form_bytes(case["form"], rows, cols, es), "flops": 0}
+    if op == "act":
+        rows, cols = case["rows"], case["cols"]
+        return {"bytes": rows * cols * es * (2 if case["gated"] else 1)
+                + _form_bytes(case["form"], rows, cols, es), "flops": 0}
+    t = case["tokens"]
+    return {"bytes": 2 * es * t * (case["heads"] + case["kv_heads"]) * case["dim"] + 4 * t, "flops": 0}
+
+
+# ---------------------------------------------------------------------------
+# what a serving program has in hand
+# ---------------------------------------------------------------------------
+
+def _angles(rot, factor, base=500000.0, original=8192, low=1.0, high=4.0):
+    """Radians per token of each pair: base^(-2i / rot), slower by `factor` where a
+    turn takes longer than original / low tokens, as they are where it takes less
+    than original / high, in between by the share of the way."""
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    turns = original * f / (2 * math.pi)
+    keep = ((turns - low) / (high - low)).clamp(0, 1)
+    return f * (keep + (1 - keep) / factor)
+
+
+def _codes(g, dev, rows, cols):
+    """INT8 codes and a scale per row, as a per-row quantizer leaves them."""
+    x = torch.randn((rows, cols), generator=g, device=dev) * 36
+    s = torch.exp(torch.randn((rows,), generator=g, device=dev) * 0.3) * 0.01
+    return x.round().clamp(-127, 127).to(torch.int8), s
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(seed)
+    dtype = torch.bfloat16 if case["dtype"] == "bf16" else torch.float32
+    op, s = case["op"], dict(case=case, dtype=dtype)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device=dev)
+
+    if op in ("gemm", "down"):
+        m, n, k = case["m"], case["n"], case["k"]
+        s["b"], s["b_scales"] = _codes(g, dev, n, k)
+        s["bias"] = normal(n) if case.get("bias") else None
+        if op == "gemm":
+            s["a"], s["a_scales"] = _codes(g, dev, m, k)
+        else:
+            both = (normal(m, 2 * k) * 1.5).to(dtype)
+            s["gate"], s["up"] = both[:, :k], both[:, k:]
+    elif op == "norm":
+        rows, cols = case["rows"], case["cols"]
+        # a few channels far larger than the rest
+        loud = 1 + 12 * (torch.rand(cols, generator=g, device=dev) < 0.01)
+        s["x"] = (normal(rows, cols) * loud).to(dtype)
+        s["residual"] = (normal(rows, cols) * loud * 3).to(dtype) if case["residual"] else None
+        s["weight"] = (1 + 0.2 * normal(cols)).to(dtype)
+        s["post_weight"] = (1 + 0.2 * normal(cols)).to(dtype) if case["post"] else None
+        s["bias"] = (0.1 * normal(cols)).to(dtype) if case["kind"] == "layer" else None
+        s["gate"] = normal(case["gates"], cols).to(dtype) if case["gates"] else None
+    elif op == "act":
+        rows, cols = case["rows"], case["cols"]
+        both = (normal(rows, (2 if case["gated"] else 1) * cols) * 1.5).to(dtype)
+        s["gate"], s["up"] = both[:, :cols], both[:, cols:] if case["gated"] else None
+    else:
+        t, hq, hk, dim = case["tokens"], case["heads"], case["kv_heads"], case["dim"]
+        qkv = normal(t, hq + 2 * hk, dim).to(dtype)     # one fused projection's output
+        s["q"], s["k"] = qkv[:, :hq], qkv[:, hq:hq + hk]
+        s["positions"] = torch.randint(0, case["far"], (t,), generator=g, device=dev, dtype=torch.int32)
+        s["angles"] = _angles(case["rot"], case["factor"]).to(dev)
+    return s
+
+
+# ---------------------------------------------------------------------------
+# one pass
+# ---------------------------------------------------------------------------
+
+FORMS = {"int8": ("int8_sym", "row"), "fp8_row": ("fp8_e4m3", "row"), "fp8_blk": ("fp8_e4m3", "1x128"),
+         "none": (None, None)}
+
+
+def run(state):
+    return {"gemm": _run_gemm, "norm": _run_norm, "act": _run_act, "rope": _run_rope,
+            "down": _run_down}[state["case"]["op"]](state)
+
+
+def _run_gemm(s):
+    if own:
+        import precision_quantization_block_amd as pqb
+        return pqb.gemm_int8((s["a"], s["a_scales"]), (s["b"], s["b_scales"]), s["dtype"], bias=s["bias"])
+    return _product(s["a"], s["a_scales"], s["b"], s["b_scales"], s["bias"], s["dtype"])
+
+
+def _run_down(s):
+    if own:
+        import precision_quantization_block_amd as pqb
+        q = pqb.act_quant(s["gate"], s["up"], "int8_sym", "row", act="silu")
+        return pqb.gemm_int8(q, (s["b"], s["b_scales"]), s["dtype"])
+    a = _activated(s["gate"].float(), s["up"], "silu")
+    codes, scales = _quantized(a, "int8", 1.0)
+    return _product(codes, scales[:, 0], s["b"], s["b_scales"], None, s["dtype"])
+
+
+def _run_norm(s):
+    case = s["case"]
+    if own:
+        import precision_quantization_block_amd as pqb
+        fmt, gran = FORMS[case["form"]]
+        out, h = pqb.norm_quant(s["x"], s["weight"], fmt, gran, kind=case["kind"], bias=s["bias"],
+                                eps=1e-5, residual=s["residual"], residual_scale=case["scale"],
+                                gate=s["gate"], post_weight=s["post_weight"])
+        return dict(h=h, **_values(out, case["form"], case["rows"], case["cols"]))
+    x, w = s["x"].float(), s["weight"].float()
+    y = x
+    if case["post"]:
+        c, r = _centred(x, case["kind"])
+        y = c * r * s["post_weight"].float()
+    if s["gate"] is not None:
+        y = y * s["gate"].float().repeat_interleave(case["rows"] // case["gates"], 0)
+    if s["residual"] is not None:
+        y = y + s["residual"].float() * case["scale"]
+    h = y.to(s["dtype"])
+    c, r = _centred(h.float(), case["kind"])
+    if case["kind"] == "layer":
+        u, r = c * r * w + s["bias"].float(), torch.ones_like(r)
+    else:
+        u = c * w
+    adds = case["residual"] or case["gates"] or case["post"]
+    return dict(h=h if adds else None, **_formed(u, case["form"], r, s["dtype"]))
+
+
+def _run_act(s):
+    case = s["case"]
+    if own:
+        import precision_quantization_block_amd as pqb
+        fmt, gran = FORMS[case["form"]]
+        out = pqb.act_quant(s["gate"], s["up"], fmt, gran, act=case["act"])
+        return _values(out, case["form"], case["rows"], case["cols"])
+    return _formed(_activated(s["gate"].float(), s["up"], case["act"]), case["form"], 1.0, s["dtype"])
+
+
+def _run_rope(s):
+    if own:
+        import precision_quantization_block_amd as pqb
+        table = pqb.RopeTable(s["angles"], 1.0, s["case"]["interleaved"])
+        q, k = pqb.rope(s["q"], s["k"], s["positions"], table)
+        return dict(q=q, k=k)
+    a = s["positions"].double()[:, None] * s["angles"]
+    c, n = a.cos().float()[:, None], a.sin().float()[:, None]
+    return dict(q=_turned(s["q"], c, n, s["case"]), k=_turned(s["k"], c, n, s["case"]))
+
+
+def _values(out, form, rows, cols):
+    """What the framework's result holds: plain values, or codes by their type and scales."""
+    if form == "none":
+        return dict(out=out)
+    codes = out.codes.view(torch.int8 if form == "int8" else E4M3).view(rows, cols)
+    return dict(codes=codes, scales=out.scales.view(rows, -1))
+
+
+def _formed(u, form, r, dtype):
+    if form == "none":
+        return dict(out=(u * r).to(dtype))
+    codes, scales = _quantized(u, form, r)
+    return dict(codes=codes, scales=scales)
+
+
+def _quantized(u, form, r):
+    """Codes of u with scales max(amax, floor) / largest over a row or 128 columns;
+    the scales returned times r."""
+    top = 127.0 if form == "int8" else 448.0
+    blocks = u.reshape(u.shape[0], -1, 128) if form == "fp8_blk" else u[:, None]
+    step = blocks.abs().amax(2).clamp(min=AMAX_FLOOR) / top
+    q = (blocks / step[:, :, None]).reshape(u.shape)
+    return q.round().to(torch.int8) if form == "int8" else q.to(E4M3), step * r
+
+
+def _centred(x, kind):
+    """x (less its mean), and 1 / sqrt(mean square + eps)."""
+    c = x - x.mean(1, keepdim=True) if kind == "layer" else x
+    return c, torch.rsqrt(c.square().mean(1, keepdim=True) + 1e-5)
+
+
+def _activated(g, up, act):
+    if act == "silu":
+        a = g / (1 + torch.exp(-g))
+    elif act == "gelu_tanh":
+        a = 0.5 * g * (1 + torch.tanh(math.sqrt(2 / math.pi) * (g + 0.044715 * g * g * g)))
+    else:       # 1 - erf loses every digit of the small tail in 32 bits
+        a = (0.5 * g.double() * torch.erfc(-g.double() / math.sqrt(2))).float()
+    return a if up is None else a * up.float()
+
+
+def _turned(x, c, n, case):
+    rot, half, y = case["rot"], case["rot"] // 2, x.float()
+    if case["interleaved"]:
+        a, b = y[..., 0:rot:2], y[..., 1:rot:2]
+        turned = torch.stack((a * c - b * n, b * c + a * n), 3).flatten(2)
+    else:
+        a, b = y[..., :half], y[..., half:rot]
+        turned = torch.cat((a * c - b * n, b * c + a * n), 2)
+    return torch.cat((turned, y[..., rot:]), 2).to(x.dtype)
+
+
+def _product(a, sa, b, sb, bias, dtype):
+    """The sums pass 2^24: they are exact in 64 bits."""
+    c = torch.matmul(a.double(), b.double().t()) * sa.double()[:, None] * sb.double()
+    return (c if bias is None else c + bias.double()).to(dtype)
+
+
+# ---------------------------------------------------------------------------
+# the definitions in 64 bits
+# ---------------------------------------------------------------------------
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "gemm":
+        return _exact_product(s["a"].double() * s["a_scales"].double()[:, None], s)
+    if op == "down":
+        a = _exact_act(s["gate"].double(), "silu") * s["up"].double()
+        step = a.abs().amax(1, keepdim=True).clamp(min=AMAX_FLOOR) / 127
+        return _exact_product(torch.round(a / step) * step, s)
+    if op == "norm":
+        return _exact_norm(case, s)
+    if op == "act":
+        a = _exact_act(s["gate"].double(), case["act"])
+        return _exact_form(a if s["up"] is None else a * s["up"].double(), case["form"])
+    return _exact_rope(case, s)
+
+
+def _exact_product(a, s):
+    b = s["b"].double() * s["b_scales"].double()[:, None]
+    out = torch.empty((a.shape[0], b.shape[0]), dtype=torch.float64, device=a.device)
+    for i in range(0, a.shape[0], 1024):
+        out[i:i + 1024] = a[i:i + 1024] @ b.T
+    return out if s["bias"] is None else out + s["bias"].double()
+
+
+def _exact_act(g, act):
+    if act == "silu":
+        return g * torch.sigmoid(g)
+    if act == "gelu_tanh":      # (1 + tanh z) / 2 = sigmoid(2 z)
+        return g * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3))
+    return g * torch.special.ndtr(g)
+
+
+def _exact_form(v, form):
+    if form == "none":
+        return dict(out=v)
+    if form == "int8":
+        return dict(codes=None, scales=v.abs().amax(1, keepdim=True).clamp(min=AMAX_FLOOR) / 127)
+    parts = v.unflatten(1, (-1, 128)) if form == "fp8_blk" else v.unsqueeze(1)
+    scales = parts.abs().amax(2).clamp(min=AMAX_FLOOR) / 448
+    q = parts / scales.unsqueeze(2)
+    e = torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6)))
+    grid = torch.exp2(e - 3)
+    return dict(codes=(torch.round(q / grid) * grid).reshape(v.shape), scales=scales)
+
+
+def _exact_norm(case, s):
+    def norm(x, w, b):
+        if case["kind"] == "layer":
+            return torch.nn.functional.layer_norm(x, x.shape[-1:], w, b, 1e-5)
+        return x * w / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-5)
+
+    h = s["x"].double()
+    if case["post"]:
+        h = norm(h, s["post_weight"].double(), None)
+    if case["gates"]:
+        h = h.unflatten(0, (case["gates"], -1)) * s["gate"].double()[:, None]
+        h = h.flatten(0, 1)
+    if case["residual"]:
+        h = h + case["scale"] * s["residual"].double()
+    adds = case["residual"] or case["gates"] or case["post"]
+    bias = None if s["bias"] is None else s["bias"].double()
+    v = norm(h.to(s["dtype"]).double(), s["weight"].double(), bias)
+    return dict(h=h if adds else None, **_exact_form(v, case["form"]))
+
+
+def _exact_rope(case, s):
+    rot, out = case["rot"], {}
+    turn = torch.polar(torch.ones((), dtype=torch.float64, device=s["q"].device),
+                       s["positions"].double()[:, None, None] * s["angles"])
+    for name in "qk":
+        x = s[name].double().clone()
+        if case["interleaved"]:
+            z = torch.view_as_complex(x[..., :rot].unflatten(2, (-1, 2)).contiguous()) * turn
+            x[..., :rot] = torch.view_as_real(z).flatten(2)
+        else:
+            z = torch.complex(x[..., :rot // 2].contiguous(), x[..., rot // 2:rot].contiguous()) * turn
+            x[..., :rot // 2], x[..., rot // 2:rot] = z.real, z.imag
+        out[name] = x
+    return out

@@ -295,7 +295,8 @@ def _quantized(u, form, r):
     the scales returned times r."""
     top = 127.0 if form == "int8" else 448.0
     blocks = u.reshape(u.shape[0], -1, 128) if form == "fp8_blk" else u[:, None]
-    step = blocks.abs().amax(2).clamp(min=AMAX_FLOOR) / top
+    most = blocks.abs().amax(2).clamp(min=AMAX_FLOOR)
+    step = most / torch.full_like(most, top)    # by a number, torch multiplies by its reciprocal
     q = (blocks / step[:, :, None]).reshape(u.shape)
     return q.round().to(torch.int8) if form == "int8" else q.to(E4M3), step * r
 

@@ -578,6 +578,157 @@ pqb_status pqb_gemm_w4a16(const void* x, int64_t m, const uint8_t* codes, const 
 pqb_status pqb_gemm_w4a16_batch(const pqb_w4a16_job* jobs, int64_t njobs, int64_t m,
                                 pqb_dtype out_dtype, void* stream);
 
+/* ---- The INT8 layer: the product of symmetric INT8 codes, and what a decoder layer
+ * does between its products, fused with the quantization of the next one's
+ * activations (page "14. 量化：让每一步搬更少的字节", 量化在做什么: q = round(x / s)
+ * with s = max|x| / 127; page "量化部署实战", exercise section on FP8 blockwise scaling:
+ * activation scales belong at the end of the kernel that produces the activations). */
+
+/* Rows of INT8 codes with their scales: codes i8 [rows, k], rows `stride` bytes apart
+ * (e.g. part of a wider matrix), scales f32 [rows] (per_row 1, the INT8_SYM x ROW
+ * layout) or [1] (per_row 0, INT8_SYM x TENSOR of one slice). */
+typedef struct pqb_int8_mat {
+  const int8_t* codes;
+  const float* scales;
+  int64_t rows, stride;
+  int32_t per_row;
+  int32_t reserved; /* must be 0 (else PQB_ERR_ENUM) */
+} pqb_int8_mat;
+
+/* W8A8 product of a token's and a channel's codes:
+ *   c[m, n] = float(S) * sa[m] * sb[n] + bias[n],   S = sum_k a[m, k] b[n, k],
+ * S exact in int32; float(S), the two products and the sum are rounded to float32 one
+ * after the other (at most 4 roundings of 2^-24, then bf16 RNE for bf16 output).  c:
+ * [a.rows, b.rows] row-major of out_dtype; bias f32 [b.rows] or NULL.  Any code value -128
+ * .. 127 and any number of rows.  c may share no memory with the inputs.
+ * Shape rules: k % 16 == 0 and k <= 131056 (S stays in int32); strides multiples of 16 in
+ * [k, 2^23); rows < 2^30 and ceil(a.rows / 128) * ceil(b.rows / 128) < 2^23.  a.rows = 0 or
+ * b.rows = 0 does nothing; k = 0 writes the bias or zeros.  Workspace (sums of parts of K, where
+ * there are few tiles): pqb_gemm_int8_workspace_bytes(), its contents on entry do not
+ * matter; calls that overlap in time need one each.  Alignment: codes, c and workspace 16
+ * bytes, scales and bias 4.  Errors, before any launch: PQB_ERR_ENUM, PQB_ERR_SHAPE,
+ * PQB_ERR_NULL, PQB_ERR_ALIGN, PQB_ERR_WORKSPACE. */
+size_t pqb_gemm_int8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+pqb_status pqb_gemm_int8(const pqb_int8_mat* a, const pqb_int8_mat* b, int64_t k, const float* bias,
+                         pqb_dtype out_dtype, void* c, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* What the two calls below write: values of the input's dtype (PQB_PLAIN; gran
+ * ignored), or codes and scales as pqb_quantize lays them out for [1, rows, cols]:
+ * FP8_E4M3 or FP8_E5M2 x ROW or BLK_1x128, INT8_SYM x ROW. */
+#define PQB_PLAIN (-1)
+
+typedef enum pqb_norm_kind { PQB_NORM_RMS = 0, PQB_NORM_LAYER = 1 } pqb_norm_kind;
+
+/* Residual, gate and norms around a block, then the norm's quantization.  Over each row of
+ * `cols` values, with N(z) = z r (RMS, r = (mean z^2 + eps)^-1/2) or (z - mean z) r (layer,
+ * r = (mean (z - mean z)^2 + eps)^-1/2):
+ *   y = x, or N(x) * post_weight            (a norm behind the block)
+ *   h = gate * y + residual_scale * residual (either part only if given), rounded to dtype
+ *   v = N(h) * weight (+ bias, layer only)
+ * h (the new residual stream) is written to `h` if any of post_weight, gate and residual is
+ * given, else `h` must be NULL and h = x.  v goes to `out`: rounded to dtype, or as codes with
+ * scales.  For a layer norm the codes are pqb_quantize's of the float32 v.  For an RMS norm
+ * v = u r with u = RN(h * weight): r is common to the row and cancels in x / s, so the codes
+ * are pqb_quantize's of u (they depend on no sum), and the scales RN(RN(max(amax u, 1e-12)
+ * / M) * r).
+ * Float32 throughout, every product and sum rounded by itself in the order written.  Inputs
+ * must be finite, and so must the float32 sums of h^2 (and of x^2 with post_weight).
+ * All arrays of `dtype`, but scales (f32).  x, residual, h: rows x_stride, residual_stride,
+ * h_stride elements apart; gate [gate_rows, cols], rows gate_stride apart, gate_rows
+ * dividing rows: row t takes gate row t / (rows / gate_rows) (one per sequence, or per
+ * token).  post_weight, weight, bias [cols]; weight NULL is all ones.  out is contiguous.  h may be x
+ * or residual itself (the same address and stride); no other output may share memory
+ * with an input or output.
+ * Shape rules: cols in [1, 32768]; BLK_1x128 needs cols % 128 == 0, 16-byte aligned arrays
+ * and strides that are multiples of 8; strides in [cols, 2^40); rows * ceil(cols / 2048) < 2^22.
+ * rows = 0 does nothing.  Widths and strides that are multiples of 8 on 16-byte aligned arrays
+ * are the fast form; others only need element alignment.  eps in (0, 1], residual_scale
+ * finite (else PQB_ERR_VALUE).  Errors, before any launch: PQB_ERR_ENUM, PQB_ERR_COMBO,
+ * PQB_ERR_SHAPE, PQB_ERR_VALUE, PQB_ERR_NULL (h missing or there without need, bias with
+ * RMS), PQB_ERR_ALIGN. */
+typedef struct pqb_norm {
+  const void* x;
+  const void* residual;    /* or NULL */
+  const void* gate;        /* or NULL */
+  const void* post_weight; /* or NULL */
+  const void* weight;      /* or NULL */
+  const void* bias;        /* or NULL */
+  void* h;
+  void* out;
+  float* scales;           /* NULL for PQB_PLAIN */
+  int64_t rows, cols, gate_rows;
+  int64_t x_stride, residual_stride, gate_stride, h_stride;
+  float residual_scale, eps;
+  int32_t dtype;           /* pqb_dtype */
+  int32_t kind;            /* pqb_norm_kind */
+  int32_t fmt;             /* pqb_format or PQB_PLAIN */
+  int32_t gran;            /* pqb_gran */
+  int32_t reserved;        /* must be 0 (else PQB_ERR_ENUM) */
+} pqb_norm;
+pqb_status pqb_norm_quant(const pqb_norm* args, void* stream);
+
+/* Gated activation, then its quantization: v = act(gate) * up, or act(gate) with up NULL,
+ * over [rows, cols] of `dtype`, rows gate_stride and up_stride elements apart (e.g. the
+ * halves of one fused projection):
+ *   SILU g / (1 + exp(-g));  GELU_TANH 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)));
+ *   GELU_ERF 0.5 g erfc(-g / sqrt 2);  RELU2 max(g, 0)^2
+ * in float32 to a few units of 2^-24 of the value (GELU_TANH: times 1 + 2 |g| + |g|^3 / 10, GELU_ERF:
+ * times 1 + g^2 / 4; values below 2^-119 may be 0).  Written
+ * to `out` (contiguous) rounded to dtype, or as codes and scales, pqb_quantize's of the
+ * float32 v.  Inputs and v must be finite.  out may share no memory with the inputs.
+ * Shape rules: cols >= 1, at most 32768 for ROW scales; BLK_1x128 needs cols % 128 == 0,
+ * 16-byte aligned arrays and strides that are multiples of 8; strides in [cols, 2^40);
+ * rows * ceil(cols / 2048) < 2^22.  Errors, before any launch: as pqb_norm_quant. */
+typedef enum pqb_act_kind {
+  PQB_ACT_SILU = 0,
+  PQB_ACT_GELU_TANH = 1,
+  PQB_ACT_GELU_ERF = 2,
+  PQB_ACT_RELU2 = 3
+} pqb_act_kind;
+pqb_status pqb_act_quant(const void* gate, const void* up, pqb_dtype dtype, int64_t rows,
+                         int64_t cols, int64_t gate_stride, int64_t up_stride, pqb_act_kind act,
+                         int fmt, pqb_gran gran, void* out, float* scales, void* stream);
+
+/* Rotary positions of q and k (`dtype` [tokens, heads, dim], a token's heads and channels
+ * contiguous, tokens *_stride elements apart) into q_out and k_out.  With angle
+ * t = pos * angles[i], i < rot / 2, c = amplitude cos t, s = amplitude sin t:
+ *   (x0, x1) -> (x0 c - x1 s, x1 c + x0 s)
+ * for the pairs (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved != 0, of each head's
+ * first rot values; the others are copied.  angles f64 [rot / 2], radians per token: a
+ * scaled context is other angles (and amplitude).  The angle is taken in float64 and
+ * reduced there; c and s are within 2^-22 of their values for |t| < 2^28.
+ * positions i32 [tokens]; or NULL, and token t is at the place that a step of the paged
+ * cache gives it: request b owns tokens q_starts[b] .. q_starts[b + 1] - 1 (i32 [batch + 1],
+ * rising), the last of them at kv_lens[b] - 1 (i32 [batch]), as pqb_kv_plan_paged writes
+ * both; tokens outside every request are left as they were.  Both are read on the GPU.
+ * q_out may be q itself with the same stride, likewise k_out; no other overlap.  k NULL turns
+ * q only.
+ * Shape rules: tokens < 2^24; heads in [1, 8192] (k_heads 0 with k NULL); dim in [2, 1024];
+ * rot even, in [2, min(dim, 512)]; strides in [heads * dim, 2^40).  Addresses need
+ * element alignment; rot / 2 (rot if interleaved), dim and strides that are multiples of 8 on
+ * 16-byte aligned arrays are the fast form.  angles 8-byte aligned, amplitude finite (else
+ * PQB_ERR_VALUE).  Errors, before any launch: PQB_ERR_ENUM, PQB_ERR_SHAPE, PQB_ERR_VALUE,
+ * PQB_ERR_NULL, PQB_ERR_ALIGN. */
+typedef struct pqb_rope_args {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t tokens, q_heads, k_heads, dim, rot;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const int32_t* positions;
+  const int32_t* q_starts;
+  const int32_t* kv_lens;
+  int64_t batch;
+  const double* angles;
+  float amplitude;
+  int32_t interleaved;
+  int32_t dtype;    /* pqb_dtype */
+  int32_t reserved; /* must be 0 (else PQB_ERR_ENUM) */
+} pqb_rope_args;
+pqb_status pqb_rope(const pqb_rope_args* args, void* stream);
+
 /* Element codecs exposed for testing the rounding rules on arrays of float32:
  * E4M3 of y (round-to-nearest-even; |y| must not exceed 464) into one byte
  * per element; E2M1 of y (ties to the smaller magnitude, saturating at 6)

@@ -975,6 +975,220 @@ pqb_status pqb_gemm_w4a16_batch(const pqb_w4a16_job* jobs, int64_t njobs, int64_
       launch_w4a16_mfma(w.data(), (int)w.size(), m, out_dtype == PQB_BF16, (hipStream_t)stream));
 }
 
+// ---------------------------------------------------------------------------
+// The INT8 layer
+// ---------------------------------------------------------------------------
+constexpr int64_t kInt8MaxK = 131056, kInt8MaxStride = (int64_t)1 << 23, kInt8MaxRows = (int64_t)1 << 30;
+
+static bool int8_dims_ok(int64_t m, int64_t n, int64_t k) {
+  return m >= 0 && n >= 0 && k >= 0 && m < kInt8MaxRows && n < kInt8MaxRows && k % 16 == 0 && k <= kInt8MaxK &&
+         (m + 127) / 128 * ((n + 127) / 128) < (int64_t)1 << 23;
+}
+
+size_t pqb_gemm_int8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  return int8_dims_ok(m, n, k) ? gemm_int8_workspace_bytes(m, n, k) : 0;
+}
+
+pqb_status pqb_gemm_int8(const pqb_int8_mat* a, const pqb_int8_mat* b, int64_t k, const float* bias,
+                         pqb_dtype out_dtype, void* c, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  if (!valid_dtype(out_dtype)) return PQB_ERR_ENUM;
+  if (!a || !b) return PQB_ERR_NULL;
+  for (const pqb_int8_mat* m : {a, b})
+    if (m->reserved || (m->per_row != 0 && m->per_row != 1)) return PQB_ERR_ENUM;
+  if (!int8_dims_ok(a->rows, b->rows, k)) return PQB_ERR_SHAPE;
+  for (const pqb_int8_mat* m : {a, b})
+    if (m->stride < k || m->stride >= kInt8MaxStride || m->stride % 16) return PQB_ERR_SHAPE;
+  if (a->rows == 0 || b->rows == 0) return PQB_OK;
+  if (!c || !a->scales || !b->scales || (k > 0 && (!a->codes || !b->codes))) return PQB_ERR_NULL;
+  if (!aligned(c, 16) || !aligned(a->scales, 4) || !aligned(b->scales, 4) || !aligned(bias, 4) ||
+      !aligned(a->codes, 16) || !aligned(b->codes, 16))
+    return PQB_ERR_ALIGN;
+  const size_t need = gemm_int8_workspace_bytes(a->rows, b->rows, k);
+  if (need) {
+    if (!workspace) return PQB_ERR_NULL;
+    if (workspace_bytes < need) return PQB_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return PQB_ERR_ALIGN;
+  }
+  Int8Args g{};
+  g.a = a->codes;
+  g.b = b->codes;
+  g.a_scales = a->scales;
+  g.b_scales = b->scales;
+  g.bias = bias;
+  g.a_stride = a->stride;
+  g.b_stride = b->stride;
+  g.a_step = a->per_row;
+  g.b_step = b->per_row;
+  g.M = (int32_t)a->rows;
+  g.N = (int32_t)b->rows;
+  g.K = (int32_t)k;
+  g.c = c;
+  return hip_status(launch_gemm_int8(g, out_dtype == PQB_BF16, workspace, (hipStream_t)stream));
+}
+
+constexpr int64_t kLayerMaxStride = (int64_t)1 << 40;
+
+// Format and scope of a fused quantization: its LayerForm and element kind.
+static pqb_status layer_form(int fmt, int gran, int32_t* form, int32_t* elem) {
+  *elem = 0;
+  if (fmt == PQB_PLAIN) {
+    *form = kFormPlain;
+    return PQB_OK;
+  }
+  if (!known_format(fmt) || !known_gran(gran)) return PQB_ERR_ENUM;
+  if (!one_byte(fmt) || !valid_pair(fmt, gran) || (gran != PQB_ROW && gran != PQB_BLK_1x128)) return PQB_ERR_COMBO;
+  *form = gran == PQB_ROW ? kFormRow : kFormBlk;
+  *elem = elem_of(fmt);
+  return PQB_OK;
+}
+
+static pqb_status layer_dims(int64_t rows, int64_t cols, int32_t form) {
+  if (rows < 0 || cols < 1 || cols > INT32_MAX - 2048 || (form == kFormBlk && cols % 128)) return PQB_ERR_SHAPE;
+  if (rows >= (int64_t)1 << 22 || rows * ((cols + 2047) / 2048) >= (int64_t)1 << 22) return PQB_ERR_SHAPE;
+  return PQB_OK;
+}
+
+// Whether an array's rows allow 16-byte accesses; clears `vec` if not, `ok` if not even its
+// elements are aligned.
+static void layer_array(const void* p, int64_t stride, int64_t es, bool* vec, bool* ok) {
+  if (!aligned(p, 16) || stride % 8) *vec = false;
+  if (!aligned(p, (uintptr_t)es)) *ok = false;
+}
+
+pqb_status pqb_norm_quant(const pqb_norm* n, void* stream) {
+  if (!n) return PQB_ERR_NULL;
+  if (!valid_dtype(n->dtype) || n->reserved || (n->kind != PQB_NORM_RMS && n->kind != PQB_NORM_LAYER))
+    return PQB_ERR_ENUM;
+  NormArgs a{};
+  pqb_status e = layer_form(n->fmt, n->gran, &a.form, &a.elem);
+  if (e == PQB_OK) e = layer_dims(n->rows, n->cols, a.form);
+  if (e != PQB_OK) return e;
+  const int64_t rows = n->rows, cols = n->cols;
+  if (cols > kLayerMaxCols) return PQB_ERR_SHAPE;
+  const bool adds = n->residual || n->gate || n->post_weight;
+  auto stride_ok = [&](const void* p, int64_t s) { return !p || (s >= cols && s < kLayerMaxStride); };
+  if (!stride_ok(n->x, n->x_stride) || !stride_ok(n->residual, n->residual_stride) ||
+      !stride_ok(n->gate, n->gate_stride) || !stride_ok(n->h, n->h_stride))
+    return PQB_ERR_SHAPE;
+  if (n->gate && (n->gate_rows < 1 || rows % n->gate_rows)) return PQB_ERR_SHAPE;
+  if (!(n->eps > 0.0f && n->eps <= 1.0f) || !(n->residual_scale - n->residual_scale == 0.0f)) return PQB_ERR_VALUE;
+  if (n->bias && n->kind != PQB_NORM_LAYER) return PQB_ERR_NULL;
+  if (rows == 0) return PQB_OK;
+  if (!n->x || !n->out || (a.form != kFormPlain && !n->scales) || adds != (n->h != nullptr)) return PQB_ERR_NULL;
+  const int64_t es = n->dtype == PQB_BF16 ? 2 : 4;
+  bool vec = cols % 8 == 0, ok = aligned(n->scales, 4);
+  layer_array(n->out, cols, a.form == kFormPlain ? es : 1, &vec, &ok);
+  const struct { const void* p; int64_t stride; } arrays[] = {
+      {n->x, n->x_stride}, {n->residual, n->residual_stride}, {n->gate, n->gate_stride}, {n->h, n->h_stride},
+      {n->post_weight, 0}, {n->weight, 0}, {n->bias, 0}};
+  for (const auto& r : arrays)
+    if (r.p) layer_array(r.p, r.stride, es, &vec, &ok);
+  if (!ok || (a.form == kFormBlk && !vec)) return PQB_ERR_ALIGN;
+  a.x = n->x;
+  a.residual = n->residual;
+  a.gate = n->gate;
+  a.post = n->post_weight;
+  a.weight = n->weight;
+  a.bias = n->bias;
+  a.h = n->h;
+  a.out = n->out;
+  a.scales = n->scales;
+  a.rows = rows;
+  a.x_stride = n->x_stride;
+  a.res_stride = n->residual_stride;
+  a.gate_stride = n->gate_stride;
+  a.h_stride = n->h_stride;
+  a.cols = (int32_t)cols;
+  a.per_gate = n->gate ? (uint32_t)(rows / n->gate_rows) : 0;
+  a.res_scale = n->residual_scale;
+  a.eps = n->eps;
+  a.layer = n->kind == PQB_NORM_LAYER;
+  return hip_status(launch_norm(a, n->dtype == PQB_BF16, vec, (hipStream_t)stream));
+}
+
+pqb_status pqb_act_quant(const void* gate, const void* up, pqb_dtype dtype, int64_t rows,
+                         int64_t cols, int64_t gate_stride, int64_t up_stride, pqb_act_kind act,
+                         int fmt, pqb_gran gran, void* out, float* scales, void* stream) {
+  if (!valid_dtype(dtype) || act < PQB_ACT_SILU || act > PQB_ACT_RELU2) return PQB_ERR_ENUM;
+  ActArgs a{};
+  pqb_status e = layer_form(fmt, gran, &a.form, &a.elem);
+  if (e == PQB_OK) e = layer_dims(rows, cols, a.form);
+  if (e != PQB_OK) return e;
+  if (a.form == kFormRow && cols > kLayerMaxCols) return PQB_ERR_SHAPE;
+  if (gate_stride < cols || gate_stride >= kLayerMaxStride) return PQB_ERR_SHAPE;
+  if (up && (up_stride < cols || up_stride >= kLayerMaxStride)) return PQB_ERR_SHAPE;
+  if (rows == 0) return PQB_OK;
+  if (!gate || !out || (a.form != kFormPlain && !scales)) return PQB_ERR_NULL;
+  const int64_t es = dtype == PQB_BF16 ? 2 : 4;
+  bool vec = cols % 8 == 0, ok = aligned(scales, 4);
+  layer_array(gate, gate_stride, es, &vec, &ok);
+  if (up) layer_array(up, up_stride, es, &vec, &ok);
+  layer_array(out, cols, a.form == kFormPlain ? es : 1, &vec, &ok);
+  if (!ok || (a.form == kFormBlk && !vec)) return PQB_ERR_ALIGN;
+  a.gate = gate;
+  a.up = up;
+  a.out = out;
+  a.scales = scales;
+  a.rows = rows;
+  a.gate_stride = gate_stride;
+  a.up_stride = up_stride;
+  a.cols = (int32_t)cols;
+  a.act = act;
+  return hip_status(launch_act(a, dtype == PQB_BF16, vec, (hipStream_t)stream));
+}
+
+pqb_status pqb_rope(const pqb_rope_args* r, void* stream) {
+  if (!r) return PQB_ERR_NULL;
+  if (!valid_dtype(r->dtype) || r->reserved) return PQB_ERR_ENUM;
+  const int64_t dim = r->dim, rot = r->rot;
+  if (r->tokens < 0 || r->tokens >= 1 << 24 || dim < 2 || dim > 1024 || rot < 2 || rot % 2 || rot > dim ||
+      rot > kRopeMaxRot || r->q_heads < 1 || r->q_heads > 8192 || r->k_heads < 0 || r->k_heads > 8192 ||
+      (r->k_heads > 0) != (r->k != nullptr || r->k_out != nullptr) || r->batch < 0 || r->batch >= 1 << 30)
+    return PQB_ERR_SHAPE;
+  auto stride_ok = [&](int64_t s, int64_t heads) { return s >= heads * dim && s < kLayerMaxStride; };
+  if (!stride_ok(r->q_stride, r->q_heads) || !stride_ok(r->q_out_stride, r->q_heads)) return PQB_ERR_SHAPE;
+  if (r->k_heads && (!stride_ok(r->k_stride, r->k_heads) || !stride_ok(r->k_out_stride, r->k_heads)))
+    return PQB_ERR_SHAPE;
+  if (!(r->amplitude - r->amplitude == 0.0f)) return PQB_ERR_VALUE;
+  if (r->tokens == 0) return PQB_OK;
+  if (!r->q || !r->q_out || !r->angles || (r->k_heads && (!r->k || !r->k_out))) return PQB_ERR_NULL;
+  if (!r->positions && r->batch == 0) return PQB_OK;  // no request owns a token
+  if (!r->positions && (!r->q_starts || !r->kv_lens)) return PQB_ERR_NULL;
+  const int64_t es = r->dtype == PQB_BF16 ? 2 : 4;
+  bool vec = dim % 8 == 0 && (r->interleaved ? rot : rot / 2) % 8 == 0;
+  bool ok = aligned(r->angles, 8) && aligned(r->positions, 4) && aligned(r->q_starts, 4) && aligned(r->kv_lens, 4);
+  layer_array(r->q, r->q_stride, es, &vec, &ok);
+  layer_array(r->q_out, r->q_out_stride, es, &vec, &ok);
+  if (r->k_heads) {
+    layer_array(r->k, r->k_stride, es, &vec, &ok);
+    layer_array(r->k_out, r->k_out_stride, es, &vec, &ok);
+  }
+  if (!ok) return PQB_ERR_ALIGN;
+  RopeArgs a{};
+  a.x[0] = r->q;
+  a.x[1] = r->k;
+  a.out[0] = r->q_out;
+  a.out[1] = r->k_out;
+  a.stride[0] = r->q_stride;
+  a.stride[1] = r->k_stride;
+  a.out_stride[0] = r->q_out_stride;
+  a.out_stride[1] = r->k_out_stride;
+  a.heads[0] = (int32_t)r->q_heads;
+  a.heads[1] = (int32_t)r->k_heads;
+  a.tokens = r->tokens;
+  a.dim = (int32_t)dim;
+  a.rot = (int32_t)rot;
+  a.interleaved = r->interleaved != 0;
+  a.positions = r->positions;
+  a.starts = r->q_starts;
+  a.kv_lens = r->kv_lens;
+  a.batch = r->batch;
+  a.angles = r->angles;
+  a.amplitude = r->amplitude;
+  return hip_status(launch_rope(a, r->dtype == PQB_BF16, vec, (hipStream_t)stream));
+}
+
 pqb_status pqb_encode_e4m3(const float* y, int64_t n, uint8_t* out, void* stream) {
   if (n < 0) return PQB_ERR_SHAPE;
   if (n == 0) return PQB_OK;

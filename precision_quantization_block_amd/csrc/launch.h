@@ -240,6 +240,63 @@ size_t attend_workspace_bytes(int64_t q_rows, int64_t batch, int64_t heads, int6
 hipError_t launch_attend(AttendArgs a, bool bf16, int head_dim, int64_t max_rows, void* workspace,
                          hipStream_t st);
 
+// ---- between the products (k_layer.hip) ---------------------------------------
+// Rows of up to kLayerMaxCols values; `vec`: widths, strides and addresses are
+// multiples of 8 elements and 16 bytes.
+constexpr int kLayerMaxCols = 32768;
+enum LayerForm { kFormPlain = 0, kFormRow = 1, kFormBlk = 2 };
+enum ActKind { kActSilu = 0, kActGeluTanh = 1, kActGeluErf = 2, kActRelu2 = 3 };
+struct NormArgs {
+  const void *x, *residual, *gate, *post, *weight, *bias;   // NULL: not there
+  void *h, *out;                                            // h NULL: nothing is added to x
+  float* scales;
+  int64_t rows, x_stride, res_stride, gate_stride, h_stride;  // strides in elements
+  int32_t cols;
+  uint32_t per_gate;                                        // rows that share a row of gate
+  float res_scale, eps;
+  int32_t layer, form, elem;                                // LayerForm; Elem of quant.h
+};
+hipError_t launch_norm(const NormArgs& a, bool bf16, bool vec, hipStream_t st);
+struct ActArgs {
+  const void *gate, *up;                                    // up NULL: not gated
+  void* out;
+  float* scales;
+  int64_t rows, gate_stride, up_stride;
+  int32_t cols, act, form, elem;
+};
+hipError_t launch_act(const ActArgs& a, bool bf16, bool vec, hipStream_t st);
+
+// ---- rotary positions (k_rope.hip) --------------------------------------------
+constexpr int kRopeMaxRot = 512;                            // rotated values of a head
+struct RopeArgs {
+  const void *x[2];                                         // q, k: [tokens, heads, dim]
+  void* out[2];
+  int64_t stride[2], out_stride[2];                         // elements between tokens
+  int32_t heads[2];
+  int64_t tokens;
+  int32_t dim, rot, interleaved;
+  const int32_t* positions;                                 // [tokens], or NULL:
+  const int32_t *starts, *kv_lens;                          // [batch + 1], [batch]
+  int64_t batch;
+  const double* angles;                                     // [rot / 2] radians per token
+  float amplitude;
+};
+hipError_t launch_rope(const RopeArgs& a, bool bf16, bool vec, hipStream_t st);
+
+// ---- INT8 product (k_gemm_int8.hip) -------------------------------------------
+struct Int8Args {
+  const int8_t *a, *b;                                      // [M, K], [N, K]
+  const float *a_scales, *b_scales, *bias;                  // bias NULL: none
+  int64_t a_stride, b_stride;                               // bytes, multiples of 16
+  int32_t a_step, b_step;                                   // 1: a scale per row, 0: one scale
+  int32_t M, N, K;                                          // K % 16 == 0
+  void* c;
+  int32_t* part;                                            // set by the launcher: split sums
+  int32_t splits, per_split;                                // K blocks per split
+};
+size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_int8(Int8Args g, bool out_bf16, void* workspace, hipStream_t st);
+
 // ---- division checks (k_check.hip) -----------------------------------------
 hipError_t launch_check_recip(uint32_t first, int64_t n, float* out, hipStream_t st);
 hipError_t launch_check_div(const float* s, int64_t ns, uint32_t x_first, int64_t nx, float* out,

@@ -65,6 +65,28 @@ class _KvPages(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class _Int8Mat(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("per_row", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in "x residual gate post_weight weight bias h out scales".split()] \
+        + [(n, ctypes.c_int64) for n in
+           "rows cols gate_rows x_stride residual_stride gate_stride h_stride".split()] \
+        + [("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)] \
+        + [(n, ctypes.c_int32) for n in "dtype kind fmt gran reserved".split()]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in "q k q_out k_out".split()] \
+        + [(n, ctypes.c_int64) for n in "tokens q_heads k_heads dim rot q_stride k_stride q_out_stride "
+                                        "k_out_stride".split()] \
+        + [(n, ctypes.c_void_p) for n in "positions q_starts kv_lens".split()] \
+        + [("batch", ctypes.c_int64), ("angles", ctypes.c_void_p), ("amplitude", ctypes.c_float)] \
+        + [(n, ctypes.c_int32) for n in "interleaved dtype reserved".split()]
+
+
 class _Sizes(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_size_t), ("scales", ctypes.c_size_t),
                 ("aux", ctypes.c_size_t), ("workspace", ctypes.c_size_t)]
@@ -114,6 +136,13 @@ def lib():
         L.pqb_gemv_w4a16_batch.argtypes = [ctypes.POINTER(_W4Job), I64, I64, I, P]
         L.pqb_gemm_w4a16.argtypes = [P, I64, P, P, P, I64, I64, I, P, P]
         L.pqb_gemm_w4a16_batch.argtypes = [ctypes.POINTER(_W4Job), I64, I64, I, P]
+        MAT = ctypes.POINTER(_Int8Mat)
+        L.pqb_gemm_int8_workspace_bytes.argtypes = [I64, I64, I64]
+        L.pqb_gemm_int8_workspace_bytes.restype = SZ
+        L.pqb_gemm_int8.argtypes = [MAT, MAT, I64, P, I, P, P, SZ, P]
+        L.pqb_norm_quant.argtypes = [ctypes.POINTER(_Norm), P]
+        L.pqb_act_quant.argtypes = [P, P, I, I64, I64, I64, I64, I, I, I, P, P, P]
+        L.pqb_rope.argtypes = [ctypes.POINTER(_Rope), P]
         L.pqb_encode_e4m3.argtypes = [P, I64, P, P]
         L.pqb_encode_e5m2.argtypes = [P, I64, P, P]
         L.pqb_encode_e2m1.argtypes = [P, I64, P, P]
@@ -126,7 +155,7 @@ def lib():
                   "pqb_kv_attend_paged", "pqb_gemm_fp8_blockscaled",
                   "pqb_gemm_fp8_blockscaled_quant", "pqb_gemv_w4a16",
                   "pqb_gemv_w4a16_batch", "pqb_gemm_mxfp4", "pqb_gemm_nvfp4", "pqb_stream_reference", "pqb_gemm_w4a16",
-                  "pqb_gemm_w4a16_batch",
+                  "pqb_gemm_w4a16_batch", "pqb_gemm_int8", "pqb_norm_quant", "pqb_act_quant", "pqb_rope",
                   "pqb_encode_e4m3", "pqb_encode_e5m2", "pqb_encode_e2m1",
                   "pqb_check_recip", "pqb_check_div"):
             getattr(L, f).restype = I
@@ -693,6 +722,407 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
     if status:
         raise PqbError(status, "kv_attend_paged")
     return out
+
+
+# --------------------------------------------------------------------------
+# the INT8 layer: its product, and what lies between a layer's products
+# --------------------------------------------------------------------------
+
+NORM_KINDS = {"rms": 0, "layer": 1}
+ACT_KINDS = {"silu": 0, "gelu_tanh": 1, "gelu_erf": 2, "relu2": 3}
+_I8 = torch.int8
+
+
+def _int8_mat(m, name, dev=None):
+    """(struct, tensors it points into, device, k) of a Quantized, or of a (codes, scales) pair."""
+    if isinstance(m, Quantized):
+        if m.fmt != "int8_sym":
+            raise ValueError(f"{name} must hold int8_sym codes, not {m.fmt}")
+        codes, scales = m.codes, m.scales
+        b, r, k = m.shape
+        rows, stride = b * r, k
+        if not isinstance(codes, torch.Tensor) or codes.numel() != rows * k or not codes.is_contiguous():
+            raise ValueError(f"{name} codes must be contiguous and hold {rows} x {k} bytes")
+    else:
+        codes, scales = m
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+            raise ValueError(f"{name} codes must be a [rows, k] tensor")
+        rows, k = codes.shape
+        stride, one = codes.stride()
+        if rows < 2:
+            stride = k
+        if (one != 1 and k > 1) or stride < k or stride & 15 or codes.data_ptr() & 15:
+            codes, stride = codes.clone(memory_format=torch.contiguous_format), k
+    if dev is None:
+        dev = codes.device
+    if codes.device != dev or dev.type != "cuda" or (codes.dtype is not _I8 and codes.dtype is not _U8):
+        _refuse(dev, (_I8, _U8), f"{name}_codes", codes, contiguous=False)
+    if not _ready(dev, _F32, scales):
+        _refuse(dev, (_F32,), f"{name}_scales", scales)
+    per_row = scales.numel()
+    if per_row != rows and per_row != 1:
+        raise ValueError(f"{name} needs a scale per row, or one")
+    return _Int8Mat(codes.data_ptr(), scales.data_ptr(), rows, stride, per_row == rows, 0), (codes, scales), dev, k
+
+
+def gemm_int8(a, b, out_dtype=torch.bfloat16, *, bias: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """C [M, N] = (A B^T) of symmetric INT8 codes, summed exactly as integers, times the
+    scale of A's row and of B's row, plus bias float32 [N].  a and b: a Quantized from
+    quantize(x, "int8_sym") (per row or per tensor), norm_quant or act_quant, or a (codes
+    [rows, K] int8 or uint8, scales float32 [rows] or [1]) pair whose rows may lie apart (a
+    copy is made unless that is by multiples of 16 bytes).  K is a multiple of 16.  workspace:
+    memory to use instead of an allocation per call (any contiguous tensor of
+    pqb_gemm_int8_workspace_bytes; calls that overlap need one each).  out may share no
+    memory with the operands."""
+    am, keep_a, dev, K = _int8_mat(a, "a")
+    bm, keep_b, _, kb = _int8_mat(b, "b", dev)
+    if K != kb:
+        raise ValueError(f"a and b must share K, got {K} and {kb}")
+    M, N = am.rows, bm.rows
+    if out_dtype is not _BF16 and out_dtype is not _F32:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+    if bias is not None:
+        if not _ready(dev, _F32, bias):
+            _refuse(dev, (_F32,), "bias", bias)
+        if bias.numel() != N:
+            raise ValueError("bias must hold a value per row of b")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    elif not _ready(dev, out_dtype, out) or out.shape != (M, N):
+        raise ValueError("out must be a contiguous [M, N] tensor of out_dtype")
+    elif any(_share(out, t) for t in (*keep_a, *keep_b, bias)):
+        raise ValueError("out must not share memory with the operands")
+    L = lib()
+    need = L.pqb_gemm_int8_workspace_bytes(M, N, K)
+    workspace, have = _workspace(workspace, need, dev)
+    status = _call_on(dev, L.pqb_gemm_int8, ctypes.byref(am), ctypes.byref(bm), K,
+                      None if bias is None else bias.data_ptr(), BF16 if out_dtype is _BF16 else F32,
+                      out.data_ptr(), None if workspace is None else workspace.data_ptr(), have)
+    if status:
+        raise PqbError(status, "gemm_int8")
+    return out
+
+
+def _workspace(workspace, need: int, dev):
+    """The caller's workspace or a new one, and its bytes."""
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
+    if isinstance(workspace, torch.Tensor) and _ready(dev, workspace.dtype, workspace):
+        return workspace, workspace.numel() * workspace.element_size()
+    raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+
+
+def _span(t):
+    """First and last byte (exclusive) that a tensor reaches."""
+    if t.numel() == 0:
+        return 0, 0
+    es, at = t.element_size(), t.data_ptr()
+    return at, at + es * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+
+
+def _share(t, other) -> bool:
+    """Whether the spans of two tensors meet."""
+    if t is None or other is None:
+        return False
+    (a, b), (c, d) = _span(t), _span(other)
+    return a < d and c < b
+
+
+def _rows_share(t, stride, other, other_stride) -> bool:
+    """Whether rows (first dimension) of two tensors, `stride` and `other_stride` elements of one
+    size apart and each contiguous, may share memory.  Rows of one stride may lie in each
+    other's gaps, as the parts of a fused projection do."""
+    if not _share(t, other):
+        return False
+    if t.shape[0] < 2 and other.shape[0] < 2:
+        return True
+    if t.shape[0] > 1 and other.shape[0] > 1 and stride != other_stride:
+        return True
+    step = stride if t.shape[0] > 1 else other_stride
+    es = t.element_size()
+    gap = (other.data_ptr() - t.data_ptr()) % (step * es)
+    return gap < t.numel() // t.shape[0] * es or gap + other.numel() // other.shape[0] * es > step * es
+
+
+def _layer_rows(t, name, dev, dtype, cols, block):
+    """t [..., cols] as rows a stride apart (copied if they are not, or where 1x128 blocks
+    need 16-byte alignment and have none): the tensor, its rows and their stride."""
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype is not dtype:
+        _refuse(dev, (dtype,), name, t, contiguous=False)
+    if t.dim() != 2:
+        t = t.reshape(-1, t.shape[-1]) if t.dim() else t.reshape(1, 1)
+    rows, c = t.shape
+    if c != cols:
+        raise ValueError(f"{name} must have {cols} columns, got {c}")
+    stride, one = t.stride()
+    if rows < 2:
+        stride = cols
+    if (one != 1 and cols > 1) or stride < cols or block and (stride & 7 or t.data_ptr() & 15):
+        t, stride = t.clone(memory_format=torch.contiguous_format), cols
+    return t, rows, stride
+
+
+def _layer_out(fmt, gran, rows, cols, like, dev):
+    """fmt and gran as numbers, and what a fused quantization of [rows, cols] writes: the
+    Quantized (or plain tensor), its codes and its scales."""
+    if fmt is None:
+        out = torch.empty(like.shape, dtype=like.dtype, device=dev)
+        return -1, 0, out, out, None
+    gran = gran or DEFAULT_GRAN.get(fmt, "row")
+    f, g = _fmt(fmt), _gran(gran)
+    codes = torch.empty(rows * cols, dtype=_U8, device=dev)
+    scales = torch.empty(rows * (cols // 128) if g == 2 else rows, dtype=_F32, device=dev)
+    return f, g, Quantized(codes, scales, None, fmt, gran, (1, rows, cols)), codes, scales
+
+
+def norm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, fmt: str | None = "int8_sym",
+               gran: str | None = None, *, kind: str = "rms", bias: torch.Tensor | None = None,
+               eps: float = 1e-6, residual: torch.Tensor | None = None, residual_scale: float = 1.0,
+               gate: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+               h_out: torch.Tensor | None = None):
+    """The residual stream h = gate * y + residual_scale * residual, y = x or its norm times
+    post_weight, then h's norm times weight (plus bias), quantized for the next product, in
+    one launch.  x [..., cols] float32 or bf16, the others of its dtype: residual of x's shape,
+    weights and bias [cols], gate [g, cols] with g dividing the rows (a gate per sequence or
+    token).  kind: "rms" or "layer".  fmt and gran: "int8_sym" per "row", "fp8_e4m3" or
+    "fp8_e5m2" per "row" or "1x128"; None: no quantization.
+    Returns (Quantized, or a tensor like x with fmt None; h, or None where x is h).  An RMS norm's
+    codes are those of h * weight (the row's 1 / rms is in its scale).  h_out: where h goes, like x;
+    it may be x or residual itself, and shares no other memory with the inputs."""
+    dev, dtype = _device_of(x, "x"), x.dtype
+    shape = x.shape
+    cols = shape[-1] if len(shape) else 1
+    block = fmt is not None and gran == "1x128"
+    a = _Norm()
+    x2, rows, a.x_stride = _layer_rows(x, "x", dev, dtype, cols, block)
+    keep = [x2]
+    a.x, a.rows, a.cols = x2.data_ptr(), rows, cols
+    adds = False
+    res = None
+    if residual is not None:
+        res, n, a.residual_stride = _layer_rows(residual, "residual", dev, dtype, cols, block)
+        if n != rows:
+            raise ValueError("residual must have x's shape")
+        a.residual = res.data_ptr()
+        keep.append(res)
+        adds = True
+    if gate is not None:
+        g, a.gate_rows, a.gate_stride = _layer_rows(gate, "gate", dev, dtype, cols, block)
+        if a.gate_rows < 1 or rows % a.gate_rows:
+            raise ValueError("gate must have a number of rows that divides x's")
+        a.gate = g.data_ptr()
+        keep.append(g)
+        adds = True
+    for name, w in (("post_weight", post_weight), ("weight", weight), ("bias", bias)):
+        if w is not None:
+            if not _ready(dev, dtype, w):
+                _refuse(dev, (dtype,), name, w)
+            if w.numel() != cols:
+                raise ValueError(f"{name} must have {cols} values")
+            if block and w.data_ptr() & 15:
+                w = w.clone()
+            setattr(a, name, w.data_ptr())
+            keep.append(w)
+    adds = adds or post_weight is not None
+    h = None
+    if adds:
+        if h_out is None:
+            h = torch.empty(shape, dtype=dtype, device=dev)
+            a.h_stride = cols
+        else:
+            h = h_out
+            h2, n, a.h_stride = _layer_rows(h, "h_out", dev, dtype, cols, block)
+            if h.shape != shape or h2.data_ptr() != h.data_ptr():
+                raise ValueError("h_out must be like x, its rows at a stride that can be used as it is")
+            for t, stride in ((x2, a.x_stride), (res, a.residual_stride)):
+                if t is not None and _rows_share(h2, a.h_stride, t, stride) \
+                        and (t.data_ptr() != h.data_ptr() or stride != a.h_stride):
+                    raise ValueError("h_out may be x or residual itself, but not overlap them otherwise")
+            if any(_share(h, t) for t in keep if t is not x2 and t is not res):
+                raise ValueError("h_out must not share memory with a gate, weight or bias")
+        a.h = h.data_ptr()
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual, gate or post_weight")
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind must be one of {tuple(NORM_KINDS)}")
+    if bias is not None and kind != "layer":
+        raise ValueError("a bias goes with a layer norm")
+    a.fmt, a.gran, result, codes, scales = _layer_out(fmt, gran, rows, cols, x, dev)
+    a.out = codes.data_ptr()
+    if scales is not None:
+        a.scales = scales.data_ptr()
+    a.residual_scale, a.eps, a.kind = residual_scale, eps, NORM_KINDS[kind]
+    a.dtype = BF16 if dtype is _BF16 else F32
+    status = _call_on(dev, lib().pqb_norm_quant, ctypes.byref(a))
+    if status:
+        raise PqbError(status, "norm_quant")
+    return result, h
+
+
+def act_quant(gate: torch.Tensor, up: torch.Tensor | None = None, fmt: str | None = "int8_sym",
+              gran: str | None = None, *, act: str = "silu"):
+    """act(gate) * up (act(gate) alone without up), quantized for the next product in one
+    launch.  gate and up [..., cols] float32 or bf16, rows at any stride (e.g. the halves of a
+    fused projection's output).  act: "silu", "gelu_tanh", "gelu_erf" or "relu2".  fmt and
+    gran as for norm_quant; returns a Quantized, or a tensor like gate with fmt None."""
+    dev, dtype = _device_of(gate, "gate"), gate.dtype
+    shape = gate.shape
+    cols = shape[-1] if len(shape) else 1
+    block = fmt is not None and gran == "1x128"
+    g, rows, g_stride = _layer_rows(gate, "gate", dev, dtype, cols, block)
+    u, u_stride = None, 0
+    if up is not None:
+        if not isinstance(up, torch.Tensor) or up.shape != shape:
+            raise ValueError("up must have gate's shape")
+        u, _, u_stride = _layer_rows(up, "up", dev, dtype, cols, block)
+    if act not in ACT_KINDS:
+        raise ValueError(f"act must be one of {tuple(ACT_KINDS)}")
+    f, gr, result, codes, scales = _layer_out(fmt, gran, rows, cols, gate, dev)
+    status = _call_on(dev, lib().pqb_act_quant, g.data_ptr(), None if u is None else u.data_ptr(),
+                      BF16 if dtype is _BF16 else F32, rows, cols, g_stride, u_stride, ACT_KINDS[act], f, gr,
+                      codes.data_ptr(), None if scales is None else scales.data_ptr())
+    if status:
+        raise PqbError(status, "act_quant")
+    return result
+
+
+@dataclass(slots=True)
+class RopeTable:
+    """What rotary positions turn by: radians per token of each pair, the factor of
+    cosine and sine, and which values make a pair."""
+    angles: torch.Tensor     # float64 [rotary_dim / 2] on the GPU
+    amplitude: float = 1.0
+    interleaved: bool = False
+
+
+def rope_table(rotary_dim: int, base: float = 10000.0, *, interleaved: bool = False,
+               scaling: str | None = None, factor: float = 1.0, original_length: int = 8192,
+               low: float | None = None, high: float | None = None, amplitude: float | None = None,
+               device="cuda") -> RopeTable:
+    """The RopeTable of base^(-2 i / rotary_dim) radians per token, scaled for long contexts:
+      None       as they are
+      "linear"   all divided by factor
+      "ntk"      base * factor^(rotary_dim / (rotary_dim - 2)): the slowest pair divided by
+                 factor, the fastest kept
+      "by_turns" pairs that make at least `high` turns over original_length tokens (4 by default)
+                 kept, those of at most `low` (1) divided by factor, in between a mean weighted
+                 by the share of the way in turns
+      "yarn"     the same with the share of the way in the pair's index (high 32 and low 1
+                 turns), and amplitude 1 + 0.1 ln(factor)
+    amplitude, if given, is used instead."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    if not (factor > 0 and base > 0 and original_length > 0):
+        raise ValueError("base, factor and original_length must be positive")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    amp = 1.0
+    if scaling == "ntk":
+        if rotary_dim == 2:
+            raise ValueError("ntk needs a rotary_dim over 2")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = float(base) ** (-2.0 * i / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("by_turns", "yarn"):
+        high = (4.0 if scaling == "by_turns" else 32.0) if high is None else high
+        low = 1.0 if low is None else low
+        if not 0 < low < high:
+            raise ValueError("0 < low < high is needed")
+        if scaling == "by_turns":
+            keep = (original_length * f / (2 * math.pi) - low) / (high - low)
+        else:   # the (whole) indices of the pairs that make `high` and `low` turns
+            at = [rotary_dim * math.log(original_length / (2 * math.pi * n)) / (2 * math.log(base))
+                  for n in (high, low)]
+            first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rotary_dim - 1)
+            keep = 1 - (i - first) / max(last - first, 0.001)
+            amp = 1.0 + 0.1 * math.log(factor) if factor > 1 else 1.0
+        keep = keep.clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    elif scaling not in (None, "ntk"):
+        raise ValueError("scaling must be None, linear, ntk, by_turns or yarn")
+    return RopeTable(f.to(device), amp if amplitude is None else amplitude, interleaved)
+
+
+def _rope_rows(x, name, dev, dtype):
+    """x [tokens, heads, dim] with a token's values contiguous (copied if not), its token stride."""
+    if not isinstance(x, torch.Tensor) or x.device != dev or x.dtype is not dtype:
+        _refuse(dev, (dtype,), name, x, contiguous=False)
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim]")
+    T, H, D = x.shape
+    ld, head, one = x.stride()
+    row = H * D
+    if T < 2:
+        ld = row
+    if (one == 1 or D == 1) and (head == D or H == 1) and ld >= row or not x.numel():
+        return x, max(ld, row)
+    return x.clone(memory_format=torch.contiguous_format), row
+
+
+def _rope_out(out, x, x2, stride, name):
+    """Where x's turned values go, and their stride."""
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[1] * x.shape[2]
+    o2, o_stride = _rope_rows(out, name, x.device, x.dtype)
+    if out.shape != x.shape or o2 is not out:
+        raise ValueError(f"{name} must be like its input, a token's values contiguous")
+    if _rows_share(out, o_stride, x2, stride) and (out.data_ptr() != x2.data_ptr() or o_stride != stride):
+        raise ValueError(f"{name} may be its input itself, but not overlap it otherwise")
+    return out, o_stride
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions, table: RopeTable, *,
+         q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """q and k [tokens, heads, dim] (float32 or bf16, tokens at any stride, e.g. parts of one
+    fused projection) turned by their positions' angles: the first 2 * len(table.angles) values
+    of each head, the rest copied.  positions: int32 [tokens], or the PagedPlan of the step, which
+    places token t where the paged cache does (tokens outside every request are left as they
+    were in the outputs).  q_out and k_out may be q and k themselves.  Returns (q_out, k_out), k_out
+    None without k."""
+    dev, dtype = _device_of(q, "q"), q.dtype
+    a = _Rope()
+    q2, a.q_stride = _rope_rows(q, "q", dev, dtype)
+    T, H, D = q2.shape
+    a.tokens, a.q_heads, a.dim = T, H, D
+    q_out, a.q_out_stride = _rope_out(q_out, q, q2, a.q_stride, "q_out")
+    a.q, a.q_out = q2.data_ptr(), q_out.data_ptr()
+    k2 = None
+    if k is not None:
+        k2, a.k_stride = _rope_rows(k, "k", dev, dtype)
+        if k2.shape[0] != T or k2.shape[2] != D:
+            raise ValueError("q and k must share tokens and dim")
+        a.k_heads = k2.shape[1]
+        k_out, a.k_out_stride = _rope_out(k_out, k, k2, a.k_stride, "k_out")
+        a.k, a.k_out = k2.data_ptr(), k_out.data_ptr()
+        if T and (_rows_share(q_out, a.q_out_stride, k2, a.k_stride)
+                  or _rows_share(k_out, a.k_out_stride, q2, a.q_stride)
+                  or _rows_share(q_out, a.q_out_stride, k_out, a.k_out_stride)):
+            raise ValueError("q_out and k_out must not share memory with each other's tokens")
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    angles = table.angles
+    if not _ready(dev, torch.float64, angles):
+        _refuse(dev, (torch.float64,), "table.angles", angles)
+    if isinstance(positions, PagedPlan):
+        starts, lens = positions.q_starts, positions.kv_lens
+        if not _ready(dev, _I32, starts, lens):
+            _refuse(dev, (_I32,), "q_starts kv_lens", starts, lens)
+        if starts.numel() != lens.numel() + 1:
+            raise ValueError("the plan must hold batch + 1 starts and batch lengths")
+        a.q_starts, a.kv_lens, a.batch = starts.data_ptr(), lens.data_ptr(), lens.numel()
+    else:
+        if not _ready(dev, _I32, positions):
+            _refuse(dev, (_I32,), "positions", positions)
+        if positions.numel() != T:
+            raise ValueError("positions must hold a value per token")
+        a.positions = positions.data_ptr()
+    a.rot, a.angles, a.amplitude = 2 * angles.numel(), angles.data_ptr(), table.amplitude
+    a.interleaved, a.dtype = bool(table.interleaved), BF16 if dtype is _BF16 else F32
+    status = _call_on(dev, lib().pqb_rope, ctypes.byref(a)) if T else 0
+    if status:
+        raise PqbError(status, "rope")
+    return q_out, k_out
 
 
 def gemm_fp8_blockscaled(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor,

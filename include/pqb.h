@@ -603,15 +603,11 @@ typedef struct pqb_int8_mat {
  * .. 127 and any number of rows.  c may share no memory with the inputs.
  * Shape rules: k % 16 == 0 and k <= 131056 (S stays in int32); strides multiples of 16 in
  * [k, 2^23); rows < 2^30 and ceil(a.rows / 128) * ceil(b.rows / 128) < 2^23.  a.rows = 0 or
- * b.rows = 0 does nothing; k = 0 writes the bias or zeros.  Workspace (sums of parts of K, where
- * there are few tiles): pqb_gemm_int8_workspace_bytes(), its contents on entry do not
- * matter; calls that overlap in time need one each.  Alignment: codes, c and workspace 16
+ * b.rows = 0 does nothing; k = 0 writes the bias or zeros.  Alignment: codes and c 16
  * bytes, scales and bias 4.  Errors, before any launch: PQB_ERR_ENUM, PQB_ERR_SHAPE,
- * PQB_ERR_NULL, PQB_ERR_ALIGN, PQB_ERR_WORKSPACE. */
-size_t pqb_gemm_int8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+ * PQB_ERR_NULL, PQB_ERR_ALIGN. */
 pqb_status pqb_gemm_int8(const pqb_int8_mat* a, const pqb_int8_mat* b, int64_t k, const float* bias,
-                         pqb_dtype out_dtype, void* c, void* workspace, size_t workspace_bytes,
-                         void* stream);
+                         pqb_dtype out_dtype, void* c, void* stream);
 
 /* What the two calls below write: values of the input's dtype (PQB_PLAIN; gran
  * ignored), or codes and scales as pqb_quantize lays them out for [1, rows, cols]:

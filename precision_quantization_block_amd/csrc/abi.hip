@@ -985,13 +985,8 @@ static bool int8_dims_ok(int64_t m, int64_t n, int64_t k) {
          (m + 127) / 128 * ((n + 127) / 128) < (int64_t)1 << 23;
 }
 
-size_t pqb_gemm_int8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  return int8_dims_ok(m, n, k) ? gemm_int8_workspace_bytes(m, n, k) : 0;
-}
-
 pqb_status pqb_gemm_int8(const pqb_int8_mat* a, const pqb_int8_mat* b, int64_t k, const float* bias,
-                         pqb_dtype out_dtype, void* c, void* workspace, size_t workspace_bytes,
-                         void* stream) {
+                         pqb_dtype out_dtype, void* c, void* stream) {
   if (!valid_dtype(out_dtype)) return PQB_ERR_ENUM;
   if (!a || !b) return PQB_ERR_NULL;
   for (const pqb_int8_mat* m : {a, b})
@@ -1004,12 +999,6 @@ pqb_status pqb_gemm_int8(const pqb_int8_mat* a, const pqb_int8_mat* b, int64_t k
   if (!aligned(c, 16) || !aligned(a->scales, 4) || !aligned(b->scales, 4) || !aligned(bias, 4) ||
       !aligned(a->codes, 16) || !aligned(b->codes, 16))
     return PQB_ERR_ALIGN;
-  const size_t need = gemm_int8_workspace_bytes(a->rows, b->rows, k);
-  if (need) {
-    if (!workspace) return PQB_ERR_NULL;
-    if (workspace_bytes < need) return PQB_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return PQB_ERR_ALIGN;
-  }
   Int8Args g{};
   g.a = a->codes;
   g.b = b->codes;
@@ -1024,7 +1013,7 @@ pqb_status pqb_gemm_int8(const pqb_int8_mat* a, const pqb_int8_mat* b, int64_t k
   g.N = (int32_t)b->rows;
   g.K = (int32_t)k;
   g.c = c;
-  return hip_status(launch_gemm_int8(g, out_dtype == PQB_BF16, workspace, (hipStream_t)stream));
+  return hip_status(launch_gemm_int8(g, out_dtype == PQB_BF16, (hipStream_t)stream));
 }
 
 constexpr int64_t kLayerMaxStride = (int64_t)1 << 40;

@@ -71,12 +71,14 @@ __device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& 
   tm = band * kBand + rem - tn * rows;
 }
 
+enum Out { kF32 = 0, kBf16 = 1 };
+
 // Eight results of row m from column n on (n % 8 == 0).
-template <bool kBf16>
+template <int kOut>
 __device__ __forceinline__ void store_out8(void* c, int64_t m, int n, int N, const float (&v)[8]) {
   if (N % 8 == 0) {
     if (n >= N) return;
-    if constexpr (kBf16) {
+    if constexpr (kOut == kBf16) {
       st_nt16(reinterpret_cast<uint16_t*>(c) + m * N + n, bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
               bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
     } else {
@@ -88,7 +90,7 @@ __device__ __forceinline__ void store_out8(void* c, int64_t m, int n, int N, con
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (n + j < N) {
-        if constexpr (kBf16)
+        if constexpr (kOut == kBf16)
           reinterpret_cast<uint16_t*>(c)[m * N + n + j] = (uint16_t)(bf16x2_rne(v[j], 0.0f) & 0xFFFFu);
         else
           reinterpret_cast<float*>(c)[m * N + n + j] = v[j];
@@ -110,10 +112,10 @@ __device__ __forceinline__ Columns columns_at(const Int8Args& g, int n) {
   }
   return c;
 }
-__device__ __forceinline__ void scaled(const int (&x)[8], float sa, const Columns& c, bool bias, float (&v)[8]) {
+__device__ __forceinline__ void scaled(v4i lo, v4i hi, float sa, const Columns& c, bool bias, float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    v[j] = (float)x[j] * sa * c.s[j];
+    v[j] = (float)(j < 4 ? lo[j & 3] : hi[j & 3]) * sa * c.s[j];
     if (bias) v[j] += c.b[j];
   }
 }
@@ -121,16 +123,16 @@ __device__ __forceinline__ void scaled(const int (&x)[8], float sa, const Column
 template <int kTM, int kTN, int kWM, int kWN>
 struct Tile {
   static constexpr int waves = kWM * kWN, threads = 64 * waves;
-  static constexpr int mt = kTM / kWM / 32, nt = kTN / kWN / 32;     // 32 x 32 products of a wave
+  static constexpr int mt = kTM / kWM / 16, nt = kTN / kWN / 16;     // 16 x 16 products of a wave
   static constexpr int slot = (kTM + kTN) * kBK;
-  static constexpr int stage_ld = 32 * nt + 4;                       // ints per staged row
+  static constexpr int stage_ld = 16 * nt + 4;                       // ints per staged row
   static constexpr int stage = waves * 32 * stage_ld * 4;
   static constexpr int lds = 2 * slot > stage ? 2 * slot : stage;
   static constexpr int a_loads = kTM / 8 / waves, b_loads = kTN / 8 / waves;
-  static_assert(a_loads * 8 * waves == kTM && b_loads * 8 * waves == kTN && nt == 2, "tile shape");
+  static_assert(a_loads * 8 * waves == kTM && b_loads * 8 * waves == kTN && nt == 4 && mt % 2 == 0, "tile shape");
 };
 
-template <int kTM, int kTN, int kWM, int kWN, bool kBf16>
+template <int kTM, int kTN, int kWM, int kWN, int kOut>
 __global__ __launch_bounds__(64 * kWM * kWN) void k_gemm_int8(Int8Args g, int tiles_m, int tiles_n) {
   using S = Tile<kTM, kTN, kWM, kWN>;
   __shared__ __align__(16) uint8_t lds[S::lds];
@@ -142,7 +144,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_gemm_int8(Int8Args g, int ti
   const int nkb = (g.K + kBK - 1) / kBK;
 
   // Instruction j of a wave fills rows 8 (j waves + wave) .. + 7 of a tile
-  const int drow = lane >> 3, chunk = (lane & 7) ^ drow;
+  const int drow = lane >> 3, chunk = (lane & 7) ^ ((drow >> 1) | (wave & 1) << 2);
   const v4i buf_a = buffer_at(g.a + (int64_t)m0 * g.a_stride), buf_b = buffer_at(g.b + (int64_t)n0 * g.b_stride);
   uint32_t off_a[S::a_loads], off_b[S::b_loads];
 #pragma unroll
@@ -156,48 +158,78 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_gemm_int8(Int8Args g, int ti
     off_b[j] = n0 + r < g.N ? (uint32_t)r * (uint32_t)g.b_stride + 16u * chunk : kOutside;
   }
   const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(lds) + wave * 1024);
-  auto issue = [&](int kb) {
+  auto issue_a = [&](int kb, int j) {
     const bool out = kb * kBK + 16 * chunk >= g.K;                   // behind the last chunk of K
-    const uint32_t to = base + (kb & 1) * S::slot;
-#pragma unroll
-    for (int j = 0; j < S::a_loads; ++j)
-      dma16(buf_a, out ? kOutside : off_a[j], kb * kBK, to + j * S::waves * 1024);
-#pragma unroll
-    for (int j = 0; j < S::b_loads; ++j)
-      dma16(buf_b, out ? kOutside : off_b[j], kb * kBK, to + kTM * kBK + j * S::waves * 1024);
+    dma16(buf_a, out ? kOutside : off_a[j], kb * kBK, base + (kb & 1) * S::slot + j * S::waves * 1024);
+  };
+  auto issue_b = [&](int kb, int j) {
+    const bool out = kb * kBK + 16 * chunk >= g.K;
+    dma16(buf_b, out ? kOutside : off_b[j], kb * kBK, base + (kb & 1) * S::slot + kTM * kBK + j * S::waves * 1024);
   };
 
-  const int wm = wave / kWN * (32 * S::mt), wn = wave % kWN * (32 * S::nt);
-  const int r32 = lane & 31, up = lane >> 5;
-  v16i acc[S::mt][S::nt];
+  const int wm = wave / kWN * (16 * S::mt), wn = wave % kWN * (16 * S::nt);
+  const int r16 = lane & 15, quarter = lane >> 4;
+  v4i acc[S::mt][S::nt];
 #pragma unroll
   for (int i = 0; i < S::mt; ++i)
 #pragma unroll
-    for (int j = 0; j < S::nt; ++j) acc[i][j] = v16i{};
+    for (int j = 0; j < S::nt; ++j) acc[i][j] = v4i{};
 
-  if (nkb > 0) issue(0);
+  // Fragments of 64 bytes of K (half s of a block).  Those of A are read for the next half as
+  // soon as their products of this one are issued, those of B into a second set.
+  v4i a[S::mt], b[2][S::nt];
+  const int row_a = (wm + r16) * kBK, row_b = (kTM + wn + r16) * kBK;
+  auto read_a = [&](int kb, int s, int i) {
+    a[i] = *reinterpret_cast<const v4i*>(lds + (kb & 1) * S::slot + row_a + 16 * i * kBK +
+                                         (((4 * s + quarter) ^ (r16 >> 1)) << 4));
+  };
+  auto read_b = [&](int kb, int s, int j) {
+    b[s][j] = *reinterpret_cast<const v4i*>(lds + (kb & 1) * S::slot + row_b + 16 * j * kBK +
+                                            (((4 * s + quarter) ^ (r16 >> 1)) << 4));
+  };
+
+#pragma unroll
+  for (int j = 0; j < S::a_loads; ++j) issue_a(0, j);
+#pragma unroll
+  for (int j = 0; j < S::b_loads; ++j) issue_b(0, j);
+  wait_vmcnt<0>();
+  barrier();
+#pragma unroll
+  for (int j = 0; j < S::a_loads; ++j) issue_a(1, j);
+#pragma unroll
+  for (int j = 0; j < S::b_loads; ++j) issue_b(1, j);
+#pragma unroll
+  for (int j = 0; j < S::nt; ++j) read_b(0, 0, j);
+#pragma unroll
+  for (int i = 0; i < S::mt; ++i) read_a(0, 0, i);
   for (int kb = 0; kb < nkb; ++kb) {
-    wait_vmcnt<0>();
-    barrier();
-    if (kb + 1 < nkb) issue(kb + 1);
-    const uint8_t* sl = lds + (kb & 1) * S::slot;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int at = ((2 * s + up) ^ (r32 & 7)) << 4;
-      v4i a[S::mt], b[S::nt];
+    for (int s = 0; s < 2; ++s) {
+      if (s == 1) {
+        // The next block has landed for every wave, and every wave has read this one: the
+        // next but one takes its slot (blocks behind the last read no memory)
+        wait_vmcnt<0>();
+        barrier();
+      }
 #pragma unroll
-      for (int i = 0; i < S::mt; ++i)
-        a[i] = *reinterpret_cast<const v4i*>(sl + (wm + 32 * i + r32) * kBK + at);
-#pragma unroll
-      for (int j = 0; j < S::nt; ++j)
-        b[j] = *reinterpret_cast<const v4i*>(sl + (kTM + wn + 32 * j + r32) * kBK + at);
-#pragma unroll
-      for (int i = 0; i < S::mt; ++i)
+      for (int i = 0; i < S::mt; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < S::nt; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[s][j], a[i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i < S::nt) read_b(kb + s, s ^ 1, i);
+        read_a(kb + s, s ^ 1, i);
+        if (s == 1) {
+#pragma unroll
+          for (int j = i; j < S::a_loads; j += S::mt) issue_a(kb + 2, j);
+#pragma unroll
+          for (int j = (i + S::mt / 2) % S::mt; j < S::b_loads; j += S::mt) issue_b(kb + 2, j);
+        }
+      }
     }
   }
+  wait_vmcnt<0>();
   barrier();   // every wave done with the ring before it becomes the output stage
 
   // 32 rows at a time through the wave's part of LDS, then eight columns a lane
@@ -205,48 +237,229 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_gemm_int8(Int8Args g, int ti
   const int n = n0 + wn + 8 * (lane & 7);
   const Columns cols = columns_at(g, n);
 #pragma unroll
-  for (int i = 0; i < S::mt; ++i) {
+  for (int i = 0; i < S::mt; i += 2) {
 #pragma unroll
-    for (int j = 0; j < S::nt; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<v4i*>(out + r32 * S::stage_ld + 32 * j + 8 * r + 4 * up) =
-            v4i{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+      for (int j = 0; j < S::nt; ++j)
+        *reinterpret_cast<v4i*>(out + (16 * h + r16) * S::stage_ld + 16 * j + 4 * quarter) = acc[i + h][j];
     wave_sync();
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int row = 8 * s + (lane >> 3), m = m0 + wm + 32 * i + row;
-      int x[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4i y = *reinterpret_cast<const v4i*>(out + row * S::stage_ld + 8 * (lane & 7) + 4 * h);
-        x[4 * h] = y[0], x[4 * h + 1] = y[1], x[4 * h + 2] = y[2], x[4 * h + 3] = y[3];
-      }
+      const int row = 8 * s + (lane >> 3), m = m0 + wm + 16 * i + row;
+      const int* x = out + row * S::stage_ld + 8 * (lane & 7);
+      const v4i lo = *reinterpret_cast<const v4i*>(x), hi = *reinterpret_cast<const v4i*>(x + 4);
       if (m < g.M) {
         float v[8];
-        scaled(x, g.a_scales[(int64_t)m * g.a_step], cols, g.bias != nullptr, v);
-        store_out8<kBf16>(g.c, m, n, g.N, v);
+        scaled(lo, hi, g.a_scales[(int64_t)m * g.a_step], cols, g.bias != nullptr, v);
+        store_out8<kOut>(g.c, m, n, g.N, v);
       }
     }
     wave_sync();
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows of A (decode steps), and few tiles: what is read once streams through LDS.
+// A workgroup owns kTM rows of A (zeros behind the last) and kTN rows of B, few enough
+// that the workgroups fill the chip, and its 8 waves share them out: kWM x kWN over the
+// products, the rest over the blocks' K, whose sums meet in LDS at the end.  Blocks of kBK
+// bytes of K pass through a ring, kSlots - 1 blocks ahead: what memory latency asks to be
+// in flight.  A row of a block is kBK / 16 chunks, chunk c of row r at c ^ mix(r): the 16
+// rows that are read at once touch 16 different groups of banks.
+// ---------------------------------------------------------------------------
+template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer>
+struct Ring {
+  static constexpr int waves = 8, wk = waves / kWM / kWN;
+  static constexpr int mt = kTM / 16 / kWM, nt = kTN / 16 / kWN, steps = kBK / 64 / wk;
+  static constexpr int chunks = kBK / 16, rows = 64 / chunks;   // of one DMA instruction
+  static constexpr int slot = (kTM + kTN) * kBK;
+  static constexpr int loads = slot / 1024 / waves;
+  static constexpr int most = 163840 / kPer / slot, slots = most < 8 ? most : 8;
+  static constexpr int ld = kTN + 4, sums = wk * kTM * ld * 4;
+  static constexpr int lds = slots * slot > sums ? slots * slot : sums;
+  static_assert(wk * kWM * kWN == waves && mt * kWM * 16 == kTM && nt * kWN * 16 == kTN, "waves");
+  static_assert(steps * wk * 64 == kBK && loads * waves * 1024 == slot && slots >= 3, "blocks");
+  static_assert(lds * kPer <= 163840 && (slots - 2) * loads < 64, "LDS and the load counter");
+  static __device__ __forceinline__ int mix(int r) { return chunks >= 16 ? r & 15 : r >> 1 & 7; }
+};
+
+template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer, int kOut>
+__global__ __launch_bounds__(512, 2 * kPer) void k_int8_ring(Int8Args g, int tiles_m) {
+  using S = Ring<kTM, kTN, kBK, kWM, kWN, kPer>;
+  __shared__ __align__(16) uint8_t lds[S::lds];
+  const int lane = threadIdx.x & 63, r16 = lane & 15, quarter = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Workgroups of one XCD take tiles in turn that share their rows of B
+  const int nwg = gridDim.x, xcd = blockIdx.x & 7, per = nwg >> 3, more = nwg & 7;
+  const int tile = xcd * per + min(xcd, more) + (blockIdx.x >> 3);
+  const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * kTM, n0 = tn * kTN;
+  const int nkb = (g.K + kBK - 1) / kBK;
+
+  // Instruction j of a wave fills rows (j waves + wave) S::rows ... of [A | B]
+  const v4i buf_a = buffer_at(g.a + (int64_t)m0 * g.a_stride), buf_b = buffer_at(g.b + (int64_t)n0 * g.b_stride);
+  uint32_t off[S::loads];
+  int chunk[S::loads];
+#pragma unroll
+  for (int j = 0; j < S::loads; ++j) {
+    const int r = (j * S::waves + wave) * S::rows + lane / S::chunks;
+    chunk[j] = (lane % S::chunks) ^ S::mix(r);
+    const bool in = r < kTM ? m0 + r < g.M : n0 + r - kTM < g.N;
+    const uint32_t at = r < kTM ? (uint32_t)r * (uint32_t)g.a_stride : (uint32_t)(r - kTM) * (uint32_t)g.b_stride;
+    off[j] = in ? at + 16u * chunk[j] : kOutside;
+  }
+  const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(lds) + wave * 1024);
+  auto issue = [&](int kb, int slot) {
+#pragma unroll
+    for (int j = 0; j < S::loads; ++j) {
+      const bool of_a = (j * S::waves + wave) * S::rows < kTM;
+      const int k = kb * kBK;
+      dma16(of_a ? buf_a : buf_b, k + 16 * chunk[j] >= g.K ? kOutside : off[j], k,
+            base + slot * S::slot + j * S::waves * 1024);
+    }
+  };
+
+  const int wn = wave % kWN, wm = wave / kWN % kWM, part = wave / (kWN * kWM);
+  v4i acc[S::mt][S::nt];
+#pragma unroll
+  for (int i = 0; i < S::mt; ++i)
+#pragma unroll
+    for (int j = 0; j < S::nt; ++j) acc[i][j] = v4i{};
+  // The fragments of one block are read from LDS while the ones before it are multiplied
+  v4i a[2][S::steps][S::mt], b[2][S::steps][S::nt];
+  auto read = [&](int slot, int set) {
+    const uint8_t* sl = lds + slot * S::slot;
+#pragma unroll
+    for (int s = 0; s < S::steps; ++s) {
+      const int at = ((4 * (part * S::steps + s) + quarter) ^ S::mix(r16)) << 4;
+#pragma unroll
+      for (int j = 0; j < S::nt; ++j)
+        b[set][s][j] = *reinterpret_cast<const v4i*>(sl + (kTM + 16 * (wn * S::nt + j) + r16) * kBK + at);
+#pragma unroll
+      for (int i = 0; i < S::mt; ++i)
+        a[set][s][i] = *reinterpret_cast<const v4i*>(sl + (16 * (wm * S::mt + i) + r16) * kBK + at);
+    }
+  };
+#pragma unroll
+  for (int t = 0; t < S::slots; ++t) issue(t, t);
+  wait_vmcnt<(S::slots - 1) * S::loads>();
+  barrier();
+  read(0, 0);
+  int slot = 0;
+  for (int t = 0; t < nkb; t += 2) {
+#pragma unroll
+    for (int set = 0; set < 2; ++set) {
+      // The next block has landed for every wave, and every wave has read this one: its
+      // slot is filled again (blocks behind the last read no memory and hold zeros)
+      wait_vmcnt<(S::slots - 2) * S::loads>();
+      barrier();
+      issue(t + set + S::slots, slot);
+      slot = slot + 1 == S::slots ? 0 : slot + 1;
+      read(slot, set ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < S::steps; ++s)
+#pragma unroll
+        for (int i = 0; i < S::mt; ++i)
+#pragma unroll
+          for (int j = 0; j < S::nt; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[set][s][j], a[set][s][i], acc[i][j], 0, 0, 0);
+    }
+  }
+  wait_vmcnt<0>();
+  barrier();   // every wave done with the ring before it holds the sums
+
+  int* sums = reinterpret_cast<int*>(lds);
+#pragma unroll
+  for (int i = 0; i < S::mt; ++i)
+#pragma unroll
+    for (int j = 0; j < S::nt; ++j)
+      *reinterpret_cast<v4i*>(sums + (part * kTM + 16 * (wm * S::mt + i) + r16) * S::ld + 16 * (wn * S::nt + j) +
+                              4 * quarter) = acc[i][j];
+  __syncthreads();
+  const int rows = min(g.M - m0, kTM);
+  for (int u = threadIdx.x; u < rows * (kTN / 8); u += 512) {   // eight columns of a row
+    const int r = u / (kTN / 8), c = 8 * (u % (kTN / 8)), n = n0 + c;
+    if (n >= g.N) continue;
+    v4i lo{}, hi{};
+#pragma unroll
+    for (int w = 0; w < S::wk; ++w) {
+      const v4i* p = reinterpret_cast<const v4i*>(sums + (w * kTM + r) * S::ld + c);
+      lo += p[0];
+      hi += p[1];
+    }
+    float v[8];
+    scaled(lo, hi, g.a_scales[(int64_t)(m0 + r) * g.a_step], columns_at(g, n), g.bias != nullptr, v);
+    store_out8<kOut>(g.c, m0 + r, n, g.N, v);
+  }
+}
+
+template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer>
+hipError_t launch_ring(const Int8Args& g, bool out_bf16, hipStream_t st) {
+  const int tiles_m = (g.M + kTM - 1) / kTM, tiles_n = (g.N + kTN - 1) / kTN;
+  const uint32_t grid = (uint32_t)tiles_m * (uint32_t)tiles_n;
+  if (out_bf16) k_int8_ring<kTM, kTN, kBK, kWM, kWN, kPer, kBf16><<<grid, 512, 0, st>>>(g, tiles_m);
+  else k_int8_ring<kTM, kTN, kBK, kWM, kWN, kPer, kF32><<<grid, 512, 0, st>>>(g, tiles_m);
+  return hipGetLastError();
+}
+
 template <int kTM, int kTN, int kWM, int kWN>
 hipError_t launch_tile(const Int8Args& g, bool out_bf16, hipStream_t st) {
   const int tiles_m = (g.M + kTM - 1) / kTM, tiles_n = (g.N + kTN - 1) / kTN;
   const uint32_t grid = (uint32_t)tiles_m * (uint32_t)tiles_n;
-  if (out_bf16) k_gemm_int8<kTM, kTN, kWM, kWN, true><<<grid, 64 * kWM * kWN, 0, st>>>(g, tiles_m, tiles_n);
-  else k_gemm_int8<kTM, kTN, kWM, kWN, false><<<grid, 64 * kWM * kWN, 0, st>>>(g, tiles_m, tiles_n);
+  if (out_bf16) k_gemm_int8<kTM, kTN, kWM, kWN, kBf16><<<grid, 64 * kWM * kWN, 0, st>>>(g, tiles_m, tiles_n);
+  else k_gemm_int8<kTM, kTN, kWM, kWN, kF32><<<grid, 64 * kWM * kWN, 0, st>>>(g, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
+int64_t tiles(const Int8Args& g, int tm, int tn) {
+  return (int64_t)((g.M + tm - 1) / tm) * ((g.N + tn - 1) / tn);
+}
+
+// What a ring of tm x tn tiles costs: the bytes per byte of K that the busiest of 256
+// CUs moves into LDS.
+int64_t ring_cost(const Int8Args& g, int tm, int tn) { return (tiles(g, tm, tn) + 255) / 256 * (tm + tn); }
+
 }  // namespace
 
-size_t gemm_int8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
-
-hipError_t launch_gemm_int8(Int8Args g, bool out_bf16, void*, hipStream_t st) {
-  return launch_tile<128, 128, 2, 2>(g, out_bf16, st);
+// Up to 128 rows of A: the ring whose busiest CU moves the least, all rows in one tile,
+// the wider tile where two are equal.  (Measured at K = 4096, us: 16 rows over 14336
+// channels 13.9 / 11.2 / 11.3 for tiles 16 x 16, 16 x 32, 32 x 64; 64 rows 28 / 13.9 / 12.7 /
+// 17.4 for 16, 32, 64, 128 columns, over 4096 channels 8.9 / 8.2 / 10.3 / 16.0; 128 rows over
+// 4096 11.0 / 14.7 / 25 for 32, 64, 128 columns, over 28672 54 / 37.6 / 35.5.)
+// More rows: rings of 128 x 64, two 128 x 128 tiles per CU or one 256 x 256 tile, by
+// what a round of them takes per 4096 of K: 16 us for 256 rings and 13.5 for 256 more;
+// 28 us for 256 tiles of 128 x 128, 40 for 512; 70 us for 256 of 256 x 256.  (512 rows
+// over 4096 channels 16 / 26 / 45, 1024 rows 27 / 28 / 46, 2048 rows 59 / 39 / 50,
+// 4096 rows 120 / 82 / 71.)
+hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st) {
+  if (g.M <= 16) {
+    const int64_t c16 = ring_cost(g, 16, 16), c32 = ring_cost(g, 16, 32), c64 = ring_cost(g, 32, 64);
+    if (c64 <= c16 && c64 <= c32) return launch_ring<32, 64, 256, 1, 4, 2>(g, out_bf16, st);
+    if (c32 <= c16) return launch_ring<16, 32, 512, 1, 2, 2>(g, out_bf16, st);
+    return launch_ring<16, 16, 512, 1, 1, 2>(g, out_bf16, st);
+  }
+  if (g.M <= 32) {
+    const int64_t c16 = ring_cost(g, 32, 16), c32 = ring_cost(g, 32, 32), c64 = ring_cost(g, 32, 64);
+    if (c64 <= c16 && c64 <= c32) return launch_ring<32, 64, 256, 1, 4, 2>(g, out_bf16, st);
+    if (c32 <= c16) return launch_ring<32, 32, 256, 1, 2, 2>(g, out_bf16, st);
+    return launch_ring<32, 16, 512, 1, 1, 2>(g, out_bf16, st);
+  }
+  if (g.M <= 64) {
+    const int64_t c16 = ring_cost(g, 64, 16), c32 = ring_cost(g, 64, 32), c64 = ring_cost(g, 64, 64),
+                  c128 = ring_cost(g, 64, 128);
+    if (c128 <= c16 && c128 <= c32 && c128 <= c64) return launch_ring<64, 128, 128, 1, 4, 2>(g, out_bf16, st);
+    if (c64 <= c16 && c64 <= c32) return launch_ring<64, 64, 128, 2, 2, 2>(g, out_bf16, st);
+    if (c32 <= c16) return launch_ring<64, 32, 256, 2, 1, 2>(g, out_bf16, st);
+    return launch_ring<64, 16, 512, 1, 1, 1>(g, out_bf16, st);
+  }
+  if (ring_cost(g, 128, 32) <= ring_cost(g, 128, 64)) return launch_ring<128, 32, 256, 2, 1, 1>(g, out_bf16, st);
+  const int64_t ring = (tiles(g, 128, 64) + 255) / 256, small = tiles(g, 128, 128);
+  const double by_ring = 2.5 + 13.5 * ring, by_large = 70.0 * ((tiles(g, 256, 256) + 255) / 256);
+  const double by_small = small / 512 * 40.0 + (small % 512 > 256 ? 40.0 : small % 512 ? 28.0 : 0.0);
+  if (by_ring <= by_small && by_ring <= by_large) return launch_ring<128, 64, 128, 2, 2, 2>(g, out_bf16, st);
+  if (by_small <= by_large) return launch_tile<128, 128, 2, 2>(g, out_bf16, st);
+  return launch_tile<256, 256, 2, 4>(g, out_bf16, st);
 }
 
 }  // namespace pqb

@@ -291,11 +291,8 @@ struct Int8Args {
   int32_t a_step, b_step;                                   // 1: a scale per row, 0: one scale
   int32_t M, N, K;                                          // K % 16 == 0
   void* c;
-  int32_t* part;                                            // set by the launcher: split sums
-  int32_t splits, per_split;                                // K blocks per split
 };
-size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
-hipError_t launch_gemm_int8(Int8Args g, bool out_bf16, void* workspace, hipStream_t st);
+hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st);
 
 // ---- division checks (k_check.hip) -----------------------------------------
 hipError_t launch_check_recip(uint32_t first, int64_t n, float* out, hipStream_t st);

@@ -137,9 +137,7 @@ def lib():
         L.pqb_gemm_w4a16.argtypes = [P, I64, P, P, P, I64, I64, I, P, P]
         L.pqb_gemm_w4a16_batch.argtypes = [ctypes.POINTER(_W4Job), I64, I64, I, P]
         MAT = ctypes.POINTER(_Int8Mat)
-        L.pqb_gemm_int8_workspace_bytes.argtypes = [I64, I64, I64]
-        L.pqb_gemm_int8_workspace_bytes.restype = SZ
-        L.pqb_gemm_int8.argtypes = [MAT, MAT, I64, P, I, P, P, SZ, P]
+        L.pqb_gemm_int8.argtypes = [MAT, MAT, I64, P, I, P, P]
         L.pqb_norm_quant.argtypes = [ctypes.POINTER(_Norm), P]
         L.pqb_act_quant.argtypes = [P, P, I, I64, I64, I64, I64, I, I, I, P, P, P]
         L.pqb_rope.argtypes = [ctypes.POINTER(_Rope), P]
@@ -766,15 +764,13 @@ def _int8_mat(m, name, dev=None):
 
 
 def gemm_int8(a, b, out_dtype=torch.bfloat16, *, bias: torch.Tensor | None = None,
-              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+              out: torch.Tensor | None = None) -> torch.Tensor:
     """C [M, N] = (A B^T) of symmetric INT8 codes, summed exactly as integers, times the
     scale of A's row and of B's row, plus bias float32 [N].  a and b: a Quantized from
     quantize(x, "int8_sym") (per row or per tensor), norm_quant or act_quant, or a (codes
     [rows, K] int8 or uint8, scales float32 [rows] or [1]) pair whose rows may lie apart (a
-    copy is made unless that is by multiples of 16 bytes).  K is a multiple of 16.  workspace:
-    memory to use instead of an allocation per call (any contiguous tensor of
-    pqb_gemm_int8_workspace_bytes; calls that overlap need one each).  out may share no
-    memory with the operands."""
+    copy is made unless that is by multiples of 16 bytes).  K is a multiple of 16.  out may share
+    no memory with the operands."""
     am, keep_a, dev, K = _int8_mat(a, "a")
     bm, keep_b, _, kb = _int8_mat(b, "b", dev)
     if K != kb:
@@ -793,24 +789,12 @@ def gemm_int8(a, b, out_dtype=torch.bfloat16, *, bias: torch.Tensor | None = Non
         raise ValueError("out must be a contiguous [M, N] tensor of out_dtype")
     elif any(_share(out, t) for t in (*keep_a, *keep_b, bias)):
         raise ValueError("out must not share memory with the operands")
-    L = lib()
-    need = L.pqb_gemm_int8_workspace_bytes(M, N, K)
-    workspace, have = _workspace(workspace, need, dev)
-    status = _call_on(dev, L.pqb_gemm_int8, ctypes.byref(am), ctypes.byref(bm), K,
+    status = _call_on(dev, lib().pqb_gemm_int8, ctypes.byref(am), ctypes.byref(bm), K,
                       None if bias is None else bias.data_ptr(), BF16 if out_dtype is _BF16 else F32,
-                      out.data_ptr(), None if workspace is None else workspace.data_ptr(), have)
+                      out.data_ptr())
     if status:
         raise PqbError(status, "gemm_int8")
     return out
-
-
-def _workspace(workspace, need: int, dev):
-    """The caller's workspace or a new one, and its bytes."""
-    if workspace is None:
-        return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
-    if isinstance(workspace, torch.Tensor) and _ready(dev, workspace.dtype, workspace):
-        return workspace, workspace.numel() * workspace.element_size()
-    raise ValueError(f"workspace must be a contiguous tensor on {dev}")
 
 
 def _span(t):

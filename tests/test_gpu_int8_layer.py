@@ -89,10 +89,22 @@ def test_gemm_shapes(m, n, k, dtype):
     check_gemm(m, n, k, dtype, seed=m * 7 + n, bias=m % 2 == 1)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (3, 14336, 4096), (64, 1024, 14336), (48, 4100, 131056), (512, 4096, 1040),
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (20, 4100, 1040), (20, 8200, 400), (20, 17000, 272), (60, 4000, 528), (60, 8200, 400),
+                                   (60, 16400, 272), (60, 32800, 144), (100, 8200, 400), (100, 16400, 144), (130, 2000, 80), (500, 4100, 272),
+                                   (1100, 7000, 144), (2100, 6000, 336), (2500, 5000, 16), (5000, 7000, 272), (300, 70000, 144), (3, 14336, 4096), (64, 1024, 14336), (48, 4100, 131056), (512, 4096, 1040),
                                    (777, 1001, 2064), (1024, 2048, 7168), (2049, 2500, 1536), (4100, 520, 144)])
 def test_gemm_large(m, n, k):
     check_gemm(m, n, k, BF, seed=k, bias=n % 2 == 1)
+
+
+@pytest.mark.parametrize("k", [16, 144, 400, 1040, 2512])
+@pytest.mark.parametrize("m,n", [(9, 300), (10, 4201), (13, 14400), (30, 2003), (20, 4100), (32, 8210), (50, 1005), (41, 4100),
+                                 (60, 8200), (64, 16401), (128, 1003), (111, 8201), (500, 4090), (129, 16400), (1300, 7001),
+                                 (2100, 6001), (2500, 5000)])
+def test_gemm_every_tile(m, n, k):
+    """Each tile that the launcher takes (16 x 16, 16 x 32, 32 x 64; 32 x 16, 32 x 32, 32 x 64; 64 x 16, 64 x 32, 64 x 64,
+    64 x 128; 128 x 32, 128 x 64 twice, 128 x 128 twice, 256 x 256 twice), with K ending in every part of a block."""
+    check_gemm(m, n, k, BF if k % 32 else F32, seed=m, bias=m % 2 == 1, pads=(0, 16) if k == 400 else (0, 0))
 
 
 @pytest.mark.parametrize("m", [1, 40, 300])
@@ -148,16 +160,17 @@ def test_gemm_output_past_2_31():
         assert torch.equal(got[rows], product(a[rows], sa[rows], b, sb, None, BF))
 
 
-def test_gemm_workspace_and_out():
+def test_gemm_into_out():
     g = gen(4)
     a, b = codes(g, 96, 8192), codes(g, 256, 8192)
     sa, sb = torch.rand(96, generator=g, device=DEV), torch.rand(256, generator=g, device=DEV)
     want = product(a, sa, b, sb, None, F32)
-    need = pqb.lib().pqb_gemm_int8_workspace_bytes(96, 256, 8192)
-    ws = torch.full((max(need, 1),), 0xAB, dtype=torch.uint8, device=DEV)
     out = torch.empty(96, 256, device=DEV)
-    assert pqb.gemm_int8((a, sa), (b, sb), F32, out=out, workspace=ws) is out and torch.equal(out, want)
-    assert torch.equal(pqb.gemm_int8((a, sa), (b, sb), F32, workspace=ws), want)
+    assert pqb.gemm_int8((a, sa), (b, sb), F32, out=out) is out and torch.equal(out, want)
+    buf = torch.empty(96 * 256 * 4 + a.numel(), dtype=torch.uint8, device=DEV)
+    inside = buf[:a.numel()].view(I8).view(a.shape)
+    with pytest.raises(ValueError, match="share memory"):
+        pqb.gemm_int8((inside, sa), (b, sb), F32, out=buf[a.numel() - 64:][:96 * 256 * 4].view(F32).view(96, 256))
 
 
 # ---------------------------------------------------------------------------

@@ -11,7 +11,7 @@ import torch
 import precision_quantization_block_amd as pqb
 from precision_quantization_block_amd import pqb as binding
 
-OK, NULL, ENUM, COMBO, SHAPE, ALIGN, WORKSPACE, VALUE = 0, -1, -2, -3, -4, -5, -6, -9
+OK, NULL, ENUM, COMBO, SHAPE, ALIGN, VALUE = 0, -1, -2, -3, -4, -5, -9
 P = 0x1000000      # an aligned address nobody reads
 
 
@@ -24,13 +24,13 @@ def L():
 # gemm_int8
 # ---------------------------------------------------------------------------
 
-def gemm(L, m=4, n=8, k=64, out=0, bias=None, c=P, ws=P, ws_bytes=1 << 40, a=None, b=None, sa=None, sb=None):
+def gemm(L, m=4, n=8, k=64, out=0, bias=None, c=P, a=None, b=None, sa=None, sb=None):
     A = binding._Int8Mat(P, P, m, k, 1, 0)
     B = binding._Int8Mat(P, P, n, k, 1, 0)
     for mat, changes in ((A, a), (B, b)):
         for f, v in (changes or {}).items():
             setattr(mat, f, v)
-    return L.pqb_gemm_int8(ctypes.byref(A), ctypes.byref(B), k, bias, out, c, ws, ws_bytes, None)
+    return L.pqb_gemm_int8(ctypes.byref(A), ctypes.byref(B), k, bias, out, c, None)
 
 
 @pytest.mark.parametrize("want,changes", [
@@ -47,23 +47,8 @@ def test_gemm_refusals(L, want, changes):
 
 def test_gemm_null_operands(L):
     A = binding._Int8Mat(P, P, 1, 16, 1, 0)
-    assert L.pqb_gemm_int8(None, ctypes.byref(A), 16, None, 0, P, None, 0, None) == NULL
-    assert L.pqb_gemm_int8(ctypes.byref(A), None, 16, None, 0, P, None, 0, None) == NULL
-
-
-def test_gemm_workspace(L):
-    size = L.pqb_gemm_int8_workspace_bytes
-    assert size(-1, 5, 16) == size(5, 5, 8) == size(5, 5, 131072) == 0
-    seen = 0
-    for m, n, k in itertools.product((1, 7, 64, 65, 96, 128, 300, 512, 2048), (1, 130, 1024, 4096), (16, 2048, 14336, 131056)):
-        need = size(m, n, k)
-        if need:
-            seen += 1
-            assert gemm(L, m, n, k, ws=None) == NULL
-            assert gemm(L, m, n, k, ws_bytes=need - 1) == WORKSPACE
-            assert gemm(L, m, n, k, ws=P + 8) == ALIGN
-        else:
-            assert gemm(L, m, n, k, c=None, ws=None) == NULL     # asks for c, not for a workspace
+    assert L.pqb_gemm_int8(None, ctypes.byref(A), 16, None, 0, P, None) == NULL
+    assert L.pqb_gemm_int8(ctypes.byref(A), None, 16, None, 0, P, None) == NULL
 
 
 # ---------------------------------------------------------------------------

@@ -784,7 +784,7 @@ def gemm_int8(a, b, out_dtype=torch.bfloat16, *, bias: torch.Tensor | None = Non
         if bias.numel() != N:
             raise ValueError("bias must hold a value per row of b")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = keep_a[0].new_empty((M, N), dtype=out_dtype)
     elif not _ready(dev, out_dtype, out) or out.shape != (M, N):
         raise ValueError("out must be a contiguous [M, N] tensor of out_dtype")
     elif any(_share(out, t) for t in (*keep_a, *keep_b, bias)):
@@ -847,16 +847,20 @@ def _layer_rows(t, name, dev, dtype, cols, block):
     return t, rows, stride
 
 
-def _layer_out(fmt, gran, rows, cols, like, dev):
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _layer_out(fmt, gran, rows, cols, like):
     """fmt and gran as numbers, and what a fused quantization of [rows, cols] writes: the
     Quantized (or plain tensor), its codes and its scales."""
     if fmt is None:
-        out = torch.empty(like.shape, dtype=like.dtype, device=dev)
+        out = like.new_empty(like.shape)
         return -1, 0, out, out, None
     gran = gran or DEFAULT_GRAN.get(fmt, "row")
     f, g = _fmt(fmt), _gran(gran)
-    codes = torch.empty(rows * cols, dtype=_U8, device=dev)
-    scales = torch.empty(rows * (cols // 128) if g == 2 else rows, dtype=_F32, device=dev)
+    codes = like.new_empty(rows * cols, dtype=_U8)
+    scales = like.new_empty(rows * (cols // 128) if g == 2 else rows, dtype=_F32)
     return f, g, Quantized(codes, scales, None, fmt, gran, (1, rows, cols)), codes, scales
 
 
@@ -878,66 +882,51 @@ def norm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, fmt: str | N
     shape = x.shape
     cols = shape[-1] if len(shape) else 1
     block = fmt is not None and gran == "1x128"
-    a = _Norm()
-    x2, rows, a.x_stride = _layer_rows(x, "x", dev, dtype, cols, block)
-    keep = [x2]
-    a.x, a.rows, a.cols = x2.data_ptr(), rows, cols
-    adds = False
-    res = None
+    x2, rows, x_stride = _layer_rows(x, "x", dev, dtype, cols, block)
+    res, g, h = None, None, None
+    res_stride = gate_rows = gate_stride = h_stride = 0
     if residual is not None:
-        res, n, a.residual_stride = _layer_rows(residual, "residual", dev, dtype, cols, block)
+        res, n, res_stride = _layer_rows(residual, "residual", dev, dtype, cols, block)
         if n != rows:
             raise ValueError("residual must have x's shape")
-        a.residual = res.data_ptr()
-        keep.append(res)
-        adds = True
     if gate is not None:
-        g, a.gate_rows, a.gate_stride = _layer_rows(gate, "gate", dev, dtype, cols, block)
-        if a.gate_rows < 1 or rows % a.gate_rows:
+        g, gate_rows, gate_stride = _layer_rows(gate, "gate", dev, dtype, cols, block)
+        if gate_rows < 1 or rows % gate_rows:
             raise ValueError("gate must have a number of rows that divides x's")
-        a.gate = g.data_ptr()
-        keep.append(g)
-        adds = True
-    for name, w in (("post_weight", post_weight), ("weight", weight), ("bias", bias)):
+    weights = (post_weight, weight, bias)
+    for name, w in zip(("post_weight", "weight", "bias"), weights):
         if w is not None:
             if not _ready(dev, dtype, w):
                 _refuse(dev, (dtype,), name, w)
             if w.numel() != cols:
                 raise ValueError(f"{name} must have {cols} values")
-            if block and w.data_ptr() & 15:
-                w = w.clone()
-            setattr(a, name, w.data_ptr())
-            keep.append(w)
-    adds = adds or post_weight is not None
-    h = None
-    if adds:
+    if block:
+        weights = tuple(w if w is None or not w.data_ptr() & 15 else w.clone() for w in weights)
+    if residual is not None or gate is not None or post_weight is not None:
         if h_out is None:
-            h = torch.empty(shape, dtype=dtype, device=dev)
-            a.h_stride = cols
+            h, h_stride = x.new_empty(shape), cols
         else:
             h = h_out
-            h2, n, a.h_stride = _layer_rows(h, "h_out", dev, dtype, cols, block)
+            h2, n, h_stride = _layer_rows(h, "h_out", dev, dtype, cols, block)
             if h.shape != shape or h2.data_ptr() != h.data_ptr():
                 raise ValueError("h_out must be like x, its rows at a stride that can be used as it is")
-            for t, stride in ((x2, a.x_stride), (res, a.residual_stride)):
-                if t is not None and _rows_share(h2, a.h_stride, t, stride) \
-                        and (t.data_ptr() != h.data_ptr() or stride != a.h_stride):
+            for t, stride in ((x2, x_stride), (res, res_stride)):
+                if t is not None and _rows_share(h2, h_stride, t, stride) \
+                        and (t.data_ptr() != h.data_ptr() or stride != h_stride):
                     raise ValueError("h_out may be x or residual itself, but not overlap them otherwise")
-            if any(_share(h, t) for t in keep if t is not x2 and t is not res):
+            if any(_share(h, t) for t in (g, *weights)):
                 raise ValueError("h_out must not share memory with a gate, weight or bias")
-        a.h = h.data_ptr()
     elif h_out is not None:
         raise ValueError("h_out needs a residual, gate or post_weight")
     if kind not in NORM_KINDS:
         raise ValueError(f"kind must be one of {tuple(NORM_KINDS)}")
     if bias is not None and kind != "layer":
         raise ValueError("a bias goes with a layer norm")
-    a.fmt, a.gran, result, codes, scales = _layer_out(fmt, gran, rows, cols, x, dev)
-    a.out = codes.data_ptr()
-    if scales is not None:
-        a.scales = scales.data_ptr()
-    a.residual_scale, a.eps, a.kind = residual_scale, eps, NORM_KINDS[kind]
-    a.dtype = BF16 if dtype is _BF16 else F32
+    f, gr, result, codes, scales = _layer_out(fmt, gran, rows, cols, x)
+    # (one constructor call: setting a struct's fields one by one took 2 of the 12 us of a small call)
+    a = _Norm(x2.data_ptr(), _at(res), _at(g), *map(_at, weights), _at(h), codes.data_ptr(), _at(scales), rows, cols,
+              gate_rows, x_stride, res_stride, gate_stride, h_stride, residual_scale, eps,
+              BF16 if dtype is _BF16 else F32, NORM_KINDS[kind], f, gr, 0)
     status = _call_on(dev, lib().pqb_norm_quant, ctypes.byref(a))
     if status:
         raise PqbError(status, "norm_quant")
@@ -962,10 +951,10 @@ def act_quant(gate: torch.Tensor, up: torch.Tensor | None = None, fmt: str | Non
         u, _, u_stride = _layer_rows(up, "up", dev, dtype, cols, block)
     if act not in ACT_KINDS:
         raise ValueError(f"act must be one of {tuple(ACT_KINDS)}")
-    f, gr, result, codes, scales = _layer_out(fmt, gran, rows, cols, gate, dev)
-    status = _call_on(dev, lib().pqb_act_quant, g.data_ptr(), None if u is None else u.data_ptr(),
+    f, gr, result, codes, scales = _layer_out(fmt, gran, rows, cols, gate)
+    status = _call_on(dev, lib().pqb_act_quant, g.data_ptr(), _at(u),
                       BF16 if dtype is _BF16 else F32, rows, cols, g_stride, u_stride, ACT_KINDS[act], f, gr,
-                      codes.data_ptr(), None if scales is None else scales.data_ptr())
+                      codes.data_ptr(), _at(scales))
     if status:
         raise PqbError(status, "act_quant")
     return result
@@ -1045,15 +1034,13 @@ def _rope_rows(x, name, dev, dtype):
 
 
 def _rope_out(out, x, x2, stride, name):
-    """Where x's turned values go, and their stride."""
-    if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[1] * x.shape[2]
+    """The caller's tensor for x's turned values, checked, and its stride."""
     o2, o_stride = _rope_rows(out, name, x.device, x.dtype)
     if out.shape != x.shape or o2 is not out:
         raise ValueError(f"{name} must be like its input, a token's values contiguous")
     if _rows_share(out, o_stride, x2, stride) and (out.data_ptr() != x2.data_ptr() or o_stride != stride):
         raise ValueError(f"{name} may be its input itself, but not overlap it otherwise")
-    return out, o_stride
+    return o_stride
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions, table: RopeTable, *,
@@ -1065,45 +1052,52 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions, table: RopeTable, *
     were in the outputs).  q_out and k_out may be q and k themselves.  Returns (q_out, k_out), k_out
     None without k."""
     dev, dtype = _device_of(q, "q"), q.dtype
-    a = _Rope()
-    q2, a.q_stride = _rope_rows(q, "q", dev, dtype)
+    q2, q_stride = _rope_rows(q, "q", dev, dtype)
     T, H, D = q2.shape
-    a.tokens, a.q_heads, a.dim = T, H, D
-    q_out, a.q_out_stride = _rope_out(q_out, q, q2, a.q_stride, "q_out")
-    a.q, a.q_out = q2.data_ptr(), q_out.data_ptr()
-    k2 = None
+    k2, Hk, k_stride, ko_stride = None, 0, 0, 0
+    given = q_out is not None or k_out is not None
     if k is not None:
-        k2, a.k_stride = _rope_rows(k, "k", dev, dtype)
+        k2, k_stride = _rope_rows(k, "k", dev, dtype)
         if k2.shape[0] != T or k2.shape[2] != D:
             raise ValueError("q and k must share tokens and dim")
-        a.k_heads = k2.shape[1]
-        k_out, a.k_out_stride = _rope_out(k_out, k, k2, a.k_stride, "k_out")
-        a.k, a.k_out = k2.data_ptr(), k_out.data_ptr()
-        if T and (_rows_share(q_out, a.q_out_stride, k2, a.k_stride)
-                  or _rows_share(k_out, a.k_out_stride, q2, a.q_stride)
-                  or _rows_share(q_out, a.q_out_stride, k_out, a.k_out_stride)):
-            raise ValueError("q_out and k_out must not share memory with each other's tokens")
+        Hk = k2.shape[1]
+        if k_out is None:
+            k_out, ko_stride = k.new_empty((T, Hk, D)), Hk * D
+        else:
+            ko_stride = _rope_out(k_out, k, k2, k_stride, "k_out")
     elif k_out is not None:
         raise ValueError("k_out needs k")
+    if q_out is None:
+        q_out, qo_stride = q.new_empty((T, H, D)), H * D
+    else:
+        qo_stride = _rope_out(q_out, q, q2, q_stride, "q_out")
+    if given and k is not None and T and (_rows_share(q_out, qo_stride, k2, k_stride)
+                                          or _rows_share(k_out, ko_stride, q2, q_stride)
+                                          or _rows_share(q_out, qo_stride, k_out, ko_stride)):
+        raise ValueError("q_out and k_out must not share memory with each other's tokens")
     angles = table.angles
     if not _ready(dev, torch.float64, angles):
         _refuse(dev, (torch.float64,), "table.angles", angles)
+    starts = lens = None
+    batch = 0
     if isinstance(positions, PagedPlan):
-        starts, lens = positions.q_starts, positions.kv_lens
+        starts, lens, positions = positions.q_starts, positions.kv_lens, None
         if not _ready(dev, _I32, starts, lens):
             _refuse(dev, (_I32,), "q_starts kv_lens", starts, lens)
-        if starts.numel() != lens.numel() + 1:
+        batch = lens.numel()
+        if starts.numel() != batch + 1:
             raise ValueError("the plan must hold batch + 1 starts and batch lengths")
-        a.q_starts, a.kv_lens, a.batch = starts.data_ptr(), lens.data_ptr(), lens.numel()
     else:
         if not _ready(dev, _I32, positions):
             _refuse(dev, (_I32,), "positions", positions)
         if positions.numel() != T:
             raise ValueError("positions must hold a value per token")
-        a.positions = positions.data_ptr()
-    a.rot, a.angles, a.amplitude = 2 * angles.numel(), angles.data_ptr(), table.amplitude
-    a.interleaved, a.dtype = bool(table.interleaved), BF16 if dtype is _BF16 else F32
-    status = _call_on(dev, lib().pqb_rope, ctypes.byref(a)) if T else 0
+    if not T:
+        return q_out, k_out
+    a = _Rope(q2.data_ptr(), _at(k2), q_out.data_ptr(), _at(k_out), T, H, Hk, D, 2 * angles.numel(), q_stride, k_stride,
+              qo_stride, ko_stride, _at(positions), _at(starts), _at(lens), batch, angles.data_ptr(), table.amplitude,
+              bool(table.interleaved), BF16 if dtype is _BF16 else F32, 0)
+    status = _call_on(dev, lib().pqb_rope, ctypes.byref(a))
     if status:
         raise PqbError(status, "rope")
     return q_out, k_out

@@ -16,6 +16,8 @@
 // v_mfma_i32_32x32x32_i8 takes the weights as its first operand: lane l holds row l & 31
 // and the 16 bytes of chunk l >> 5; result register r is weight row
 // 8 (r / 4) + 4 (l >> 5) + r % 4 of activation row l & 31.
+#include <algorithm>
+
 #include "launch.h"
 #include "quant.h"
 
@@ -59,12 +61,10 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Tile (tm, tn) of workgroup t of tiles_m x tiles_n: workgroups i, i + 8, ... share an
-// XCD and its L2, and take a contiguous run of tiles down bands of kBand tile rows.
+// Tile (tm, tn) of number t: down bands of kBand tile rows, so that tiles of neighbouring
+// numbers share rows of A and of B.
 template <int kBand>
-__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int nwg = tiles_m * tiles_n, xcd = blockIdx.x & 7, per = nwg >> 3, more = nwg & 7;
-  const int t = xcd * per + min(xcd, more) + (blockIdx.x >> 3);
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int band = t / (kBand * tiles_n), rem = t - band * kBand * tiles_n;
   const int rows = min(kBand, tiles_m - band * kBand);
   tn = rem / rows;
@@ -120,143 +120,228 @@ __device__ __forceinline__ void scaled(v4i lo, v4i hi, float sa, const Columns& 
   }
 }
 
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// p[n .. n + 3] (p[0] with step 0), 0 at and behind N.
+__device__ __forceinline__ v4f four_at(const float* p, int step, int n, int N) {
+  typedef float v4u __attribute__((ext_vector_type(4), aligned(4)));
+  if (step == 0) return v4f{p[0], p[0], p[0], p[0]};
+  if (n + 4 <= N) return *reinterpret_cast<const v4u*>(p + n);
+  v4f v{};
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    if (n + j < N) v[j] = p[n + j];
+  return v;
+}
+
 template <int kTM, int kTN, int kWM, int kWN>
 struct Tile {
   static constexpr int waves = kWM * kWN, threads = 64 * waves;
   static constexpr int mt = kTM / kWM / 16, nt = kTN / kWN / 16;     // 16 x 16 products of a wave
   static constexpr int slot = (kTM + kTN) * kBK;
-  static constexpr int stage_ld = 16 * nt + 4;                       // ints per staged row
-  static constexpr int stage = waves * 32 * stage_ld * 4;
-  static constexpr int lds = 2 * slot > stage ? 2 * slot : stage;
+  static constexpr int stage = 4096;                                 // bytes of a wave's staged results
+  static constexpr int lds = 2 * slot + waves * stage;
   static constexpr int a_loads = kTM / 8 / waves, b_loads = kTN / 8 / waves;
   static_assert(a_loads * 8 * waves == kTM && b_loads * 8 * waves == kTN && nt == 4 && mt % 2 == 0, "tile shape");
+  static_assert(a_loads <= mt && b_loads <= mt, "one load of each operand per row of products at most");
 };
 
+// Many tiles.  Workgroups stay and take tiles in turn, and the blocks of all their tiles are
+// one stream: the first ones of the next tile are on their way, and its first fragments
+// in registers, while a tile's results are scaled and stored.
 template <int kTM, int kTN, int kWM, int kWN, int kOut>
-__global__ __launch_bounds__(64 * kWM * kWN) void k_gemm_int8(Int8Args g, int tiles_m, int tiles_n) {
+__global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int tiles_m, int tiles_n) {
   using S = Tile<kTM, kTN, kWM, kWN>;
   __shared__ __align__(16) uint8_t lds[S::lds];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int tm, tn;
-  tile_of<1024 / kTM>(tiles_m, tiles_n, tm, tn);
-  const int m0 = tm * kTM, n0 = tn * kTN;
-  const int nkb = (g.K + kBK - 1) / kBK;
+  const int nkb = max((g.K + kBK - 1) / kBK, 1);
+  // Workgroups i, i + 8, ... share an XCD and its L2: they take a contiguous run of tiles
+  const int all = tiles_m * tiles_n, xcd = blockIdx.x & 7, per = all >> 3, more = all & 7;
+  const int stride = ((int)gridDim.x - xcd + 7) >> 3;
+  const int end = (xcd + 1) * per + min(xcd + 1, more);
+  int tile = xcd * per + min(xcd, more) + (blockIdx.x >> 3);
 
-  // Instruction j of a wave fills rows 8 (j waves + wave) .. + 7 of a tile
-  const int drow = lane >> 3, chunk = (lane & 7) ^ ((drow >> 1) | (wave & 1) << 2);
-  const v4i buf_a = buffer_at(g.a + (int64_t)m0 * g.a_stride), buf_b = buffer_at(g.b + (int64_t)n0 * g.b_stride);
-  uint32_t off_a[S::a_loads], off_b[S::b_loads];
-#pragma unroll
-  for (int j = 0; j < S::a_loads; ++j) {
-    const int r = (j * S::waves + wave) * 8 + drow;
-    off_a[j] = m0 + r < g.M ? (uint32_t)r * (uint32_t)g.a_stride + 16u * chunk : kOutside;
-  }
-#pragma unroll
-  for (int j = 0; j < S::b_loads; ++j) {
-    const int r = (j * S::waves + wave) * 8 + drow;
-    off_b[j] = n0 + r < g.N ? (uint32_t)r * (uint32_t)g.b_stride + 16u * chunk : kOutside;
-  }
-  const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(lds) + wave * 1024);
-  auto issue_a = [&](int kb, int j) {
-    const bool out = kb * kBK + 16 * chunk >= g.K;                   // behind the last chunk of K
-    dma16(buf_a, out ? kOutside : off_a[j], kb * kBK, base + (kb & 1) * S::slot + j * S::waves * 1024);
+  auto place = [&](int t, int& m0, int& n0) {
+    tile_at<1024 / kTM>(t, tiles_m, tiles_n, m0, n0);
+    m0 *= kTM;
+    n0 *= kTN;
   };
-  auto issue_b = [&](int kb, int j) {
-    const bool out = kb * kBK + 16 * chunk >= g.K;
-    dma16(buf_b, out ? kOutside : off_b[j], kb * kBK, base + (kb & 1) * S::slot + kTM * kBK + j * S::waves * 1024);
+
+  // The stream's next block: kb_in of tile tile_in.  Instruction j of a wave fills rows
+  // 8 (j waves + wave) .. + 7 of a tile.
+  const int drow = lane >> 3, chunk = (lane & 7) ^ ((drow >> 1) | (wave & 1) << 2);
+  int tile_in = tile, kb_in = 0;
+  v4i buf_a, buf_b;
+  uint32_t off_a[S::a_loads], off_b[S::b_loads];
+  auto enter = [&]() {
+    int m0 = 0, n0 = 0;
+    if (tile_in < end) place(tile_in, m0, n0);
+    const int rows_a = tile_in < end ? g.M - m0 : 0, rows_b = tile_in < end ? g.N - n0 : 0;
+    buf_a = buffer_at(g.a + (int64_t)m0 * g.a_stride);
+    buf_b = buffer_at(g.b + (int64_t)n0 * g.b_stride);
+#pragma unroll
+    for (int j = 0; j < S::a_loads; ++j) {
+      const int r = (j * S::waves + wave) * 8 + drow;
+      off_a[j] = r < rows_a ? (uint32_t)r * (uint32_t)g.a_stride + 16u * chunk : kOutside;
+    }
+#pragma unroll
+    for (int j = 0; j < S::b_loads; ++j) {
+      const int r = (j * S::waves + wave) * 8 + drow;
+      off_b[j] = r < rows_b ? (uint32_t)r * (uint32_t)g.b_stride + 16u * chunk : kOutside;
+    }
+  };
+  const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(lds) + wave * 1024);
+  auto issue_a = [&](int slot, int j) {
+    const bool out = kb_in * kBK + 16 * chunk >= g.K;                // behind the last chunk of K
+    dma16(buf_a, out ? kOutside : off_a[j], kb_in * kBK, base + slot * S::slot + j * S::waves * 1024);
+  };
+  auto issue_b = [&](int slot, int j) {
+    const bool out = kb_in * kBK + 16 * chunk >= g.K;
+    dma16(buf_b, out ? kOutside : off_b[j], kb_in * kBK, base + slot * S::slot + kTM * kBK + j * S::waves * 1024);
+  };
+  auto advance = [&]() {
+    if (++kb_in < nkb) return;
+    kb_in = 0;
+    tile_in += stride;
+    enter();
   };
 
   const int wm = wave / kWN * (16 * S::mt), wn = wave % kWN * (16 * S::nt);
   const int r16 = lane & 15, quarter = lane >> 4;
   v4i acc[S::mt][S::nt];
-#pragma unroll
-  for (int i = 0; i < S::mt; ++i)
-#pragma unroll
-    for (int j = 0; j < S::nt; ++j) acc[i][j] = v4i{};
-
   // Fragments of 64 bytes of K (half s of a block).  Those of A are read for the next half as
   // soon as their products of this one are issued, those of B into a second set.
   v4i a[S::mt], b[2][S::nt];
   const int row_a = (wm + r16) * kBK, row_b = (kTM + wn + r16) * kBK;
-  auto read_a = [&](int kb, int s, int i) {
-    a[i] = *reinterpret_cast<const v4i*>(lds + (kb & 1) * S::slot + row_a + 16 * i * kBK +
+  auto read_a = [&](int slot, int s, int i) {
+    a[i] = *reinterpret_cast<const v4i*>(lds + slot * S::slot + row_a + 16 * i * kBK +
                                          (((4 * s + quarter) ^ (r16 >> 1)) << 4));
   };
-  auto read_b = [&](int kb, int s, int j) {
-    b[s][j] = *reinterpret_cast<const v4i*>(lds + (kb & 1) * S::slot + row_b + 16 * j * kBK +
+  auto read_b = [&](int slot, int s, int j) {
+    b[s][j] = *reinterpret_cast<const v4i*>(lds + slot * S::slot + row_b + 16 * j * kBK +
                                             (((4 * s + quarter) ^ (r16 >> 1)) << 4));
   };
 
+  enter();
 #pragma unroll
-  for (int j = 0; j < S::a_loads; ++j) issue_a(0, j);
+  for (int t = 0; t < 2; ++t) {
 #pragma unroll
-  for (int j = 0; j < S::b_loads; ++j) issue_b(0, j);
-  wait_vmcnt<0>();
+    for (int j = 0; j < S::a_loads; ++j) issue_a(t, j);
+#pragma unroll
+    for (int j = 0; j < S::b_loads; ++j) issue_b(t, j);
+    advance();
+  }
+  wait_vmcnt<S::a_loads + S::b_loads>();
   barrier();
-#pragma unroll
-  for (int j = 0; j < S::a_loads; ++j) issue_a(1, j);
-#pragma unroll
-  for (int j = 0; j < S::b_loads; ++j) issue_b(1, j);
 #pragma unroll
   for (int j = 0; j < S::nt; ++j) read_b(0, 0, j);
 #pragma unroll
   for (int i = 0; i < S::mt; ++i) read_a(0, 0, i);
-  for (int kb = 0; kb < nkb; ++kb) {
+
+  // A wave's stores of a whole tile.  The vector memory counter counts down in order, and they
+  // are behind the loads of the block that the next wait is for, so it need not be for them.
+  constexpr int kRows = kOut == kBf16 ? 32 : 16, kStores = 16 * S::mt / kRows * 4;
+  bool stored = false;
+  int slot = 0;
+  for (;;) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s == 1) {
-        // The next block has landed for every wave, and every wave has read this one: the
-        // next but one takes its slot (blocks behind the last read no memory)
-        wait_vmcnt<0>();
-        barrier();
-      }
+    for (int i = 0; i < S::mt; ++i)
 #pragma unroll
-      for (int i = 0; i < S::mt; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < S::nt; ++j) acc[i][j] = v4i{};
+    for (int kb = 0; kb < nkb; ++kb) {
 #pragma unroll
-        for (int j = 0; j < S::nt; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[s][j], a[i], acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (i < S::nt) read_b(kb + s, s ^ 1, i);
-        read_a(kb + s, s ^ 1, i);
+      for (int s = 0; s < 2; ++s) {
         if (s == 1) {
+          // The next block has landed for every wave, and every wave has read this one: the
+          // next but one takes its slot (blocks behind the last tile read no memory)
+          if (stored) wait_vmcnt<kStores>();
+          else wait_vmcnt<0>();
+          stored = false;
+          barrier();
+        }
 #pragma unroll
-          for (int j = i; j < S::a_loads; j += S::mt) issue_a(kb + 2, j);
+        for (int i = 0; i < S::mt; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int j = (i + S::mt / 2) % S::mt; j < S::b_loads; j += S::mt) issue_b(kb + 2, j);
+          for (int j = 0; j < S::nt; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[s][j], a[i], acc[i][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          if (i < S::nt) read_b(slot ^ s, s ^ 1, i);
+          read_a(slot ^ s, s ^ 1, i);
+          if (s == 1) {
+            if (i < S::a_loads) issue_a(slot, i);
+            if (i >= S::mt - S::b_loads) issue_b(slot, i - (S::mt - S::b_loads));
+          }
         }
       }
+      advance();
+      slot ^= 1;
     }
-  }
-  wait_vmcnt<0>();
-  barrier();   // every wave done with the ring before it becomes the output stage
 
-  // 32 rows at a time through the wave's part of LDS, then eight columns a lane
-  int* out = reinterpret_cast<int*>(lds) + wave * 32 * S::stage_ld;
-  const int n = n0 + wn + 8 * (lane & 7);
-  const Columns cols = columns_at(g, n);
+    int m0, n0;
+    place(tile, m0, n0);
+    m0 += wm;
+    n0 += wn;
+    v4f sb[S::nt];
+    float sa[S::mt];
 #pragma unroll
-  for (int i = 0; i < S::mt; i += 2) {
+    for (int j = 0; j < S::nt; ++j) sb[j] = four_at(g.b_scales, g.b_step, n0 + 16 * j + 4 * quarter, g.N);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < S::mt; ++i)
+      sa[i] = g.a_scales[(int64_t)min(m0 + 16 * i + r16, g.M - 1) * g.a_step];
+    // kRows rows of 64 results at a time through the wave's own part of LDS, then 16 bytes a
+    // lane; 16-byte chunk c of row r at c ^ r, so that rows meet in no bank
+    uint8_t* out = lds + 2 * S::slot + wave * S::stage;
+    constexpr int kChunks = kOut == kBf16 ? 8 : 16, kEach = 64 / kChunks;   // chunks of a row, results of a chunk
+    const bool whole = m0 + 16 * S::mt <= g.M && n0 + 64 <= g.N && g.N % kEach == 0;
 #pragma unroll
-      for (int j = 0; j < S::nt; ++j)
-        *reinterpret_cast<v4i*>(out + (16 * h + r16) * S::stage_ld + 16 * j + 4 * quarter) = acc[i + h][j];
-    wave_sync();
+    for (int i = 0; i < S::mt; i += kRows / 16) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int row = 8 * s + (lane >> 3), m = m0 + wm + 16 * i + row;
-      const int* x = out + row * S::stage_ld + 8 * (lane & 7);
-      const v4i lo = *reinterpret_cast<const v4i*>(x), hi = *reinterpret_cast<const v4i*>(x + 4);
-      if (m < g.M) {
-        float v[8];
-        scaled(lo, hi, g.a_scales[(int64_t)m * g.a_step], cols, g.bias != nullptr, v);
-        store_out8<kOut>(g.c, m, n, g.N, v);
+      for (int h = 0; h < kRows / 16; ++h)
+#pragma unroll
+        for (int j = 0; j < S::nt; ++j) {
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = (float)acc[i + h][j][r] * sa[i + h] * sb[j][r];
+          if (g.bias) {   // (read again for every row: held, its 16 registers spilled others)
+            const v4f bias = four_at(g.bias, 1, n0 + 16 * j + 4 * quarter, g.N);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += bias[r];
+          }
+          const int row = 16 * h + r16;
+          if constexpr (kOut == kBf16)
+            *reinterpret_cast<uint2*>(out + row * 128 + (((2 * j + (quarter >> 1)) ^ (row & 7)) << 4) +
+                                      8 * (quarter & 1)) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+          else
+            *reinterpret_cast<v4f*>(out + row * 256 + (((4 * j + quarter) ^ row) << 4)) = v4f{v[0], v[1], v[2], v[3]};
+        }
+      wave_sync();
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int row = s * (kRows / 4) + lane / kChunks, c = lane % kChunks;
+        const uint4 x = *reinterpret_cast<const uint4*>(out + row * (kChunks * 16) + ((c ^ (row & (kChunks - 1))) << 4));
+        const int m = m0 + 16 * i + row, n = n0 + kEach * c;
+        uint8_t* p = reinterpret_cast<uint8_t*>(g.c) + ((int64_t)m * g.N + n) * (16 / kEach);
+        if (whole) {
+          st_nt16(p, x.x, x.y, x.z, x.w);
+        } else if (m < g.M) {
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < kEach; ++e)
+            if (n + e < g.N) {
+              if constexpr (kOut == kBf16) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+              else reinterpret_cast<uint32_t*>(p)[e] = w[e];
+            }
+        }
       }
+      wave_sync();
     }
-    wave_sync();
+    stored = whole;
+    tile += stride;
+    if (tile >= end) break;
   }
+  wait_vmcnt<0>();   // no load into LDS outlives the workgroup
 }
 
 // ---------------------------------------------------------------------------
@@ -403,12 +488,13 @@ hipError_t launch_ring(const Int8Args& g, bool out_bf16, hipStream_t st) {
   return hipGetLastError();
 }
 
+// `most` workgroups take the tiles in turn.
 template <int kTM, int kTN, int kWM, int kWN>
-hipError_t launch_tile(const Int8Args& g, bool out_bf16, hipStream_t st) {
+hipError_t launch_tile(const Int8Args& g, bool out_bf16, int64_t most, hipStream_t st) {
   const int tiles_m = (g.M + kTM - 1) / kTM, tiles_n = (g.N + kTN - 1) / kTN;
-  const uint32_t grid = (uint32_t)tiles_m * (uint32_t)tiles_n;
-  if (out_bf16) k_gemm_int8<kTM, kTN, kWM, kWN, kBf16><<<grid, 64 * kWM * kWN, 0, st>>>(g, tiles_m, tiles_n);
-  else k_gemm_int8<kTM, kTN, kWM, kWN, kF32><<<grid, 64 * kWM * kWN, 0, st>>>(g, tiles_m, tiles_n);
+  const uint32_t grid = (uint32_t)std::min((int64_t)tiles_m * tiles_n, most);
+  if (out_bf16) k_int8_tile<kTM, kTN, kWM, kWN, kBf16><<<grid, 64 * kWM * kWN, 0, st>>>(g, tiles_m, tiles_n);
+  else k_int8_tile<kTM, kTN, kWM, kWN, kF32><<<grid, 64 * kWM * kWN, 0, st>>>(g, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
@@ -427,11 +513,12 @@ int64_t ring_cost(const Int8Args& g, int tm, int tn) { return (tiles(g, tm, tn) 
 // channels 13.9 / 11.2 / 11.3 for tiles 16 x 16, 16 x 32, 32 x 64; 64 rows 28 / 13.9 / 12.7 /
 // 17.4 for 16, 32, 64, 128 columns, over 4096 channels 8.9 / 8.2 / 10.3 / 16.0; 128 rows over
 // 4096 11.0 / 14.7 / 25 for 32, 64, 128 columns, over 28672 54 / 37.6 / 35.5.)
-// More rows: rings of 128 x 64, two 128 x 128 tiles per CU or one 256 x 256 tile, by
-// what a round of them takes per 4096 of K: 16 us for 256 rings and 13.5 for 256 more;
-// 28 us for 256 tiles of 128 x 128, 40 for 512; 70 us for 256 of 256 x 256.  (512 rows
-// over 4096 channels 16 / 26 / 45, 1024 rows 27 / 28 / 46, 2048 rows 59 / 39 / 50,
-// 4096 rows 120 / 82 / 71.)
+// More rows: what rings of 128 x 64, tiles of 128 x 128 (two a CU) and tiles of 256 x 256 are
+// estimated to take.  (Measured, us: 512 rows over 4096 channels of 4096 16 / 26 / 44, 1024
+// rows 27 / 26 / 44, 2048 rows 60 / 40 / 47, 4096 rows 151 / 83 / 65, 512 rows over 4096
+// channels of 14336 43 / 76 / 127, 8192 over 7168 of 2048 269 / 146 / 125.  The last, partial
+// round of 256 x 256 tiles cut into 128 x 128 ones in a second launch gained nothing: 124, and
+// 125 against 113 for 2048 over 14336 of 4096.)
 hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st) {
   if (g.M <= 16) {
     const int64_t c16 = ring_cost(g, 16, 16), c32 = ring_cost(g, 16, 32), c64 = ring_cost(g, 32, 64);
@@ -454,12 +541,13 @@ hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st) {
     return launch_ring<64, 16, 512, 1, 1, 1>(g, out_bf16, st);
   }
   if (ring_cost(g, 128, 32) <= ring_cost(g, 128, 64)) return launch_ring<128, 32, 256, 2, 1, 1>(g, out_bf16, st);
-  const int64_t ring = (tiles(g, 128, 64) + 255) / 256, small = tiles(g, 128, 128);
-  const double by_ring = 2.5 + 13.5 * ring, by_large = 70.0 * ((tiles(g, 256, 256) + 255) / 256);
-  const double by_small = small / 512 * 40.0 + (small % 512 > 256 ? 40.0 : small % 512 ? 28.0 : 0.0);
+  const double k = g.K / 4096.0;
+  const int64_t rings = (tiles(g, 128, 64) + 255) / 256, small = tiles(g, 128, 128), large = (tiles(g, 256, 256) + 255) / 256;
+  const double by_ring = 3 + 12 * k + (1 + 11 * k) * (rings - 1), by_large = 8 + (54 * k + 3) * large;
+  const double by_small = 4 + 36 * k * (small / 512) + (small % 512 > 256 ? 36 * k : small % 512 ? 22 * k : 0);
   if (by_ring <= by_small && by_ring <= by_large) return launch_ring<128, 64, 128, 2, 2, 2>(g, out_bf16, st);
-  if (by_small <= by_large) return launch_tile<128, 128, 2, 2>(g, out_bf16, st);
-  return launch_tile<256, 256, 2, 4>(g, out_bf16, st);
+  if (by_small <= by_large) return launch_tile<128, 128, 2, 2>(g, out_bf16, small, st);
+  return launch_tile<256, 256, 2, 4>(g, out_bf16, 256, st);
 }
 
 }  // namespace pqb

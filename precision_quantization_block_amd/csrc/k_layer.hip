@@ -12,9 +12,10 @@
 // in the codes: they are formed from u, before r is known, and the stored scale is
 // s r.  So an RMS norm's codes depend on no sum.
 //
-// A row stays in registers (kTpr threads, kU units of 8 elements each) from its
-// one read to its one write; the row's sums and maxima meet by DPP, two shuffles and
-// one LDS exchange.  All of it is bound by HBM, and by latency where there are few rows.
+// A row stays in registers (kU units of 8 elements a thread) from its one read to its one
+// write; the row's sums and maxima meet by DPP, two shuffles and one LDS exchange.  A
+// workgroup has one row and as many waves as that takes, or four rows of up to 1024
+// elements, a wave each.  All of it is bound by HBM, and by latency where there are few rows.
 #include "launch.h"
 #include "quant.h"
 
@@ -22,13 +23,16 @@ namespace pqb {
 namespace {
 
 // ---------------------------------------------------------------------------
-// A row in registers.  kVec: unit k of thread t is elements 8 (k kTpr + t) ..., by
+// A row in registers.  Thread t of n, kVec: unit k is elements 8 (k n + t) ..., by
 // 16-byte accesses.  Otherwise (odd widths, strides or addresses) element j of
-// unit k is (8 k + j) kTpr + t, so that neighbours still share a line.
+// unit k is (8 k + j) n + t, so that neighbours still share a line.
 // ---------------------------------------------------------------------------
-template <bool kVec, int kTpr>
-__device__ __forceinline__ int elem_at(int k, int j, int t) {
-  return kVec ? 8 * (k * kTpr + t) + j : (8 * k + j) * kTpr + t;
+struct Who {
+  int t, n;
+};
+template <bool kVec>
+__device__ __forceinline__ int elem_at(int k, int j, Who w) {
+  return kVec ? 8 * (k * w.n + w.t) + j : (8 * k + j) * w.n + w.t;
 }
 
 __device__ __forceinline__ Raw8 load_cached8(const uint16_t* p) {
@@ -39,13 +43,13 @@ __device__ __forceinline__ Raw8 load_cached8(const float* p) {
 }
 
 // kOnce: read by this thread only (non-temporal); else shared with other rows.
-template <bool kVec, int kTpr, int kU, bool kOnce, typename T>
-__device__ __forceinline__ void load_row(const T* __restrict__ p, int cols, int t, float (&v)[kU][8]) {
+template <bool kVec, int kU, bool kOnce, typename T>
+__device__ __forceinline__ void load_row(const T* __restrict__ p, int cols, Who t, float (&v)[kU][8]) {
   if constexpr (kVec) {
     Raw8 raw[kU];
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      const int e = elem_at<true, kTpr>(k, 0, t);
+      const int e = elem_at<true>(k, 0, t);
       raw[k] = e < cols ? (kOnce ? load_raw8(p + e) : load_cached8(p + e)) : Raw8{};
     }
 #pragma unroll
@@ -55,7 +59,7 @@ __device__ __forceinline__ void load_row(const T* __restrict__ p, int cols, int 
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int e = elem_at<false, kTpr>(k, j, t);
+        const int e = elem_at<false>(k, j, t);
         v[k][j] = e < cols ? ld1(p + e) : 0.0f;
       }
   }
@@ -74,17 +78,17 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   st_nt16(p + 4, as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7]));
 }
 
-template <bool kVec, int kTpr, int kU, typename T>
-__device__ __forceinline__ void store_row(T* __restrict__ p, int cols, int t, const float (&v)[kU][8]) {
+template <bool kVec, int kU, typename T>
+__device__ __forceinline__ void store_row(T* __restrict__ p, int cols, Who t, const float (&v)[kU][8]) {
 #pragma unroll
   for (int k = 0; k < kU; ++k) {
     if constexpr (kVec) {
-      const int e = elem_at<true, kTpr>(k, 0, t);
+      const int e = elem_at<true>(k, 0, t);
       if (e < cols) store8(p + e, v[k]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int e = elem_at<false, kTpr>(k, j, t);
+        const int e = elem_at<false>(k, j, t);
         if (e < cols) store1(p + e, v[k][j]);
       }
     }
@@ -104,19 +108,19 @@ __device__ __forceinline__ float scale_of(int elem, uint32_t amax) {
                      : elem == kE4M3 ? fp8_scale_bits<kE4M3>(amax) : fp8_scale_bits<kE5M2>(amax);
 }
 
-template <bool kVec, int kTpr, int kU>
-__device__ __forceinline__ void store_codes(uint8_t* __restrict__ p, int cols, int t, int elem, float s,
+template <bool kVec, int kU>
+__device__ __forceinline__ void store_codes(uint8_t* __restrict__ p, int cols, Who t, int elem, float s,
                                             const float (&v)[kU][8]) {
 #pragma unroll
   for (int k = 0; k < kU; ++k) {
     const uint2 w = pack_codes(elem, v[k], s);
     if constexpr (kVec) {
-      const int e = elem_at<true, kTpr>(k, 0, t);
+      const int e = elem_at<true>(k, 0, t);
       if (e < cols) st_nt8(p + e, w.x, w.y);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int e = elem_at<false, kTpr>(k, j, t);
+        const int e = elem_at<false>(k, j, t);
         if (e < cols) p[e] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
       }
     }
@@ -124,7 +128,7 @@ __device__ __forceinline__ void store_codes(uint8_t* __restrict__ p, int cols, i
 }
 
 // ---------------------------------------------------------------------------
-// Reductions over the kTpr threads of a row; every thread receives the result.
+// Reductions over the threads of a row; every thread receives the result.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float wave_sum(float v) {
   v += as_f(dpp<kDppXor1>(as_u(v)));
@@ -140,21 +144,20 @@ struct SumMax {
   float sum;
   uint32_t max;
 };
+constexpr int kWaves = 16;   // at most, of a workgroup
 
-// The sum and the largest bit pattern at once.  `red` (kTpr / 64 entries) is free to be
-// written when the call starts; a second call takes another one.
-template <int kTpr>
+// The sum and the largest bit pattern at once.  `red` (kWaves entries) is free to be
+// written when the call starts; a second call takes another one.  kMany: a row a wave.
+template <bool kMany>
 __device__ __forceinline__ SumMax row_reduce(float sum, uint32_t most, SumMax* red) {
   sum = wave_sum(sum);
   most = wave_umax(most);
-  if constexpr (kTpr > kWave) {
-    constexpr int kWaves = kTpr / kWave;
+  if constexpr (!kMany) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = SumMax{sum, most};
     __syncthreads();
     sum = 0.0f;
     most = 0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < (int)blockDim.x >> 6; ++i) {
       sum += red[i].sum;
       most = max(most, red[i].max);
     }
@@ -172,8 +175,8 @@ __device__ __forceinline__ uint32_t amax_of(const float (&v)[kU][8]) {
 
 // (mean, r) of a row; kinds: RMS (mean 0) or layer.  v keeps its values, centred for a
 // layer norm (elements behind the row stay 0).
-template <bool kVec, int kTpr, int kU>
-__device__ __forceinline__ float norm_stats(bool layer, float eps, int cols, int t, float (&v)[kU][8],
+template <bool kVec, bool kMany, int kU>
+__device__ __forceinline__ float norm_stats(bool layer, float eps, int cols, Who t, float (&v)[kU][8],
                                             SumMax* red) {
   if (layer) {
     float s = 0.0f;
@@ -181,39 +184,56 @@ __device__ __forceinline__ float norm_stats(bool layer, float eps, int cols, int
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += v[k][j];
-    const float mean = row_reduce<kTpr>(s, 0, red).sum / (float)cols;
+    const float mean = row_reduce<kMany>(s, 0, red).sum / (float)cols;
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        v[k][j] = elem_at<kVec, kTpr>(k, j, t) < cols ? v[k][j] - mean : 0.0f;
+        v[k][j] = elem_at<kVec>(k, j, t) < cols ? v[k][j] - mean : 0.0f;
   }
   float q = 0.0f;
 #pragma unroll
   for (int k = 0; k < kU; ++k)
 #pragma unroll
     for (int j = 0; j < 8; ++j) q = __builtin_fmaf(v[k][j], v[k][j], q);
-  const float ms = row_reduce<kTpr>(q, 0, red + kTpr / kWave).sum / (float)cols;
+  const float ms = row_reduce<kMany>(q, 0, red + kWaves).sum / (float)cols;
   return 1.0f / sqrtf(ms + eps);
 }
 
-constexpr int block_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+// How rows are taken: four a workgroup, a wave each, or one by up to kThreads threads; kU
+// units a thread.
+template <int kUnits, int kMost>
+struct Shape {
+  static constexpr bool many = kMost == 0;
+  static constexpr int kU = kUnits, threads = many ? 256 : kMost;
+};
 
-template <typename T, bool kVec, int kTpr, int kU>
-__global__ __launch_bounds__(block_of(kTpr)) void k_norm(NormArgs a) {
-  constexpr int kRows = block_of(kTpr) / kTpr, kRed = kTpr / kWave;
-  __shared__ SumMax red[5 * kRed];
-  const int t = threadIdx.x % kTpr;
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kTpr;
-  if (kRows > 1 && row >= a.rows) return;   // whole waves; no barrier with several rows
+// This thread's row and place in it.
+template <bool kMany>
+__device__ __forceinline__ int64_t row_of(Who& t) {
+  t = kMany ? Who{(int)threadIdx.x & 63, 64} : Who{(int)threadIdx.x, (int)blockDim.x};
+  return kMany ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+}
 
-  float v[kU][8];
-  load_row<kVec, kTpr, kU, true>(reinterpret_cast<const T*>(a.x) + row * a.x_stride, a.cols, t, v);
+template <typename T, bool kVec, typename S>
+__global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
+  constexpr bool kMany = S::many;
+  constexpr int kU = S::kU;
+  __shared__ SumMax red[5 * kWaves];
+  Who t;
+  const int64_t row = row_of<kMany>(t);
+  if (kMany && row >= a.rows) return;   // whole waves; no barrier with several rows
+
+  // everything that the row alone decides is on its way before the first sum
+  float v[kU][8], res[kU][8];
+  load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.x) + row * a.x_stride, a.cols, t, v);
+  if (a.residual)
+    load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.residual) + row * a.res_stride, a.cols, t, res);
   const bool layer = a.layer;
   if (a.post) {
-    const float r = norm_stats<kVec, kTpr, kU>(layer, a.eps, a.cols, t, v, red + 3 * kRed);
+    const float r = norm_stats<kVec, kMany, kU>(layer, a.eps, a.cols, t, v, red + 3 * kWaves);
     float w[kU][8];
-    load_row<kVec, kTpr, kU, false>(reinterpret_cast<const T*>(a.post), a.cols, t, w);
+    load_row<kVec, kU, false>(reinterpret_cast<const T*>(a.post), a.cols, t, w);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
@@ -221,7 +241,7 @@ __global__ __launch_bounds__(block_of(kTpr)) void k_norm(NormArgs a) {
   }
   if (a.gate) {
     float g[kU][8];
-    load_row<kVec, kTpr, kU, false>(
+    load_row<kVec, kU, false>(
         reinterpret_cast<const T*>(a.gate) + (int64_t)((uint32_t)row / a.per_gate) * a.gate_stride, a.cols, t, g);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
@@ -229,16 +249,14 @@ __global__ __launch_bounds__(block_of(kTpr)) void k_norm(NormArgs a) {
       for (int j = 0; j < 8; ++j) v[k][j] *= g[k][j];
   }
   if (a.residual) {
-    float g[kU][8];
-    load_row<kVec, kTpr, kU, true>(reinterpret_cast<const T*>(a.residual) + row * a.res_stride, a.cols, t, g);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[k][j] += g[k][j] * a.res_scale;
+      for (int j = 0; j < 8; ++j) v[k][j] += res[k][j] * a.res_scale;
   }
   if (a.h) {
     T* h = reinterpret_cast<T*>(a.h) + row * a.h_stride;
-    store_row<kVec, kTpr, kU>(h, a.cols, t, v);
+    store_row<kVec, kU>(h, a.cols, t, v);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
@@ -248,7 +266,7 @@ __global__ __launch_bounds__(block_of(kTpr)) void k_norm(NormArgs a) {
   // u, and r where it is not in u
   float w[kU][8];
   if (a.weight) {
-    load_row<kVec, kTpr, kU, false>(reinterpret_cast<const T*>(a.weight), a.cols, t, w);
+    load_row<kVec, kU, false>(reinterpret_cast<const T*>(a.weight), a.cols, t, w);
   } else {
 #pragma unroll
     for (int k = 0; k < kU; ++k)
@@ -258,14 +276,14 @@ __global__ __launch_bounds__(block_of(kTpr)) void k_norm(NormArgs a) {
   float r = 1.0f;
   uint32_t most = 0;
   if (layer) {
-    const float rl = norm_stats<kVec, kTpr, kU>(true, a.eps, a.cols, t, v, red);
+    const float rl = norm_stats<kVec, kMany, kU>(true, a.eps, a.cols, t, v, red);
     float b[kU][8] = {};
-    if (a.bias) load_row<kVec, kTpr, kU, false>(reinterpret_cast<const T*>(a.bias), a.cols, t, b);
+    if (a.bias) load_row<kVec, kU, false>(reinterpret_cast<const T*>(a.bias), a.cols, t, b);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * rl * w[k][j] + b[k][j];
-    if (a.form == kFormRow) most = row_reduce<kTpr>(0.0f, amax_of(v), red + 2 * kRed).max;
+    if (a.form == kFormRow) most = row_reduce<kMany>(0.0f, amax_of(v), red + 2 * kWaves).max;
   } else {
     float q = 0.0f;
 #pragma unroll
@@ -275,7 +293,7 @@ __global__ __launch_bounds__(block_of(kTpr)) void k_norm(NormArgs a) {
         q = __builtin_fmaf(v[k][j], v[k][j], q);
         v[k][j] *= w[k][j];
       }
-    const SumMax m = row_reduce<kTpr>(q, amax_of(v), red);
+    const SumMax m = row_reduce<kMany>(q, amax_of(v), red);
     r = 1.0f / sqrtf(m.sum / (float)a.cols + a.eps);
     most = m.max;
   }
@@ -285,20 +303,20 @@ __global__ __launch_bounds__(block_of(kTpr)) void k_norm(NormArgs a) {
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] *= r;
-    store_row<kVec, kTpr, kU>(reinterpret_cast<T*>(a.out) + row * a.cols, a.cols, t, v);
+    store_row<kVec, kU>(reinterpret_cast<T*>(a.out) + row * a.cols, a.cols, t, v);
   } else if (a.form == kFormRow) {
     const float s = scale_of(a.elem, most);
-    store_codes<kVec, kTpr, kU>(reinterpret_cast<uint8_t*>(a.out) + row * a.cols, a.cols, t, a.elem, s, v);
-    if (t == 0) a.scales[row] = s * r;
+    store_codes<kVec, kU>(reinterpret_cast<uint8_t*>(a.out) + row * a.cols, a.cols, t, a.elem, s, v);
+    if (t.t == 0) a.scales[row] = s * r;
   } else if constexpr (kVec) {   // 1x128 blocks: 16 threads each (cols % 128 == 0)
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      const int e = elem_at<true, kTpr>(k, 0, t);
+      const int e = elem_at<true>(k, 0, t);
       const float s = scale_of(a.elem, group_umax<16>(as_u(absmax8(v[k]))));
       const uint2 c = pack_codes(a.elem, v[k], s);
       if (e < a.cols) {
         st_nt8(reinterpret_cast<uint8_t*>(a.out) + row * a.cols + e, c.x, c.y);
-        if ((t & 15) == 0) a.scales[row * (a.cols / 128) + e / 128] = s * r;
+        if ((t.t & 15) == 0) a.scales[row * (a.cols / 128) + e / 128] = s * r;
       }
     }
   }
@@ -334,13 +352,13 @@ __device__ __forceinline__ float activate(int act, float g) {
   return p * p;
 }
 
-template <typename T, bool kVec, int kTpr, int kU>
-__device__ __forceinline__ void act_values(const ActArgs& a, int64_t row, int cols, int col0, int t,
+template <typename T, bool kVec, int kU>
+__device__ __forceinline__ void act_values(const ActArgs& a, int64_t row, int cols, int col0, Who t,
                                            float (&v)[kU][8]) {
   float up[kU][8];
-  load_row<kVec, kTpr, kU, true>(reinterpret_cast<const T*>(a.gate) + row * a.gate_stride + col0, cols, t, v);
+  load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.gate) + row * a.gate_stride + col0, cols, t, v);
   if (a.up)
-    load_row<kVec, kTpr, kU, true>(reinterpret_cast<const T*>(a.up) + row * a.up_stride + col0, cols, t, up);
+    load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.up) + row * a.up_stride + col0, cols, t, up);
 #pragma unroll
   for (int k = 0; k < kU; ++k)
 #pragma unroll
@@ -351,50 +369,61 @@ __device__ __forceinline__ void act_values(const ActArgs& a, int64_t row, int co
 }
 
 // A scale per row.
-template <typename T, bool kVec, int kTpr, int kU>
-__global__ __launch_bounds__(block_of(kTpr)) void k_act_row(ActArgs a) {
-  constexpr int kRows = block_of(kTpr) / kTpr;
-  __shared__ SumMax red[kTpr / kWave];
-  const int t = threadIdx.x % kTpr;
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kTpr;
-  if (kRows > 1 && row >= a.rows) return;
+template <typename T, bool kVec, typename S>
+__global__ __launch_bounds__(S::threads) void k_act_row(ActArgs a) {
+  constexpr bool kMany = S::many;
+  constexpr int kU = S::kU;
+  __shared__ SumMax red[kWaves];
+  Who t;
+  const int64_t row = row_of<kMany>(t);
+  if (kMany && row >= a.rows) return;
   float v[kU][8];
-  act_values<T, kVec, kTpr, kU>(a, row, a.cols, 0, t, v);
-  const float s = scale_of(a.elem, row_reduce<kTpr>(0.0f, amax_of(v), red).max);
-  store_codes<kVec, kTpr, kU>(reinterpret_cast<uint8_t*>(a.out) + row * a.cols, a.cols, t, a.elem, s, v);
-  if (t == 0) a.scales[row] = s;
+  act_values<T, kVec, kU>(a, row, a.cols, 0, t, v);
+  const float s = scale_of(a.elem, row_reduce<kMany>(0.0f, amax_of(v), red).max);
+  store_codes<kVec, kU>(reinterpret_cast<uint8_t*>(a.out) + row * a.cols, a.cols, t, a.elem, s, v);
+  if (t.t == 0) a.scales[row] = s;
 }
 
 // Plain values or 1x128 blocks: a workgroup takes 256 units of one row.
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void k_act_flat(ActArgs a, uint32_t pieces) {
-  const int t = threadIdx.x;
+  const Who t{(int)threadIdx.x, 256};
   const int64_t row = blockIdx.x / pieces;
   const int col0 = (int)(blockIdx.x % pieces) * 2048, cols = min(a.cols - col0, 2048);
   float v[1][8];
-  act_values<T, kVec, 256, 1>(a, row, cols, col0, t, v);
+  act_values<T, kVec, 1>(a, row, cols, col0, t, v);
   if (a.form == kFormPlain) {
-    store_row<kVec, 256, 1>(reinterpret_cast<T*>(a.out) + row * a.cols + col0, cols, t, v);
+    store_row<kVec, 1>(reinterpret_cast<T*>(a.out) + row * a.cols + col0, cols, t, v);
   } else if constexpr (kVec) {
     const float s = scale_of(a.elem, group_umax<16>(as_u(absmax8(v[0]))));
     const uint2 c = pack_codes(a.elem, v[0], s);
-    if (8 * t < cols) {
-      st_nt8(reinterpret_cast<uint8_t*>(a.out) + row * a.cols + col0 + 8 * t, c.x, c.y);
-      if ((t & 15) == 0) a.scales[row * (a.cols / 128) + (col0 + 8 * t) / 128] = s;
+    if (8 * t.t < cols) {
+      st_nt8(reinterpret_cast<uint8_t*>(a.out) + row * a.cols + col0 + 8 * t.t, c.x, c.y);
+      if ((t.t & 15) == 0) a.scales[row * (a.cols / 128) + (col0 + 8 * t.t) / 128] = s;
     }
   }
 }
 
-// f(threads per row, units per thread) for the smallest row shape that holds `cols`.
+// f(shape, grid, threads) for rows of `cols` elements.  Up to 512, or 1024 of many rows, fit a
+// wave; wider ones get as many waves as they need.  Threads without an element cost as much
+// as others (16384 rows of 1024: 21 us with 64 threads a row, 30 with 256), and fewer units a
+// thread shorten a few rows (64 of 4096: 3.2 / 3.9 / 4.0 us at 1 / 2 / 4 units) and cost
+// many little (8192 of 4096: 41.7 / 39.8 / 39.8).  Many wide rows of an activation are
+// faster with four units (8192 of 14336 118 us, 136 with two; 512 11.8 and 10.3), of a norm,
+// which holds more arrays, with two (4096 of 12288 59 us, 79 with four).
 template <typename F>
-void with_row_shape(int cols, F f) {
-  if (cols <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  else if (cols <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  else if (cols <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  else if (cols <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  else if (cols <= 8192) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
-  else if (cols <= 16384) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
-  else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+void with_row_shape(int64_t rows, int cols, bool light, F f) {
+  auto go = [&](auto shape) {
+    using S = decltype(shape);
+    if (S::many) f(shape, (uint32_t)((rows + 3) / 4), S::threads);
+    else f(shape, (uint32_t)rows, (cols + 512 * S::kU - 1) / (512 * S::kU) * 64);
+  };
+  if (cols <= 512) go(Shape<1, 0>{});
+  else if (cols <= 1024 && rows >= 4096) go(Shape<2, 0>{});
+  else if (cols <= 4096) go(Shape<1, 512>{});
+  else if (cols <= 8192) go(Shape<2, 512>{});
+  else if (cols <= 16384 && !(light && rows >= 2048)) go(Shape<2, 1024>{});
+  else go(Shape<4, 1024>{});
 }
 
 // f(T, whether 16-byte accesses fit).
@@ -406,20 +435,13 @@ void with_type(bool bf16, bool vec, F f) {
   else f((const float*)nullptr, std::false_type{});
 }
 
-template <typename K>
-uint32_t row_grid(int64_t rows, K tpr) {
-  constexpr int kRows = block_of(K::value) / K::value;
-  return (uint32_t)((rows + kRows - 1) / kRows);
-}
-
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, bool bf16, bool vec, hipStream_t st) {
   with_type(bf16, vec, [&](auto type, auto v) {
-    with_row_shape(a.cols, [&](auto tpr, auto units) {
+    with_row_shape(a.rows, a.cols, false, [&](auto shape, uint32_t grid, int threads) {
       using T = std::remove_const_t<std::remove_pointer_t<decltype(type)>>;
-      k_norm<T, decltype(v)::value, decltype(tpr)::value, decltype(units)::value>
-          <<<row_grid(a.rows, tpr), block_of(tpr), 0, st>>>(a);
+      k_norm<T, decltype(v)::value, decltype(shape)><<<grid, threads, 0, st>>>(a);
     });
   });
   return hipGetLastError();
@@ -430,9 +452,8 @@ hipError_t launch_act(const ActArgs& a, bool bf16, bool vec, hipStream_t st) {
     using T = std::remove_const_t<std::remove_pointer_t<decltype(type)>>;
     constexpr bool kVec = decltype(v)::value;
     if (a.form == kFormRow) {
-      with_row_shape(a.cols, [&](auto tpr, auto units) {
-        k_act_row<T, kVec, decltype(tpr)::value, decltype(units)::value>
-            <<<row_grid(a.rows, tpr), block_of(tpr), 0, st>>>(a);
+      with_row_shape(a.rows, a.cols, true, [&](auto shape, uint32_t grid, int threads) {
+        k_act_row<T, kVec, decltype(shape)><<<grid, threads, 0, st>>>(a);
       });
     } else {
       const uint32_t pieces = (uint32_t)(a.cols + 2047) / 2048;

@@ -7,7 +7,7 @@
 // in float32, to Taylor's polynomials of degree 9 and 10 (the next terms are below
 // 2^-29 there).
 //
-// A workgroup takes kTokens tokens: its threads form each cosine and sine once, into
+// A workgroup takes one token, or up to four of small heads: its threads form each cosine and sine once, into
 // LDS, and every head of q and k is then turned from there.  Reading and writing q and k
 // is all that costs: bound by HBM, by latency for few tokens.
 #include "launch.h"
@@ -16,7 +16,7 @@
 namespace pqb {
 namespace {
 
-constexpr int kThreads = 256, kTokens = 4;
+constexpr int kThreads = 256, kTokens = 4;   // (tokens of a workgroup at most)
 
 __device__ __forceinline__ float2 cos_sin(double turns, float amp) {
   turns -= __builtin_rint(turns);
@@ -55,6 +55,7 @@ __device__ __forceinline__ bool position_of(const RopeArgs& a, int64_t t, int& p
   return true;
 }
 
+// kV values: 16 bytes (8 of bf16, 4 of float32), or fewer one by one.
 template <int kV>
 __device__ __forceinline__ void load_v(const uint16_t* p, float (&v)[kV]) {
   if constexpr (kV == 8) widen8(load_raw8(p), p, v);
@@ -62,8 +63,12 @@ __device__ __forceinline__ void load_v(const uint16_t* p, float (&v)[kV]) {
 }
 template <int kV>
 __device__ __forceinline__ void load_v(const float* p, float (&v)[kV]) {
-  if constexpr (kV == 8) widen8(load_raw8(p), p, v);
-  else for (int j = 0; j < kV; ++j) v[j] = ld1(p + j);
+  if constexpr (kV == 4) {
+    const uint4 w = ld_nt16(p);
+    v[0] = as_f(w.x), v[1] = as_f(w.y), v[2] = as_f(w.z), v[3] = as_f(w.w);
+  } else {
+    for (int j = 0; j < kV; ++j) v[j] = ld1(p + j);
+  }
 }
 template <int kV>
 __device__ __forceinline__ void store_v(uint16_t* p, const float (&v)[kV]) {
@@ -74,23 +79,19 @@ __device__ __forceinline__ void store_v(uint16_t* p, const float (&v)[kV]) {
 }
 template <int kV>
 __device__ __forceinline__ void store_v(float* p, const float (&v)[kV]) {
-  if constexpr (kV == 8) {
-    st_nt16(p, as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
-    st_nt16(p + 4, as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7]));
-  } else {
-    for (int j = 0; j < kV; ++j) p[j] = v[j];
-  }
+  if constexpr (kV == 4) st_nt16(p, as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
+  else for (int j = 0; j < kV; ++j) p[j] = v[j];
 }
 
-// Parts of a head: kV = 8 consecutive values a thread (16-byte accesses), or 2 (pairs; any
-// even dim, stride and address).  A part is kV values of each half, kV / 2 pairs of an
-// interleaved head, or kV values behind `rot`.
+// Parts of a head, one a thread: kV values of each half, kV / 2 pairs of an interleaved head, or
+// kV values behind `rot`.  kV is 16 bytes' worth, or 1 (2 if interleaved) for any even
+// dim, stride and address.
 template <typename T, int kV, bool kInterleaved>
-__global__ __launch_bounds__(kThreads) void k_rope(RopeArgs a) {
+__global__ __launch_bounds__(kThreads) void k_rope(RopeArgs a, int tokens) {
   __shared__ float2 cs[kTokens * kRopeMaxRot / 2];
   __shared__ int owned[kTokens];
-  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
-  const int nt = (int)min((int64_t)kTokens, a.tokens - t0);
+  const int64_t t0 = (int64_t)blockIdx.x * tokens;
+  const int nt = (int)min((int64_t)tokens, a.tokens - t0);
   const int half = a.rot / 2;
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int t = i / half, p = i - t * half;
@@ -143,13 +144,19 @@ __global__ __launch_bounds__(kThreads) void k_rope(RopeArgs a) {
 
 template <typename T>
 void launch(const RopeArgs& a, bool vec, hipStream_t st) {
-  const uint32_t grid = (uint32_t)((a.tokens + kTokens - 1) / kTokens);
+  constexpr int kV = 16 / sizeof(T);
+  // As many tokens as give each thread a part (8192 tokens of 32 + 8 heads of 128, bf16: 29.0,
+  // 30.6 and 31.7 us with 1, 2 and 4; of 8 + 1 heads of 64: 8.6, 7.0 and 6.1)
+  const int64_t parts = (int64_t)(a.heads[0] + a.heads[1]) * ((a.interleaved ? a.rot : a.rot / 2) + a.dim - a.rot) /
+                        (vec ? kV : a.interleaved ? 2 : 1);
+  const int tokens = parts >= kThreads ? 1 : parts >= kThreads / 2 ? 2 : kTokens;
+  const uint32_t grid = (uint32_t)((a.tokens + tokens - 1) / tokens);
   if (a.interleaved) {
-    if (vec) k_rope<T, 8, true><<<grid, kThreads, 0, st>>>(a);
-    else k_rope<T, 2, true><<<grid, kThreads, 0, st>>>(a);
+    if (vec) k_rope<T, kV, true><<<grid, kThreads, 0, st>>>(a, tokens);
+    else k_rope<T, 2, true><<<grid, kThreads, 0, st>>>(a, tokens);
   } else {
-    if (vec) k_rope<T, 8, false><<<grid, kThreads, 0, st>>>(a);
-    else k_rope<T, 1, false><<<grid, kThreads, 0, st>>>(a);
+    if (vec) k_rope<T, kV, false><<<grid, kThreads, 0, st>>>(a, tokens);
+    else k_rope<T, 1, false><<<grid, kThreads, 0, st>>>(a, tokens);
   }
 }
 

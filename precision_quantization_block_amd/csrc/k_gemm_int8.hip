@@ -73,51 +73,23 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm
 
 enum Out { kF32 = 0, kBf16 = 1 };
 
-// Eight results of row m from column n on (n % 8 == 0).
+// Eight results of row m from column n on, N and n multiples of 8.
 template <int kOut>
 __device__ __forceinline__ void store_out8(void* c, int64_t m, int n, int N, const float (&v)[8]) {
-  if (N % 8 == 0) {
-    if (n >= N) return;
-    if constexpr (kOut == kBf16) {
-      st_nt16(reinterpret_cast<uint16_t*>(c) + m * N + n, bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
-              bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-    } else {
-      float* p = reinterpret_cast<float*>(c) + m * N + n;
-      st_nt16(p, as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
-      st_nt16(p + 4, as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7]));
-    }
+  if constexpr (kOut == kBf16) {
+    st_nt16(reinterpret_cast<uint16_t*>(c) + m * N + n, bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
+            bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (n + j < N) {
-        if constexpr (kOut == kBf16)
-          reinterpret_cast<uint16_t*>(c)[m * N + n + j] = (uint16_t)(bf16x2_rne(v[j], 0.0f) & 0xFFFFu);
-        else
-          reinterpret_cast<float*>(c)[m * N + n + j] = v[j];
-      }
+    float* p = reinterpret_cast<float*>(c) + m * N + n;
+    st_nt16(p, as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
+    st_nt16(p + 4, as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7]));
   }
 }
 
-// Scales and bias of eight columns from n on, 0 behind the last.
-struct Columns {
-  float s[8], b[8];
-};
-__device__ __forceinline__ Columns columns_at(const Int8Args& g, int n) {
-  Columns c;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const bool in = n + j < g.N;
-    c.s[j] = in ? g.b_scales[(int64_t)(n + j) * g.b_step] : 0.0f;
-    c.b[j] = in && g.bias ? g.bias[n + j] : 0.0f;
-  }
-  return c;
-}
-__device__ __forceinline__ void scaled(v4i lo, v4i hi, float sa, const Columns& c, bool bias, float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = (float)(j < 4 ? lo[j & 3] : hi[j & 3]) * sa * c.s[j];
-    if (bias) v[j] += c.b[j];
-  }
+// The result of sum x in row m, column n.
+__device__ __forceinline__ float scaled(const Int8Args& g, int x, int64_t m, int n) {
+  const float v = (float)x * g.a_scales[m * g.a_step] * g.b_scales[(int64_t)n * g.b_step];
+  return g.bias ? v + g.bias[n] : v;
 }
 
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -317,22 +289,23 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int ti
             *reinterpret_cast<v4f*>(out + row * 256 + (((4 * j + quarter) ^ row) << 4)) = v4f{v[0], v[1], v[2], v[3]};
         }
       wave_sync();
+      if (whole) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int row = s * (kRows / 4) + lane / kChunks, c = lane % kChunks;
-        const uint4 x = *reinterpret_cast<const uint4*>(out + row * (kChunks * 16) + ((c ^ (row & (kChunks - 1))) << 4));
-        const int m = m0 + 16 * i + row, n = n0 + kEach * c;
-        uint8_t* p = reinterpret_cast<uint8_t*>(g.c) + ((int64_t)m * g.N + n) * (16 / kEach);
-        if (whole) {
-          st_nt16(p, x.x, x.y, x.z, x.w);
-        } else if (m < g.M) {
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < kEach; ++e)
-            if (n + e < g.N) {
-              if constexpr (kOut == kBf16) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-              else reinterpret_cast<uint32_t*>(p)[e] = w[e];
-            }
+        for (int s = 0; s < 4; ++s) {
+          const int row = s * (kRows / 4) + lane / kChunks, c = lane % kChunks;
+          const uint4 x = *reinterpret_cast<const uint4*>(out + row * (kChunks * 16) + ((c ^ (row & (kChunks - 1))) << 4));
+          st_nt16(reinterpret_cast<uint8_t*>(g.c) + ((int64_t)(m0 + 16 * i + row) * g.N + n0 + kEach * c) * (16 / kEach),
+                  x.x, x.y, x.z, x.w);
+        }
+      } else if (n0 + lane < g.N) {   // a row of 64 at a time
+        const int rows = min(kRows, g.M - m0 - 16 * i);
+        for (int row = 0; row < rows; ++row) {
+          const uint8_t* x = out + row * (kChunks * 16) + (((lane / kEach) ^ (row & (kChunks - 1))) << 4);
+          const int64_t at = (int64_t)(m0 + 16 * i + row) * g.N + n0 + lane;
+          if constexpr (kOut == kBf16)
+            reinterpret_cast<uint16_t*>(g.c)[at] = reinterpret_cast<const uint16_t*>(x)[lane % kEach];
+          else
+            reinterpret_cast<float*>(g.c)[at] = reinterpret_cast<const float*>(x)[lane % kEach];
         }
       }
       wave_sync();
@@ -463,19 +436,35 @@ __global__ __launch_bounds__(512, 2 * kPer) void k_int8_ring(Int8Args g, int til
                               4 * quarter) = acc[i][j];
   __syncthreads();
   const int rows = min(g.M - m0, kTM);
-  for (int u = threadIdx.x; u < rows * (kTN / 8); u += 512) {   // eight columns of a row
-    const int r = u / (kTN / 8), c = 8 * (u % (kTN / 8)), n = n0 + c;
-    if (n >= g.N) continue;
-    v4i lo{}, hi{};
+  if (g.N % 8 == 0) {
+    for (int u = threadIdx.x; u < rows * (kTN / 8); u += 512) {   // eight columns of a row
+      const int r = u / (kTN / 8), c = 8 * (u % (kTN / 8)), n = n0 + c;
+      if (n >= g.N) continue;
+      v4i lo{}, hi{};
 #pragma unroll
-    for (int w = 0; w < S::wk; ++w) {
-      const v4i* p = reinterpret_cast<const v4i*>(sums + (w * kTM + r) * S::ld + c);
-      lo += p[0];
-      hi += p[1];
+      for (int w = 0; w < S::wk; ++w) {
+        const v4i* p = reinterpret_cast<const v4i*>(sums + (w * kTM + r) * S::ld + c);
+        lo += p[0];
+        hi += p[1];
+      }
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = scaled(g, j < 4 ? lo[j & 3] : hi[j & 3], m0 + r, n + j);
+      store_out8<kOut>(g.c, m0 + r, n, g.N, v);
     }
-    float v[8];
-    scaled(lo, hi, g.a_scales[(int64_t)(m0 + r) * g.a_step], columns_at(g, n), g.bias != nullptr, v);
-    store_out8<kOut>(g.c, m0 + r, n, g.N, v);
+  } else {
+    for (int u = threadIdx.x; u < rows * kTN; u += 512) {
+      const int r = u / kTN, c = u % kTN, n = n0 + c;
+      if (n >= g.N) continue;
+      int x = 0;
+#pragma unroll
+      for (int w = 0; w < S::wk; ++w) x += sums[(w * kTM + r) * S::ld + c];
+      const float v = scaled(g, x, m0 + r, n);
+      if constexpr (kOut == kBf16)
+        reinterpret_cast<uint16_t*>(g.c)[(int64_t)(m0 + r) * g.N + n] = (uint16_t)(bf16x2_rne(v, 0.0f) & 0xFFFFu);
+      else
+        reinterpret_cast<float*>(g.c)[(int64_t)(m0 + r) * g.N + n] = v;
+    }
   }
 }
 
@@ -502,50 +491,47 @@ int64_t tiles(const Int8Args& g, int tm, int tn) {
   return (int64_t)((g.M + tm - 1) / tm) * ((g.N + tn - 1) / tn);
 }
 
-// What a ring of tm x tn tiles costs: the bytes per byte of K that the busiest of 256
-// CUs moves into LDS.
-int64_t ring_cost(const Int8Args& g, int tm, int tn) { return (tiles(g, tm, tn) + 255) / 256 * (tm + tn); }
+// The rings, smaller tiles first.
+struct RingTile {
+  int tm, tn;
+  hipError_t (*launch)(const Int8Args&, bool, hipStream_t);
+};
+constexpr RingTile kRings[] = {
+    {16, 16, launch_ring<16, 16, 512, 1, 1, 2>},   {16, 32, launch_ring<16, 32, 512, 1, 2, 2>},
+    {32, 16, launch_ring<32, 16, 512, 1, 1, 2>},   {32, 32, launch_ring<32, 32, 256, 1, 2, 2>},
+    {32, 64, launch_ring<32, 64, 256, 1, 4, 2>},   {64, 32, launch_ring<64, 32, 256, 2, 1, 2>},
+    {64, 64, launch_ring<64, 64, 128, 2, 2, 2>},   {64, 128, launch_ring<64, 128, 128, 1, 4, 2>},
+    {128, 64, launch_ring<128, 64, 128, 2, 2, 2>}};
 
 }  // namespace
 
-// Up to 128 rows of A: the ring whose busiest CU moves the least, all rows in one tile,
-// the wider tile where two are equal.  (Measured at K = 4096, us: 16 rows over 14336
-// channels 13.9 / 11.2 / 11.3 for tiles 16 x 16, 16 x 32, 32 x 64; 64 rows 28 / 13.9 / 12.7 /
-// 17.4 for 16, 32, 64, 128 columns, over 4096 channels 8.9 / 8.2 / 10.3 / 16.0; 128 rows over
-// 4096 11.0 / 14.7 / 25 for 32, 64, 128 columns, over 28672 54 / 37.6 / 35.5.)
-// More rows: what rings of 128 x 64, tiles of 128 x 128 (two a CU) and tiles of 256 x 256 are
-// estimated to take.  (Measured, us: 512 rows over 4096 channels of 4096 16 / 26 / 44, 1024
-// rows 27 / 26 / 44, 2048 rows 60 / 40 / 47, 4096 rows 151 / 83 / 65, 512 rows over 4096
-// channels of 14336 43 / 76 / 127, 8192 over 7168 of 2048 269 / 146 / 125.  The last, partial
-// round of 256 x 256 tiles cut into 128 x 128 ones in a second launch gained nothing: 124, and
-// 125 against 113 for 2048 over 14336 of 4096.)
+// The ring whose busiest of 256 CUs moves the fewest bytes into LDS for each byte of K, the
+// larger tile where two are equal; or tiles of 128 x 128 (two a CU) or 256 x 256, if they are
+// estimated to take less.  Measured, us:
+//   K = 4096, tiles        16 x 16  16 x 32  32 x 16  32 x 32  32 x 64  64 x 32  64 x 64  128 x 64
+//   16 over 14336             13.9     11.2               -      11.3                -         -
+//   64 over 2048               6.8      5.3      5.8      5.9      7.0      6.7      9.7      12.4
+//   64 over 4096              12.4      8.3      8.8      6.9      8.0      8.2     10.1      13.2
+//   33 over 14336             29.2     19.6     23.7     17.5     12.8     12.5     12.1      13.7
+//   128 over 4096             22.2     13.9     14.3      9.7      8.3      8.3     10.1      14.4
+//   256 over 4096             40.4     27.3     26.3     16.9     12.2     12.3     10.8      14.7
+//   rings of 128 x 64, 128 x 128, 256 x 256: 512 rows over 4096 16 / 26 / 44, 1024 rows 27 / 26 / 44,
+//   2048 rows 60 / 40 / 47, 4096 rows 151 / 83 / 65; 8192 over 7168 of 2048 269 / 146 / 122
+// (The last, partial round of 256 x 256 tiles cut into 128 x 128 ones in a second launch gained
+// nothing, nor did parts of K summed by a second launch: 512 over 4096 of 14336 43 us as a
+// ring, 45 in four parts.)
 hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st) {
-  if (g.M <= 16) {
-    const int64_t c16 = ring_cost(g, 16, 16), c32 = ring_cost(g, 16, 32), c64 = ring_cost(g, 32, 64);
-    if (c64 <= c16 && c64 <= c32) return launch_ring<32, 64, 256, 1, 4, 2>(g, out_bf16, st);
-    if (c32 <= c16) return launch_ring<16, 32, 512, 1, 2, 2>(g, out_bf16, st);
-    return launch_ring<16, 16, 512, 1, 1, 2>(g, out_bf16, st);
+  const RingTile* ring = kRings;
+  int64_t least = INT64_MAX;
+  for (const RingTile& r : kRings) {
+    const int64_t n = tiles(g, r.tm, r.tn), cost = (n + 255) / 256 * (r.tm + r.tn);
+    if (n < 1 << 22 && cost <= least)   // (a grid has less than 2^32 threads) least = cost, ring = &r;
   }
-  if (g.M <= 32) {
-    const int64_t c16 = ring_cost(g, 32, 16), c32 = ring_cost(g, 32, 32), c64 = ring_cost(g, 32, 64);
-    if (c64 <= c16 && c64 <= c32) return launch_ring<32, 64, 256, 1, 4, 2>(g, out_bf16, st);
-    if (c32 <= c16) return launch_ring<32, 32, 256, 1, 2, 2>(g, out_bf16, st);
-    return launch_ring<32, 16, 512, 1, 1, 2>(g, out_bf16, st);
-  }
-  if (g.M <= 64) {
-    const int64_t c16 = ring_cost(g, 64, 16), c32 = ring_cost(g, 64, 32), c64 = ring_cost(g, 64, 64),
-                  c128 = ring_cost(g, 64, 128);
-    if (c128 <= c16 && c128 <= c32 && c128 <= c64) return launch_ring<64, 128, 128, 1, 4, 2>(g, out_bf16, st);
-    if (c64 <= c16 && c64 <= c32) return launch_ring<64, 64, 128, 2, 2, 2>(g, out_bf16, st);
-    if (c32 <= c16) return launch_ring<64, 32, 256, 2, 1, 2>(g, out_bf16, st);
-    return launch_ring<64, 16, 512, 1, 1, 1>(g, out_bf16, st);
-  }
-  if (ring_cost(g, 128, 32) <= ring_cost(g, 128, 64)) return launch_ring<128, 32, 256, 2, 1, 1>(g, out_bf16, st);
   const double k = g.K / 4096.0;
-  const int64_t rings = (tiles(g, 128, 64) + 255) / 256, small = tiles(g, 128, 128), large = (tiles(g, 256, 256) + 255) / 256;
-  const double by_ring = 3 + 12 * k + (1 + 11 * k) * (rings - 1), by_large = 8 + (54 * k + 3) * large;
+  const int64_t small = tiles(g, 128, 128), large = (tiles(g, 256, 256) + 255) / 256;
+  const double by_ring = 3 + 12 * k * ((double)least / 192), by_large = 8 + (54 * k + 3) * large;
   const double by_small = 4 + 36 * k * (small / 512) + (small % 512 > 256 ? 36 * k : small % 512 ? 22 * k : 0);
-  if (by_ring <= by_small && by_ring <= by_large) return launch_ring<128, 64, 128, 2, 2, 2>(g, out_bf16, st);
+  if (by_ring <= by_small && by_ring <= by_large) return ring->launch(g, out_bf16, st);
   if (by_small <= by_large) return launch_tile<128, 128, 2, 2>(g, out_bf16, small, st);
   return launch_tile<256, 256, 2, 4>(g, out_bf16, 256, st);
 }

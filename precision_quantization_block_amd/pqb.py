@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -138,9 +139,9 @@ def lib():
         L.pqb_gemm_w4a16_batch.argtypes = [ctypes.POINTER(_W4Job), I64, I64, I, P]
         MAT = ctypes.POINTER(_Int8Mat)
         L.pqb_gemm_int8.argtypes = [MAT, MAT, I64, P, I, P, P]
-        L.pqb_norm_quant.argtypes = [ctypes.POINTER(_Norm), P]
+        L.pqb_norm_quant.argtypes = [P, P]
         L.pqb_act_quant.argtypes = [P, P, I, I64, I64, I64, I64, I, I, I, P, P, P]
-        L.pqb_rope.argtypes = [ctypes.POINTER(_Rope), P]
+        L.pqb_rope.argtypes = [P, P]
         L.pqb_encode_e4m3.argtypes = [P, I64, P, P]
         L.pqb_encode_e5m2.argtypes = [P, I64, P, P]
         L.pqb_encode_e2m1.argtypes = [P, I64, P, P]
@@ -726,6 +727,10 @@ def kv_attend_paged(q: torch.Tensor, cache: PagedKV, block_table: torch.Tensor,
 # the INT8 layer: its product, and what lies between a layer's products
 # --------------------------------------------------------------------------
 
+# The argument structs as bytes (their fields in order): packing one takes 0.6 us, a ctypes structure 1.5
+_NORM_BYTES, _ROPE_BYTES = struct.Struct("9Q7q2f5i4x"), struct.Struct("4Q9q3QqQf3i")
+assert _NORM_BYTES.size == ctypes.sizeof(_Norm) and _ROPE_BYTES.size == ctypes.sizeof(_Rope)
+
 NORM_KINDS = {"rms": 0, "layer": 1}
 ACT_KINDS = {"silu": 0, "gelu_tanh": 1, "gelu_erf": 2, "relu2": 3}
 _I8 = torch.int8
@@ -832,11 +837,13 @@ def _rows_share(t, stride, other, other_stride) -> bool:
 def _layer_rows(t, name, dev, dtype, cols, block):
     """t [..., cols] as rows a stride apart (copied if they are not, or where 1x128 blocks
     need 16-byte alignment and have none): the tensor, its rows and their stride."""
-    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype is not dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev:
         _refuse(dev, (dtype,), name, t, contiguous=False)
-    if t.dim() != 2:
-        t = t.reshape(-1, t.shape[-1]) if t.dim() else t.reshape(1, 1)
-    rows, c = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        t = t.reshape(-1, shape[-1]) if shape else t.reshape(1, 1)
+        shape = t.shape
+    rows, c = shape
     if c != cols:
         raise ValueError(f"{name} must have {cols} columns, got {c}")
     stride, one = t.stride()
@@ -847,8 +854,16 @@ def _layer_rows(t, name, dev, dtype, cols, block):
     return t, rows, stride
 
 
+def _packed(layout, *fields):
+    """The fields as a struct's bytes; numbers that are none, or pass their type, are refused."""
+    try:
+        return layout.pack(*fields)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"an argument is no number of its type: {e}") from None
+
+
 def _at(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _layer_out(fmt, gran, rows, cols, like):
@@ -886,25 +901,28 @@ def norm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, fmt: str | N
     res, g, h = None, None, None
     res_stride = gate_rows = gate_stride = h_stride = 0
     if residual is not None:
-        res, n, res_stride = _layer_rows(residual, "residual", dev, dtype, cols, block)
-        if n != rows:
-            raise ValueError("residual must have x's shape")
+        if not block and _ready(dev, dtype, residual) and residual.shape == shape:
+            res, res_stride = residual, cols
+        else:
+            res, n, res_stride = _layer_rows(residual, "residual", dev, dtype, cols, block)
+            if n != rows:
+                raise ValueError("residual must have x's shape")
     if gate is not None:
         g, gate_rows, gate_stride = _layer_rows(gate, "gate", dev, dtype, cols, block)
         if gate_rows < 1 or rows % gate_rows:
             raise ValueError("gate must have a number of rows that divides x's")
     weights = (post_weight, weight, bias)
-    for name, w in zip(("post_weight", "weight", "bias"), weights):
-        if w is not None:
-            if not _ready(dev, dtype, w):
-                _refuse(dev, (dtype,), name, w)
-            if w.numel() != cols:
-                raise ValueError(f"{name} must have {cols} values")
+    for w in weights:
+        if w is not None and not (_ready(dev, dtype, w) and w.numel() == cols):
+            name = "post_weight" if w is post_weight else "weight" if w is weight else "bias"
+            _refuse(dev, (dtype,), name, w)
+            raise ValueError(f"{name} must have {cols} values")
     if block:
-        weights = tuple(w if w is None or not w.data_ptr() & 15 else w.clone() for w in weights)
+        weights = post_weight, weight, bias = tuple(w if w is None or not w.data_ptr() & 15 else w.clone()
+                                                    for w in weights)
     if residual is not None or gate is not None or post_weight is not None:
         if h_out is None:
-            h, h_stride = x.new_empty(shape), cols
+            h, h_stride = torch.empty_like(x) if x2 is x and x_stride == cols else x.new_empty(shape), cols
         else:
             h = h_out
             h2, n, h_stride = _layer_rows(h, "h_out", dev, dtype, cols, block)
@@ -923,11 +941,10 @@ def norm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, fmt: str | N
     if bias is not None and kind != "layer":
         raise ValueError("a bias goes with a layer norm")
     f, gr, result, codes, scales = _layer_out(fmt, gran, rows, cols, x)
-    # (one constructor call: setting a struct's fields one by one took 2 of the 12 us of a small call)
-    a = _Norm(x2.data_ptr(), _at(res), _at(g), *map(_at, weights), _at(h), codes.data_ptr(), _at(scales), rows, cols,
-              gate_rows, x_stride, res_stride, gate_stride, h_stride, residual_scale, eps,
-              BF16 if dtype is _BF16 else F32, NORM_KINDS[kind], f, gr, 0)
-    status = _call_on(dev, lib().pqb_norm_quant, ctypes.byref(a))
+    a = _packed(_NORM_BYTES, x2.data_ptr(), _at(res), _at(g), _at(post_weight), _at(weight), _at(bias), _at(h),
+                codes.data_ptr(), _at(scales), rows, cols, gate_rows, x_stride, res_stride, gate_stride, h_stride,
+                residual_scale, eps, BF16 if dtype is _BF16 else F32, NORM_KINDS[kind], f, gr, 0)
+    status = _call_on(dev, lib().pqb_norm_quant, a)
     if status:
         raise PqbError(status, "norm_quant")
     return result, h
@@ -1094,10 +1111,10 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions, table: RopeTable, *
             raise ValueError("positions must hold a value per token")
     if not T:
         return q_out, k_out
-    a = _Rope(q2.data_ptr(), _at(k2), q_out.data_ptr(), _at(k_out), T, H, Hk, D, 2 * angles.numel(), q_stride, k_stride,
-              qo_stride, ko_stride, _at(positions), _at(starts), _at(lens), batch, angles.data_ptr(), table.amplitude,
-              bool(table.interleaved), BF16 if dtype is _BF16 else F32, 0)
-    status = _call_on(dev, lib().pqb_rope, ctypes.byref(a))
+    a = _packed(_ROPE_BYTES, q2.data_ptr(), _at(k2), q_out.data_ptr(), _at(k_out), T, H, Hk, D, 2 * angles.numel(),
+                q_stride, k_stride, qo_stride, ko_stride, _at(positions), _at(starts), _at(lens), batch,
+                angles.data_ptr(), table.amplitude, bool(table.interleaved), BF16 if dtype is _BF16 else F32, 0)
+    status = _call_on(dev, lib().pqb_rope, a)
     if status:
         raise PqbError(status, "rope")
     return q_out, k_out

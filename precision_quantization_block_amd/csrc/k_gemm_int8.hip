@@ -525,7 +525,7 @@ hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st) {
   int64_t least = INT64_MAX;
   for (const RingTile& r : kRings) {
     const int64_t n = tiles(g, r.tm, r.tn), cost = (n + 255) / 256 * (r.tm + r.tn);
-    if (n < 1 << 22 && cost <= least)   // (a grid has less than 2^32 threads) least = cost, ring = &r;
+    if (n < 1 << 22 && cost <= least) least = cost, ring = &r;   // (a grid has less than 2^32 threads)
   }
   const double k = g.K / 4096.0;
   const int64_t small = tiles(g, 128, 128), large = (tiles(g, 256, 256) + 255) / 256;

@@ -702,8 +702,8 @@ pqb_status pqb_act_quant(const void* gate, const void* up, pqb_dtype dtype, int6
  * q only.
  * Shape rules: tokens < 2^24; heads in [1, 8192] (k_heads 0 with k NULL); dim in [2, 1024];
  * rot even, in [2, min(dim, 512)]; strides in [heads * dim, 2^40).  Addresses need
- * element alignment; rot / 2 (rot if interleaved), dim and strides that are multiples of 8 on
- * 16-byte aligned arrays are the fast form.  angles 8-byte aligned, amplitude finite (else
+ * element alignment; the more low zeros rot / 2 (rot if interleaved), dim, strides and addresses have, the wider the
+ * accesses, up to 16 bytes.  angles 8-byte aligned, amplitude finite (else
  * PQB_ERR_VALUE).  Errors, before any launch: PQB_ERR_ENUM, PQB_ERR_SHAPE, PQB_ERR_VALUE,
  * PQB_ERR_NULL, PQB_ERR_ALIGN. */
 typedef struct pqb_rope_args {

@@ -1145,15 +1145,22 @@ pqb_status pqb_rope(const pqb_rope_args* r, void* stream) {
   if (!r->positions && r->batch == 0) return PQB_OK;  // no request owns a token
   if (!r->positions && (!r->q_starts || !r->kv_lens)) return PQB_ERR_NULL;
   const int64_t es = r->dtype == PQB_BF16 ? 2 : 4;
-  bool vec = dim % 8 == 0 && (r->interleaved ? rot : rot / 2) % 8 == 0;
   bool ok = aligned(r->angles, 8) && aligned(r->positions, 4) && aligned(r->q_starts, 4) && aligned(r->kv_lens, 4);
-  layer_array(r->q, r->q_stride, es, &vec, &ok);
-  layer_array(r->q_out, r->q_out_stride, es, &vec, &ok);
+  uint64_t all = (uint64_t)dim;   // its low zeros: the elements that every head's start is a multiple of
+  auto array = [&](const void* p, int64_t stride) {
+    if (!aligned(p, (uintptr_t)es)) ok = false;
+    all |= (uint64_t)stride | (uintptr_t)p / es;
+  };
+  array(r->q, r->q_stride);
+  array(r->q_out, r->q_out_stride);
   if (r->k_heads) {
-    layer_array(r->k, r->k_stride, es, &vec, &ok);
-    layer_array(r->k_out, r->k_out_stride, es, &vec, &ok);
+    array(r->k, r->k_stride);
+    array(r->k_out, r->k_out_stride);
   }
   if (!ok) return PQB_ERR_ALIGN;
+  const uint64_t most = 16 / es, turned = (uint64_t)(r->interleaved ? rot : rot / 2);
+  int unit = (int)most;
+  while (unit > 1 && (all | turned) & (uint64_t)(unit - 1)) unit /= 2;
   RopeArgs a{};
   a.x[0] = r->q;
   a.x[1] = r->k;
@@ -1175,7 +1182,7 @@ pqb_status pqb_rope(const pqb_rope_args* r, void* stream) {
   a.batch = r->batch;
   a.angles = r->angles;
   a.amplitude = r->amplitude;
-  return hip_status(launch_rope(a, r->dtype == PQB_BF16, vec, (hipStream_t)stream));
+  return hip_status(launch_rope(a, r->dtype == PQB_BF16, unit, !(all & (most - 1)), (hipStream_t)stream));
 }
 
 pqb_status pqb_encode_e4m3(const float* y, int64_t n, uint8_t* out, void* stream) {

@@ -55,39 +55,65 @@ __device__ __forceinline__ bool position_of(const RopeArgs& a, int64_t t, int& p
   return true;
 }
 
-// kV values: 16 bytes (8 of bf16, 4 of float32), or fewer one by one.
-template <int kV>
-__device__ __forceinline__ void load_v(const uint16_t* p, float (&v)[kV]) {
-  if constexpr (kV == 8) widen8(load_raw8(p), p, v);
-  else for (int j = 0; j < kV; ++j) v[j] = ld1(p + j);
-}
-template <int kV>
-__device__ __forceinline__ void load_v(const float* p, float (&v)[kV]) {
-  if constexpr (kV == 4) {
-    const uint4 w = ld_nt16(p);
-    v[0] = as_f(w.x), v[1] = as_f(w.y), v[2] = as_f(w.z), v[3] = as_f(w.w);
+// kV consecutive values by one access of up to 16 bytes, aligned to its size; kOnce: with
+// non-temporal hints, for heads that are whole 16-byte parts (where narrow parts share
+// lines with others, the hints write lines twice: 20 of 128 turned, bf16, 69 us with them, 49
+// without).
+template <int kBytes>
+struct Words {
+  typedef uint32_t type __attribute__((ext_vector_type(kBytes / 4)));
+};
+template <>
+struct Words<4> {
+  typedef uint32_t type;
+};
+template <>
+struct Words<2> {
+  typedef uint16_t type;
+};
+
+template <bool kOnce, int kV, typename T>
+__device__ __forceinline__ void load_v(const T* p, float (&v)[kV]) {
+  using words = typename Words<kV * sizeof(T)>::type;
+  if constexpr (kV == 1) {
+    v[0] = ld1(p);
   } else {
-    for (int j = 0; j < kV; ++j) v[j] = ld1(p + j);
+    const words* q = reinterpret_cast<const words*>(p);
+    const words w = kOnce ? __builtin_nontemporal_load(q) : *q;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      if constexpr (kV * sizeof(T) == 4) v[j] = as_f(j ? w & 0xFFFF0000u : w << 16);
+      else if constexpr (sizeof(T) == 2) v[j] = as_f(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+      else v[j] = as_f(w[j]);
+    }
   }
 }
-template <int kV>
-__device__ __forceinline__ void store_v(uint16_t* p, const float (&v)[kV]) {
-  if constexpr (kV == 8)
-    st_nt16(p, bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-  else
-    for (int j = 0; j < kV; ++j) p[j] = (uint16_t)(bf16x2_rne(v[j], 0.0f) & 0xFFFFu);
-}
-template <int kV>
-__device__ __forceinline__ void store_v(float* p, const float (&v)[kV]) {
-  if constexpr (kV == 4) st_nt16(p, as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
-  else for (int j = 0; j < kV; ++j) p[j] = v[j];
+template <bool kOnce, int kV, typename T>
+__device__ __forceinline__ void store_v(T* p, const float (&v)[kV]) {
+  using words = typename Words<kV * sizeof(T)>::type;
+  if constexpr (kV == 1) {
+    if constexpr (sizeof(T) == 2) *p = (uint16_t)(bf16x2_rne(v[0], 0.0f) & 0xFFFFu);
+    else *p = v[0];
+  } else {
+    words w;
+    if constexpr (kV * sizeof(T) == 4) w = bf16x2_rne(v[0], v[1]);
+    else
+#pragma unroll
+      for (int j = 0; j < (int)(kV * sizeof(T) / 4); ++j) {
+        if constexpr (sizeof(T) == 2) w[j] = bf16x2_rne(v[2 * j], v[2 * j + 1]);
+        else w[j] = as_u(v[j]);
+      }
+    words* q = reinterpret_cast<words*>(p);
+    if (kOnce) __builtin_nontemporal_store(w, q);
+    else *q = w;
+  }
 }
 
-// Parts of a head, one a thread: kV values of each half, kV / 2 pairs of an interleaved head, or
-// kV values behind `rot`.  kV is 16 bytes' worth, or 1 (2 if interleaved) for any even
-// dim, stride and address.
+// Parts of a head, one a thread: kV values of each half or kV / 2 pairs of an interleaved
+// head; behind `rot`, which are copied, kV values up to `wide` and 16 bytes from there on.  kV
+// is the most that rot, dim, strides and addresses allow.
 template <typename T, int kV, bool kInterleaved>
-__global__ __launch_bounds__(kThreads) void k_rope(RopeArgs a, int tokens) {
+__global__ __launch_bounds__(kThreads) void k_rope(RopeArgs a, int tokens, int wide) {
   __shared__ float2 cs[kTokens * kRopeMaxRot / 2];
   __shared__ int owned[kTokens];
   const int64_t t0 = (int64_t)blockIdx.x * tokens;
@@ -102,69 +128,103 @@ __global__ __launch_bounds__(kThreads) void k_rope(RopeArgs a, int tokens) {
   }
   __syncthreads();
 
-  const int turned = kInterleaved ? a.rot / kV : half / kV;
-  const int parts = turned + (a.dim - a.rot) / kV, heads = a.heads[0] + a.heads[1];
-  for (int i = threadIdx.x; i < nt * heads * parts; i += kThreads) {
-    const int th = i / parts, p = i - th * parts, t = th / heads;
-    int h = th - t * heads;
-    if (!owned[t]) continue;
-    const int which = h >= a.heads[0];
-    h -= which ? a.heads[0] : 0;
-    const T* x = reinterpret_cast<const T*>(a.x[which]) + (t0 + t) * a.stride[which] + (int64_t)h * a.dim;
-    T* out = reinterpret_cast<T*>(a.out[which]) + (t0 + t) * a.out_stride[which] + (int64_t)h * a.dim;
-    float u[kV], v[kV];
-    if (p >= turned) {
-      const int e = a.rot + (p - turned) * kV;
-      load_v<kV>(x + e, u);
-      store_v<kV>(out + e, u);
-    } else if constexpr (kInterleaved) {
-      load_v<kV>(x + p * kV, u);
-#pragma unroll
-      for (int j = 0; j < kV; j += 2) {
-        const float2 w = cs[t * half + (p * kV + j) / 2];
-        v[j] = __builtin_fmaf(u[j], w.x, -(u[j + 1] * w.y));
-        v[j + 1] = __builtin_fmaf(u[j + 1], w.x, u[j] * w.y);
+  // f(x, out, part, the token's cosines and sines) for each of `parts` parts of every head: the
+  // parts of a kind together, so that a wave's threads do the same, and their places by
+  // steps, not by a division each.
+  const int heads = a.heads[0] + a.heads[1];
+  auto each = [&](int parts, auto f) {
+    if (parts == 0) return;
+    int h = (int)threadIdx.x / parts, p = (int)threadIdx.x - h * parts, t = 0;
+    const int step_h = kThreads / parts, step_p = kThreads - step_h * parts;
+    for (;;) {
+      while (h >= heads) h -= heads, ++t;
+      if (t >= nt) return;
+      if (owned[t]) {
+        const int which = h >= a.heads[0], head = h - (which ? a.heads[0] : 0);
+        f(reinterpret_cast<const T*>(a.x[which]) + (t0 + t) * a.stride[which] + (int64_t)head * a.dim,
+          reinterpret_cast<T*>(a.out[which]) + (t0 + t) * a.out_stride[which] + (int64_t)head * a.dim, p, cs + t * half);
       }
-      store_v<kV>(out + p * kV, v);
+      h += step_h;
+      p += step_p;
+      if (p >= parts) p -= parts, ++h;
+    }
+  };
+  constexpr int kPairs = kInterleaved ? (kV > 1 ? kV / 2 : 1) : kV;   // of a turned part
+  constexpr int kWide = 16 / sizeof(T);
+  constexpr bool kOnce = kV == kWide;
+  each(half / kPairs, [&](const T* x, T* out, int p, const float2* c) {
+    c += kPairs * p;
+    if constexpr (kInterleaved) {
+      float y[2 * kPairs];
+      x += 2 * kPairs * p;
+      out += 2 * kPairs * p;
+      if constexpr (kV > 1) load_v<kOnce, kV>(x, y);
+      else y[0] = ld1(x), y[1] = ld1(x + 1);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const float x0 = y[2 * j], x1 = y[2 * j + 1];
+        y[2 * j] = __builtin_fmaf(x0, c[j].x, -(x1 * c[j].y));
+        y[2 * j + 1] = __builtin_fmaf(x1, c[j].x, x0 * c[j].y);
+      }
+      if constexpr (kV > 1) {
+        store_v<kOnce, kV>(out, y);
+      } else {
+        store_v<kOnce, 1>(out, {y[0]});
+        store_v<kOnce, 1>(out + 1, {y[1]});
+      }
     } else {
-      load_v<kV>(x + p * kV, u);
-      load_v<kV>(x + half + p * kV, v);
+      float u[kV], v[kV];
+      load_v<kOnce, kV>(x + p * kV, u);
+      load_v<kOnce, kV>(x + half + p * kV, v);
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        const float2 w = cs[t * half + p * kV + j];
         const float x0 = u[j], x1 = v[j];
-        u[j] = __builtin_fmaf(x0, w.x, -(x1 * w.y));
-        v[j] = __builtin_fmaf(x1, w.x, x0 * w.y);
+        u[j] = __builtin_fmaf(x0, c[j].x, -(x1 * c[j].y));
+        v[j] = __builtin_fmaf(x1, c[j].x, x0 * c[j].y);
       }
-      store_v<kV>(out + p * kV, u);
-      store_v<kV>(out + half + p * kV, v);
+      store_v<kOnce, kV>(out + p * kV, u);
+      store_v<kOnce, kV>(out + half + p * kV, v);
     }
-  }
+  });
+  each((wide - a.rot) / kV, [&](const T* x, T* out, int p, const float2*) {
+    float u[kV];
+    load_v<kOnce, kV>(x + a.rot + p * kV, u);
+    store_v<kOnce, kV>(out + a.rot + p * kV, u);
+  });
+  each((a.dim - wide) / kWide, [&](const T* x, T* out, int p, const float2*) {
+    float u[kWide];
+    load_v<kOnce, kWide>(x + wide + p * kWide, u);
+    store_v<kOnce, kWide>(out + wide + p * kWide, u);
+  });
 }
 
-template <typename T>
-void launch(const RopeArgs& a, bool vec, hipStream_t st) {
-  constexpr int kV = 16 / sizeof(T);
+template <typename T, int kV>
+void launch(const RopeArgs& a, int wide, hipStream_t st) {
   // As many tokens as give each thread a part (8192 tokens of 32 + 8 heads of 128, bf16: 29.0,
   // 30.6 and 31.7 us with 1, 2 and 4; of 8 + 1 heads of 64: 8.6, 7.0 and 6.1)
-  const int64_t parts = (int64_t)(a.heads[0] + a.heads[1]) * ((a.interleaved ? a.rot : a.rot / 2) + a.dim - a.rot) /
-                        (vec ? kV : a.interleaved ? 2 : 1);
+  const int pairs = a.interleaved && kV > 1 ? kV / 2 : kV;
+  const int64_t parts = (int64_t)(a.heads[0] + a.heads[1]) *
+                        (a.rot / 2 / pairs + (wide - a.rot) / kV + (a.dim - wide) * (int)sizeof(T) / 16);
   const int tokens = parts >= kThreads ? 1 : parts >= kThreads / 2 ? 2 : kTokens;
   const uint32_t grid = (uint32_t)((a.tokens + tokens - 1) / tokens);
-  if (a.interleaved) {
-    if (vec) k_rope<T, kV, true><<<grid, kThreads, 0, st>>>(a, tokens);
-    else k_rope<T, 2, true><<<grid, kThreads, 0, st>>>(a, tokens);
-  } else {
-    if (vec) k_rope<T, kV, false><<<grid, kThreads, 0, st>>>(a, tokens);
-    else k_rope<T, 1, false><<<grid, kThreads, 0, st>>>(a, tokens);
-  }
+  if (a.interleaved) k_rope<T, kV, true><<<grid, kThreads, 0, st>>>(a, tokens, wide);
+  else k_rope<T, kV, false><<<grid, kThreads, 0, st>>>(a, tokens, wide);
 }
 
 }  // namespace
 
-hipError_t launch_rope(const RopeArgs& a, bool bf16, bool vec, hipStream_t st) {
-  if (bf16) launch<uint16_t>(a, vec, st);
-  else launch<float>(a, vec, st);
+hipError_t launch_rope(const RopeArgs& a, bool bf16, int unit, bool aligned, hipStream_t st) {
+  const int most = bf16 ? 8 : 4, wide = aligned ? (a.rot + most - 1) / most * most : a.dim;
+  if (bf16) {
+    if (unit >= 8) launch<uint16_t, 8>(a, wide, st);
+    else if (unit == 4) launch<uint16_t, 4>(a, wide, st);
+    else if (unit == 2) launch<uint16_t, 2>(a, wide, st);
+    else launch<uint16_t, 1>(a, wide, st);
+  } else {
+    if (unit >= 4) launch<float, 4>(a, wide, st);
+    else if (unit == 2) launch<float, 2>(a, wide, st);
+    else launch<float, 1>(a, wide, st);
+  }
   return hipGetLastError();
 }
 

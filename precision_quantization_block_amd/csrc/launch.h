@@ -281,7 +281,8 @@ struct RopeArgs {
   const double* angles;                                     // [rot / 2] radians per token
   float amplitude;
 };
-hipError_t launch_rope(const RopeArgs& a, bool bf16, bool vec, hipStream_t st);
+// unit: values of one access in the turned part, 1 to 8; aligned: heads start at multiples of 16 bytes.
+hipError_t launch_rope(const RopeArgs& a, bool bf16, int unit, bool aligned, hipStream_t st);
 
 // ---- INT8 product (k_gemm_int8.hip) -------------------------------------------
 struct Int8Args {

@@ -538,7 +538,7 @@ def check_rope(tokens, hq, hk, dim, rot, dtype, interleaved, seed=0, far=100000,
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dim,rot", [(128, 128), (64, 64), (256, 64), (80, 32), (96, 96), (128, 16), (80, 20), (6, 2), (30, 22),
-                                     (1024, 512)])
+                                     (1024, 512), (128, 20), (96, 24), (80, 40), (77, 30), (3, 2), (129, 128), (100, 100)])
 @pytest.mark.parametrize("tokens,hq,hk", [(1, 32, 8), (5, 3, 1), (67, 4, 4), (9, 2, 0)])
 def test_rope(tokens, hq, hk, dim, rot, interleaved, dtype):
     check_rope(tokens, hq, hk, dim, rot, dtype, interleaved, seed=dim + tokens)

@@ -100,7 +100,7 @@ def test_gemm_large(m, n, k):
 @pytest.mark.parametrize("k", [16, 144, 400, 1040, 2512])
 @pytest.mark.parametrize("m,n", [(9, 300), (50, 1005), (10, 4201), (99, 1075), (38, 1418), (367, 180), (20, 4100), (134, 1616), (13, 14400),
                                  (22, 34746), (41, 4100), (302, 1309), (60, 8200), (378, 2048), (64, 16401), (136, 26739), (111, 8201),
-                                 (500, 4090), (244, 81468), (1300, 7001), (2100, 6001), (2500, 5000)])
+                                 (500, 4090), (1000, 4090), (244, 81468), (1300, 7001), (2100, 6001), (2500, 5000)])
 def test_gemm_every_tile(m, n, k):
     """Each tile that the launcher takes, twice or more (16 x 16, 16 x 32, 32 x 16, 32 x 32, 32 x 64, 64 x 32, 64 x 64, 64 x 128,
     128 x 64, 128 x 128, 256 x 256), with K ending in every part of a block."""

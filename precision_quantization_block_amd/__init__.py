@@ -7,7 +7,9 @@ KV-cache write (per layer, per head or static scale) and the KIVI-style
 scale per page and head) with its page planning, appends and attention, plus
 the block-scaled FP8 GEMM that consumes 1x128 / 128x128 codes on the matrix cores, the MXFP4
 product, and the W4A16 product on INT4 codes (decode rows on the vector
-units, any number of rows on the matrix cores), as HIP kernels behind
+units, any number of rows on the matrix cores), the INT8 product with a scale
+per token and channel, and what lies between a layer's products (norms with
+residual and gate, gated activations, rotary positions), as HIP kernels behind
 the C ABI in include/pqb.h.  The binding is loaded on first use so that the input
 generators in `synth` import without the engine.
 """

@@ -4,18 +4,22 @@
 //
 //   C[m, n] = ((float(S) * sA[m]) * sB[n]) + bias[n],   S = sum_k a[m, k] b[n, k],
 //
-// S exact in int32 (K <= 131071 keeps |S| <= 2^14 K below 2^31), so neither the
-// order of the sum nor a split of K changes a bit of C.
+// S exact in int32 (K <= 131056 keeps |S| <= 2^14 K below 2^31), so neither the
+// order of the sum nor how K is shared out changes a bit of C.
 //
-// A workgroup owns a kTM x kTN tile; both operands' kBK = 128 bytes of K go straight
-// from global memory into LDS (buffer_load_dwordx4 ... lds) in a ring of two slots,
-// the next block's while this one is multiplied.  A row is 8 chunks of 16 bytes, chunk c
-// of row r at position c ^ (r & 7): the 8 lanes that read one chunk of 8 rows touch 8
-// different groups of banks.  A lane whose row or chunk lies outside the matrix
-// gives the load an offset past the buffer's end, which reads as zeros.
-// v_mfma_i32_32x32x32_i8 takes the weights as its first operand: lane l holds row l & 31
-// and the 16 bytes of chunk l >> 5; result register r is weight row
-// 8 (r / 4) + 4 (l >> 5) + r % 4 of activation row l & 31.
+// Both operands' blocks of K go straight from global memory into LDS
+// (buffer_load_dwordx4 ... lds, issued from inline assembly and waited for with explicit
+// counts: the compiler would wait for all of them before every LDS read).  A lane whose
+// row or chunk lies outside the matrix gives the load an offset past the buffer's end,
+// which reads as zeros.  Rows in LDS are chunks of 16 bytes, permuted by row so that the 16
+// lanes which read one chunk of 16 rows touch all 64 banks once.
+// v_mfma_i32_16x16x64_i8 takes the weights as its first operand: lane l holds row l & 15
+// and chunk l >> 4 of 64 bytes of K, and result register r is weight row 4 (l >> 4) + r of
+// activation row l & 15, so that a lane has four columns of one row of C.  (Its loop of random
+// operands runs at 3.8-4.1 POP/s here, the 32x32x32 product's at 3.4-3.5: power.)
+//
+// Two kernels: k_int8_ring where the matrices are read about once (decode steps, chunks),
+// k_int8_tile where they are read often.
 #include <algorithm>
 
 #include "launch.h"
@@ -25,7 +29,6 @@ namespace pqb {
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v16i __attribute__((ext_vector_type(16)));
 
 constexpr int kBK = 128;                  // bytes of K per block
 constexpr uint32_t kOutside = 0x80000000u;  // a buffer's size, and an offset past it
@@ -108,7 +111,7 @@ __device__ __forceinline__ v4f four_at(const float* p, int step, int n, int N) {
 
 template <int kTM, int kTN, int kWM, int kWN>
 struct Tile {
-  static constexpr int waves = kWM * kWN, threads = 64 * waves;
+  static constexpr int waves = kWM * kWN;
   static constexpr int mt = kTM / kWM / 16, nt = kTN / kWN / 16;     // 16 x 16 products of a wave
   static constexpr int slot = (kTM + kTN) * kBK;
   static constexpr int stage = 4096;                                 // bytes of a wave's staged results
@@ -118,9 +121,16 @@ struct Tile {
   static_assert(a_loads <= mt && b_loads <= mt, "one load of each operand per row of products at most");
 };
 
-// Many tiles.  Workgroups stay and take tiles in turn, and the blocks of all their tiles are
-// one stream: the first ones of the next tile are on their way, and its first fragments
-// in registers, while a tile's results are scaled and stored.
+// Many tiles.  A wave's products of one half of a 128-byte block run while its fragments of
+// the next are read and, behind the barrier, the next but one block is loaded: reads, loads and
+// products issue one between the other (left to the compiler, every read was waited for at
+// once: 8192^3 445 us, 435 so).  Chunk c of row r lies at c ^ (r / 2); at c ^ r the 16 rows met in
+// pairs, half of the LDS cycles.  Workgroups stay and take tiles in turn, and the blocks of
+// all their tiles are one stream: the first ones of the next tile are on their way, and its
+// first fragments in registers, while a tile's results are scaled and stored (8192 x 7168 x
+// 2048 142 to 122 us).  256 x 256 tiles, 8 waves of 128 x 64: 8192^3 in 410-425 us, 2.6 POP/s (the
+// vendor's 521); the same without its loads 354, without LDS reads too 314: what is left is
+// the operand stream and the clock that the power leaves (2.0 GHz).
 template <int kTM, int kTN, int kWM, int kWN, int kOut>
 __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int tiles_m, int tiles_n) {
   using S = Tile<kTM, kTN, kWM, kWN>;
@@ -323,8 +333,11 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int ti
 // that the workgroups fill the chip, and its 8 waves share them out: kWM x kWN over the
 // products, the rest over the blocks' K, whose sums meet in LDS at the end.  Blocks of kBK
 // bytes of K pass through a ring, kSlots - 1 blocks ahead: what memory latency asks to be
-// in flight.  A row of a block is kBK / 16 chunks, chunk c of row r at c ^ mix(r): the 16
-// rows that are read at once touch 16 different groups of banks.
+// in flight.  A row of a block is kBK / 16 chunks, chunk c of row r at c ^ mix(r).  (Straight
+// from global memory into registers, 64 rows over 14336 channels of 4096 took 23 us, 12.5 so:
+// a fragment's rows are 64-byte pieces, and each line was fetched twice.)  One row over 4096
+// channels of 14336 from HBM 12.7 us, 4.6 TB/s; 64 over 14336 of 4096 16 us from HBM, 12.5 from
+// the Infinity Cache (4.8 TB/s).
 // ---------------------------------------------------------------------------
 template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer>
 struct Ring {

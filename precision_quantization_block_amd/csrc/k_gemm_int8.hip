@@ -332,7 +332,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int ti
 // A workgroup owns kTM rows of A (zeros behind the last) and kTN rows of B, few enough
 // that the workgroups fill the chip, and its 8 waves share them out: kWM x kWN over the
 // products, the rest over the blocks' K, whose sums meet in LDS at the end.  Blocks of kBK
-// bytes of K pass through a ring, kSlots - 1 blocks ahead: what memory latency asks to be
+// bytes of K pass through a ring of as many slots as fit: what memory latency asks to be
 // in flight.  A row of a block is kBK / 16 chunks, chunk c of row r at c ^ mix(r).  (Straight
 // from global memory into registers, 64 rows over 14336 channels of 4096 took 23 us, 12.5 so:
 // a fragment's rows are 64-byte pieces, and each line was fetched twice.)  One row over 4096
@@ -550,7 +550,7 @@ hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st) {
   const int64_t small = tiles(g, 128, 128), large = (tiles(g, 256, 256) + 255) / 256;
   const double by_ring = 3 + 12 * k * ((double)least / 192), by_large = 8 + (54 * k + 3) * large;
   const double by_small = 4 + 36 * k * (small / 512) + (small % 512 > 256 ? 36 * k : small % 512 ? 22 * k : 0);
-  if (by_ring <= by_small && by_ring <= by_large) {
+  if (least != INT64_MAX && by_ring <= by_small && by_ring <= by_large) {   // (K = 0: all are 0)
     if (ring->tm == 128 && least == 192) return kDeepRing(g, out_bf16, st);   // one round
     return ring->launch(g, out_bf16, st);
   }

@@ -754,7 +754,7 @@ def _int8_mat(m, name, dev=None):
         stride, one = codes.stride()
         if rows < 2:
             stride = k
-        if (one != 1 and k > 1) or stride < k or stride & 15 or codes.data_ptr() & 15:
+        if (one != 1 and k > 1) or stride < k or stride & 15 or stride >> 23 or codes.data_ptr() & 15:
             codes, stride = codes.clone(memory_format=torch.contiguous_format), k
     if dev is None:
         dev = codes.device
@@ -774,7 +774,7 @@ def gemm_int8(a, b, out_dtype=torch.bfloat16, *, bias: torch.Tensor | None = Non
     scale of A's row and of B's row, plus bias float32 [N].  a and b: a Quantized from
     quantize(x, "int8_sym") (per row or per tensor), norm_quant or act_quant, or a (codes
     [rows, K] int8 or uint8, scales float32 [rows] or [1]) pair whose rows may lie apart (a
-    copy is made unless that is by multiples of 16 bytes).  K is a multiple of 16.  out may share
+    copy is made unless that is by multiples of 16 bytes, below 2^23).  K is a multiple of 16.  out may share
     no memory with the operands."""
     am, keep_a, dev, K = _int8_mat(a, "a")
     bm, keep_b, _, kb = _int8_mat(b, "b", dev)

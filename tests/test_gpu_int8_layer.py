@@ -150,6 +150,25 @@ def test_gemm_empty():
     assert torch.equal(pqb.gemm_int8((e, one), (e, one), BF), torch.zeros(3, 3, dtype=BF, device=DEV))
 
 
+def test_gemm_empty_sums_of_most_rows():
+    """2^29 rows of no codes, a column: more tiles than a grid of any ring holds."""
+    rows = 2 ** 29
+    a, b = torch.empty(rows, 0, dtype=I8, device=DEV), torch.empty(1, 0, dtype=I8, device=DEV)
+    one = torch.ones(1, device=DEV)
+    got = pqb.gemm_int8((a, one), (b, one), BF, bias=torch.full((1,), 3.0, device=DEV))
+    assert got.shape == (rows, 1) and (got == 3).all()
+
+
+def test_gemm_rows_far_apart():
+    """Rows 2^23 bytes apart, which the kernels' offsets do not reach, are copied."""
+    g = gen(6)
+    big = torch.zeros(40 * 2 ** 23, dtype=I8, device=DEV)
+    a = big.view(40, 2 ** 23)[:, :272]
+    a.copy_(codes(g, 40, 272))
+    b, sa, sb = codes(g, 50, 272), torch.rand(40, generator=g, device=DEV), torch.rand(50, generator=g, device=DEV)
+    assert torch.equal(pqb.gemm_int8((a, sa), (b, sb), F32), product(a, sa, b, sb, None, F32))
+
+
 def test_gemm_output_past_2_31():
     """65600 x 33000 results of 2 bytes; rows on both sides of element 2^31."""
     g = gen(2)

@@ -14,8 +14,8 @@
 //
 // A row stays in registers (kU units of 8 elements a thread) from its one read to its one
 // write; the row's sums and maxima meet by DPP, two shuffles and one LDS exchange.  A
-// workgroup has one row and as many waves as that takes, or four rows of up to 1024
-// elements, a wave each.  All of it is bound by HBM, and by latency where there are few rows:
+// workgroup has one row and as many waves as that takes, or several narrow ones (a wave or part
+// of one each).  All of it is bound by HBM, and by latency where there are few rows:
 // 8192 rows of 7168 (bf16, residual, E4M3 1x128) 70 us, 5.9 TB/s; 4096 rows of 14336 through
 // SwiGLU to E4M3 1x128 52 us, 5.6 TB/s; 64 rows of 4096 to INT8 3.2 us.
 #include "launch.h"
@@ -25,17 +25,16 @@ namespace pqb {
 namespace {
 
 // ---------------------------------------------------------------------------
-// A row in registers.  Thread t of n, kVec: unit k is elements 8 (k n + t) ..., by
-// 16-byte accesses.  Otherwise (odd widths, strides or addresses) element j of
-// unit k is (8 k + j) n + t, so that neighbours still share a line.
+// A row in registers: unit k of thread t of n is elements 8 (k n + t) ....  kVec: units are whole
+// and 16-byte aligned.  Otherwise (odd widths, strides or addresses) the same accesses at the
+// elements' own alignment, which this GPU's memory instructions allow; a row's last unit is
+// loaded with the elements in front of it, and stored one by one.  (One by one throughout, 8192
+// rows of 1005, bf16, with residual to INT8 31 us, 14 so; 2048 of 4097 45 and 17.)
 // ---------------------------------------------------------------------------
 struct Who {
   int t, n;
 };
-template <bool kVec>
-__device__ __forceinline__ int elem_at(int k, int j, Who w) {
-  return kVec ? 8 * (k * w.n + w.t) + j : (8 * k + j) * w.n + w.t;
-}
+__device__ __forceinline__ int elem_at(int k, int j, Who w) { return 8 * (k * w.n + w.t) + j; }
 
 __device__ __forceinline__ Raw8 load_cached8(const uint16_t* p) {
   return Raw8{*reinterpret_cast<const uint4*>(p), make_uint4(0, 0, 0, 0)};
@@ -44,26 +43,57 @@ __device__ __forceinline__ Raw8 load_cached8(const float* p) {
   return Raw8{*reinterpret_cast<const uint4*>(p), *reinterpret_cast<const uint4*>(p + 4)};
 }
 
-// kOnce: read by this thread only (non-temporal); else shared with other rows.
+// 16 and 8 bytes at the alignment of what they hold (no hints: neighbours share the lines).
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_at1 __attribute__((ext_vector_type(2), aligned(1)));
+__device__ __forceinline__ Raw8 load_any8(const uint16_t* p) {
+  const u32x4_at2 w = *reinterpret_cast<const u32x4_at2*>(p);
+  return Raw8{make_uint4(w.x, w.y, w.z, w.w), make_uint4(0, 0, 0, 0)};
+}
+__device__ __forceinline__ Raw8 load_any8(const float* p) {
+  const u32x4_at4 w = reinterpret_cast<const u32x4_at4*>(p)[0], z = reinterpret_cast<const u32x4_at4*>(p)[1];
+  return Raw8{make_uint4(w.x, w.y, w.z, w.w), make_uint4(z.x, z.y, z.z, z.w)};
+}
+
+// The elements of a unit from d on (below 8), zeros behind them.
+__device__ __forceinline__ Raw8 without(Raw8 r, const uint16_t*, int d) {
+  if (d & 4) r.a = make_uint4(r.a.z, r.a.w, 0, 0);
+  if (d & 2) r.a = make_uint4(r.a.y, r.a.z, r.a.w, 0);
+  if (d & 1)
+    r.a = make_uint4(r.a.x >> 16 | r.a.y << 16, r.a.y >> 16 | r.a.z << 16, r.a.z >> 16 | r.a.w << 16, r.a.w >> 16);
+  return r;
+}
+__device__ __forceinline__ Raw8 without(Raw8 r, const float*, int d) {
+  if (d & 4) r = Raw8{r.b, make_uint4(0, 0, 0, 0)};
+  if (d & 2) r = Raw8{make_uint4(r.a.z, r.a.w, r.b.x, r.b.y), make_uint4(r.b.z, r.b.w, 0, 0)};
+  if (d & 1) r = Raw8{make_uint4(r.a.y, r.a.z, r.a.w, r.b.x), make_uint4(r.b.y, r.b.z, r.b.w, 0)};
+  return r;
+}
+
+// kOnce: read by this thread only (non-temporal); else shared with other rows.  `front` elements of
+// the row lie in front of p.
 template <bool kVec, int kU, bool kOnce, typename T>
-__device__ __forceinline__ void load_row(const T* __restrict__ p, int cols, Who t, float (&v)[kU][8]) {
-  if constexpr (kVec) {
-    Raw8 raw[kU];
+__device__ __forceinline__ void load_row(const T* __restrict__ p, int cols, Who t, float (&v)[kU][8], int front = 0) {
+  if (!kVec && kU == 1 && front + cols < 8) {   // (such rows have one unit a thread)
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      const int e = elem_at<true>(k, 0, t);
-      raw[k] = e < cols ? (kOnce ? load_raw8(p + e) : load_cached8(p + e)) : Raw8{};
+    for (int j = 0; j < 8; ++j) v[0][j] = elem_at(0, j, t) < cols ? ld1(p + elem_at(0, j, t)) : 0.0f;
+    return;
+  }
+  Raw8 raw[kU];
+#pragma unroll
+  for (int k = 0; k < kU; ++k) {
+    const int e = elem_at(k, 0, t);
+    if constexpr (kVec) raw[k] = e < cols ? (kOnce ? load_raw8(p + e) : load_cached8(p + e)) : Raw8{};
+    else raw[k] = e < cols ? load_any8(p + min(e, cols - 8)) : Raw8{};
+  }
+#pragma unroll
+  for (int k = 0; k < kU; ++k) {
+    if constexpr (!kVec) {
+      const int e = elem_at(k, 0, t);
+      if (e < cols && e > cols - 8) raw[k] = without(raw[k], p, e - (cols - 8));
     }
-#pragma unroll
-    for (int k = 0; k < kU; ++k) widen8(raw[k], p, v[k]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < kU; ++k)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = elem_at<false>(k, j, t);
-        v[k][j] = e < cols ? ld1(p + e) : 0.0f;
-      }
+    widen8(raw[k], p, v[k]);
   }
 }
 
@@ -79,20 +109,28 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   st_nt16(p, as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
   st_nt16(p + 4, as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7]));
 }
+__device__ __forceinline__ void store_any8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<u32x4_at2*>(p) =
+      u32x4_at2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+}
+__device__ __forceinline__ void store_any8(float* p, const float (&v)[8]) {
+  reinterpret_cast<u32x4_at4*>(p)[0] = u32x4_at4{as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3])};
+  reinterpret_cast<u32x4_at4*>(p)[1] = u32x4_at4{as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7])};
+}
 
 template <bool kVec, int kU, typename T>
 __device__ __forceinline__ void store_row(T* __restrict__ p, int cols, Who t, const float (&v)[kU][8]) {
 #pragma unroll
   for (int k = 0; k < kU; ++k) {
+    const int e = elem_at(k, 0, t);
     if constexpr (kVec) {
-      const int e = elem_at<true>(k, 0, t);
       if (e < cols) store8(p + e, v[k]);
+    } else if (e + 8 <= cols) {
+      store_any8(p + e, v[k]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = elem_at<false>(k, j, t);
-        if (e < cols) store1(p + e, v[k][j]);
-      }
+      for (int j = 0; j < 7; ++j)
+        if (e + j < cols) store1(p + e + j, v[k][j]);
     }
   }
 }
@@ -116,15 +154,15 @@ __device__ __forceinline__ void store_codes(uint8_t* __restrict__ p, int cols, W
 #pragma unroll
   for (int k = 0; k < kU; ++k) {
     const uint2 w = pack_codes(elem, v[k], s);
+    const int e = elem_at(k, 0, t);
     if constexpr (kVec) {
-      const int e = elem_at<true>(k, 0, t);
       if (e < cols) st_nt8(p + e, w.x, w.y);
+    } else if (e + 8 <= cols) {
+      *reinterpret_cast<u32x2_at1*>(p + e) = u32x2_at1{w.x, w.y};
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = elem_at<false>(k, j, t);
-        if (e < cols) p[e] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-      }
+      for (int j = 0; j < 7; ++j)
+        if (e + j < cols) p[e + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
     }
   }
 }
@@ -132,16 +170,6 @@ __device__ __forceinline__ void store_codes(uint8_t* __restrict__ p, int cols, W
 // ---------------------------------------------------------------------------
 // Reductions over the threads of a row; every thread receives the result.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float wave_sum(float v) {
-  v += as_f(dpp<kDppXor1>(as_u(v)));
-  v += as_f(dpp<kDppXor2>(as_u(v)));
-  v += as_f(dpp<kDppHalfMirror>(as_u(v)));
-  v += as_f(dpp<kDppMirror>(as_u(v)));
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
-  return v;
-}
-
 struct SumMax {
   float sum;
   uint32_t max;
@@ -149,12 +177,21 @@ struct SumMax {
 constexpr int kWaves = 16;   // at most, of a workgroup
 
 // The sum and the largest bit pattern at once.  `red` (kWaves entries) is free to be
-// written when the call starts; a second call takes another one.  kMany: a row a wave.
-template <bool kMany>
+// written when the call starts; a second call takes another one.  kLanes: of a row, 8 to 64, or
+// more for the whole workgroup.
+template <int kLanes>
 __device__ __forceinline__ SumMax row_reduce(float sum, uint32_t most, SumMax* red) {
-  sum = wave_sum(sum);
-  most = wave_umax(most);
-  if constexpr (!kMany) {
+  sum += as_f(dpp<kDppXor1>(as_u(sum)));
+  sum += as_f(dpp<kDppXor2>(as_u(sum)));
+  sum += as_f(dpp<kDppHalfMirror>(as_u(sum)));
+  if constexpr (kLanes > 8) sum += as_f(dpp<kDppMirror>(as_u(sum)));
+  most = group_umax<(kLanes > 8 ? 16 : 8)>(most);
+#pragma unroll
+  for (int far = 16; far < 64 && far < kLanes; far *= 2) {
+    sum += __shfl_xor(sum, far);
+    most = max(most, (uint32_t)__shfl_xor((int)most, far));
+  }
+  if constexpr (kLanes > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = SumMax{sum, most};
     __syncthreads();
     sum = 0.0f;
@@ -177,7 +214,7 @@ __device__ __forceinline__ uint32_t amax_of(const float (&v)[kU][8]) {
 
 // (mean, r) of a row; kinds: RMS (mean 0) or layer.  v keeps its values, centred for a
 // layer norm (elements behind the row stay 0).
-template <bool kVec, bool kMany, int kU>
+template <int kLanes, int kU>
 __device__ __forceinline__ float norm_stats(bool layer, float eps, int cols, Who t, float (&v)[kU][8],
                                             SumMax* red) {
   if (layer) {
@@ -186,45 +223,44 @@ __device__ __forceinline__ float norm_stats(bool layer, float eps, int cols, Who
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += v[k][j];
-    const float mean = row_reduce<kMany>(s, 0, red).sum / (float)cols;
+    const float mean = row_reduce<kLanes>(s, 0, red).sum / (float)cols;
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        v[k][j] = elem_at<kVec>(k, j, t) < cols ? v[k][j] - mean : 0.0f;
+        v[k][j] = elem_at(k, j, t) < cols ? v[k][j] - mean : 0.0f;
   }
   float q = 0.0f;
 #pragma unroll
   for (int k = 0; k < kU; ++k)
 #pragma unroll
     for (int j = 0; j < 8; ++j) q = __builtin_fmaf(v[k][j], v[k][j], q);
-  const float ms = row_reduce<kMany>(q, 0, red + kWaves).sum / (float)cols;
+  const float ms = row_reduce<kLanes>(q, 0, red + kWaves).sum / (float)cols;
   return 1.0f / sqrtf(ms + eps);
 }
 
-// How rows are taken: four a workgroup, a wave each, or one by up to kThreads threads; kU
-// units a thread.
+// How rows are taken: by 8 to 64 lanes each, as many as 256 threads hold, or one by up to
+// kMost threads; kU units a thread.
 template <int kUnits, int kMost>
 struct Shape {
-  static constexpr bool many = kMost == 0;
-  static constexpr int kU = kUnits, threads = many ? 256 : kMost;
+  static constexpr int kU = kUnits, lanes = kMost, threads = kMost > 64 ? kMost : 256;
+  static constexpr int rows = kMost > 64 ? 1 : 256 / kMost;
 };
 
 // This thread's row and place in it.
-template <bool kMany>
+template <typename S>
 __device__ __forceinline__ int64_t row_of(Who& t) {
-  t = kMany ? Who{(int)threadIdx.x & 63, 64} : Who{(int)threadIdx.x, (int)blockDim.x};
-  return kMany ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  t = S::rows > 1 ? Who{(int)threadIdx.x & (S::lanes - 1), S::lanes} : Who{(int)threadIdx.x, (int)blockDim.x};
+  return (int64_t)blockIdx.x * S::rows + (S::rows > 1 ? threadIdx.x / S::lanes : 0);
 }
 
 template <typename T, bool kVec, typename S>
 __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
-  constexpr bool kMany = S::many;
-  constexpr int kU = S::kU;
+  constexpr int kU = S::kU, kLanes = S::lanes;
   __shared__ SumMax red[5 * kWaves];
   Who t;
-  const int64_t row = row_of<kMany>(t);
-  if (kMany && row >= a.rows) return;   // whole waves; no barrier with several rows
+  const int64_t row = row_of<S>(t);
+  if (row >= a.rows) return;   // all of a row's lanes; no barrier with several rows
 
   // everything that the row alone decides is on its way before the first sum
   float v[kU][8], res[kU][8];
@@ -233,7 +269,7 @@ __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
     load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.residual) + row * a.res_stride, a.cols, t, res);
   const bool layer = a.layer;
   if (a.post) {
-    const float r = norm_stats<kVec, kMany, kU>(layer, a.eps, a.cols, t, v, red + 3 * kWaves);
+    const float r = norm_stats<kLanes, kU>(layer, a.eps, a.cols, t, v, red + 3 * kWaves);
     float w[kU][8];
     load_row<kVec, kU, false>(reinterpret_cast<const T*>(a.post), a.cols, t, w);
 #pragma unroll
@@ -278,14 +314,14 @@ __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
   float r = 1.0f;
   uint32_t most = 0;
   if (layer) {
-    const float rl = norm_stats<kVec, kMany, kU>(true, a.eps, a.cols, t, v, red);
+    const float rl = norm_stats<kLanes, kU>(true, a.eps, a.cols, t, v, red);
     float b[kU][8] = {};
     if (a.bias) load_row<kVec, kU, false>(reinterpret_cast<const T*>(a.bias), a.cols, t, b);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * rl * w[k][j] + b[k][j];
-    if (a.form == kFormRow) most = row_reduce<kMany>(0.0f, amax_of(v), red + 2 * kWaves).max;
+    if (a.form == kFormRow) most = row_reduce<kLanes>(0.0f, amax_of(v), red + 2 * kWaves).max;
   } else {
     float q = 0.0f;
 #pragma unroll
@@ -295,7 +331,7 @@ __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
         q = __builtin_fmaf(v[k][j], v[k][j], q);
         v[k][j] *= w[k][j];
       }
-    const SumMax m = row_reduce<kMany>(q, amax_of(v), red);
+    const SumMax m = row_reduce<kLanes>(q, amax_of(v), red);
     r = 1.0f / sqrtf(m.sum / (float)a.cols + a.eps);
     most = m.max;
   }
@@ -313,7 +349,7 @@ __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
   } else if constexpr (kVec) {   // 1x128 blocks: 16 threads each (cols % 128 == 0)
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      const int e = elem_at<true>(k, 0, t);
+      const int e = elem_at(k, 0, t);
       const float s = scale_of(a.elem, group_umax<16>(as_u(absmax8(v[k]))));
       const uint2 c = pack_codes(a.elem, v[k], s);
       if (e < a.cols) {
@@ -358,9 +394,9 @@ template <typename T, bool kVec, int kU>
 __device__ __forceinline__ void act_values(const ActArgs& a, int64_t row, int cols, int col0, Who t,
                                            float (&v)[kU][8]) {
   float up[kU][8];
-  load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.gate) + row * a.gate_stride + col0, cols, t, v);
+  load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.gate) + row * a.gate_stride + col0, cols, t, v, col0);
   if (a.up)
-    load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.up) + row * a.up_stride + col0, cols, t, up);
+    load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.up) + row * a.up_stride + col0, cols, t, up, col0);
 #pragma unroll
   for (int k = 0; k < kU; ++k)
 #pragma unroll
@@ -373,24 +409,25 @@ __device__ __forceinline__ void act_values(const ActArgs& a, int64_t row, int co
 // A scale per row.
 template <typename T, bool kVec, typename S>
 __global__ __launch_bounds__(S::threads) void k_act_row(ActArgs a) {
-  constexpr bool kMany = S::many;
-  constexpr int kU = S::kU;
+  constexpr int kU = S::kU, kLanes = S::lanes;
   __shared__ SumMax red[kWaves];
   Who t;
-  const int64_t row = row_of<kMany>(t);
-  if (kMany && row >= a.rows) return;
+  const int64_t row = row_of<S>(t);
+  if (row >= a.rows) return;
   float v[kU][8];
   act_values<T, kVec, kU>(a, row, a.cols, 0, t, v);
-  const float s = scale_of(a.elem, row_reduce<kMany>(0.0f, amax_of(v), red).max);
+  const float s = scale_of(a.elem, row_reduce<kLanes>(0.0f, amax_of(v), red).max);
   store_codes<kVec, kU>(reinterpret_cast<uint8_t*>(a.out) + row * a.cols, a.cols, t, a.elem, s, v);
   if (t.t == 0) a.scales[row] = s;
 }
 
-// Plain values or 1x128 blocks: a workgroup takes 256 units of one row.
+// Plain values or 1x128 blocks: a workgroup takes 256 units of one row, or several narrow rows
+// by 2^shift threads each (327680 rows of 128, bf16 SwiGLU 44 us, 330 with a workgroup each).
 template <typename T, bool kVec>
-__global__ __launch_bounds__(256) void k_act_flat(ActArgs a, uint32_t pieces) {
-  const Who t{(int)threadIdx.x, 256};
-  const int64_t row = blockIdx.x / pieces;
+__global__ __launch_bounds__(256) void k_act_flat(ActArgs a, uint32_t pieces, int shift) {
+  const Who t{(int)threadIdx.x & ((1 << shift) - 1), 256};
+  const int64_t row = ((int64_t)(blockIdx.x / pieces) << (8 - shift)) + (threadIdx.x >> shift);
+  if (row >= a.rows) return;
   const int col0 = (int)(blockIdx.x % pieces) * 2048, cols = min(a.cols - col0, 2048);
   float v[1][8];
   act_values<T, kVec, 1>(a, row, cols, col0, t, v);
@@ -407,7 +444,8 @@ __global__ __launch_bounds__(256) void k_act_flat(ActArgs a, uint32_t pieces) {
 }
 
 // f(shape, grid, threads) for rows of `cols` elements.  Up to 512, or 1024 of many rows, fit a
-// wave; wider ones get as many waves as they need.  Threads without an element cost as much
+// wave, narrow ones a part of it (327680 heads of 128 31 us with 16 lanes each, 87 with 64; of 64
+// 16 with 8, 24 with 16); wider ones get as many waves as they need.  Threads without an element cost as much
 // as others (16384 rows of 1024: 21 us with 64 threads a row, 30 with 256), and fewer units a
 // thread shorten a few rows (64 of 4096: 3.2 / 3.9 / 4.0 us at 1 / 2 / 4 units) and cost
 // many little (8192 of 4096: 41.7 / 39.8 / 39.8).  Many wide rows of an activation are
@@ -417,11 +455,14 @@ template <typename F>
 void with_row_shape(int64_t rows, int cols, bool light, F f) {
   auto go = [&](auto shape) {
     using S = decltype(shape);
-    if (S::many) f(shape, (uint32_t)((rows + 3) / 4), S::threads);
-    else f(shape, (uint32_t)rows, (cols + 512 * S::kU - 1) / (512 * S::kU) * 64);
+    const int threads = S::rows > 1 ? S::threads : (cols + 512 * S::kU - 1) / (512 * S::kU) * 64;
+    f(shape, (uint32_t)((rows + S::rows - 1) / S::rows), threads);
   };
-  if (cols <= 512) go(Shape<1, 0>{});
-  else if (cols <= 1024 && rows >= 4096) go(Shape<2, 0>{});
+  if (cols <= 64) go(Shape<1, 8>{});
+  else if (cols <= 128) go(Shape<1, 16>{});
+  else if (cols <= 256) go(Shape<1, 32>{});
+  else if (cols <= 512) go(Shape<1, 64>{});
+  else if (cols <= 1024 && rows >= 4096) go(Shape<2, 64>{});
   else if (cols <= 4096) go(Shape<1, 512>{});
   else if (cols <= 8192) go(Shape<2, 512>{});
   else if (cols <= 16384 && !(light && rows >= 2048)) go(Shape<2, 1024>{});
@@ -459,7 +500,10 @@ hipError_t launch_act(const ActArgs& a, bool bf16, bool vec, hipStream_t st) {
       });
     } else {
       const uint32_t pieces = (uint32_t)(a.cols + 2047) / 2048;
-      k_act_flat<T, kVec><<<(uint32_t)a.rows * pieces, 256, 0, st>>>(a, pieces);
+      int shift = 3;
+      while (shift < 8 && 8 << shift < a.cols) ++shift;
+      const uint32_t grid = (uint32_t)((a.rows + (256 >> shift) - 1) >> (8 - shift)) * pieces;
+      k_act_flat<T, kVec><<<grid, 256, 0, st>>>(a, pieces, shift);
     }
   });
   return hipGetLastError();

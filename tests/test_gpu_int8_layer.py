@@ -325,6 +325,20 @@ def test_norm_odd_widths(cols, fmt, gran, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("base", [0, 504, 4096, 8192, 20480])
+def test_norm_ends_of_rows(base, dtype):
+    """A last unit of every length; what lies between the rows of h stays as it was."""
+    for cols in range(base + 1, base + 17):
+        check_norm(3, cols, dtype, "int8_sym", "row", seed=cols, eps=1e-2)
+        check_norm(3, cols, dtype, None, None, "layer", bias=True, post=True, seed=cols, eps=1e-2)
+        g = gen(cols)
+        x, r = normal(g, 3, cols).to(dtype), normal(g, 3, cols).to(dtype)
+        wide = torch.full((3, cols + 11), 7.0, dtype=dtype, device=DEV)
+        _, h = pqb.norm_quant(x, None, None, residual=r, h_out=wide[:, :cols])
+        assert torch.equal(h, (x.float() + r.float()).to(dtype)) and (wide[:, cols:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 @pytest.mark.parametrize("parts", [dict(residual=False), dict(residual=False, weight=False), dict(scale=0.22),
                                    dict(gates=1), dict(gates=4), dict(gates=12, scale=0.5), dict(post=True),
@@ -461,6 +475,15 @@ def test_act(rows, cols, fmt, gran, gated, act, dtype):
 @pytest.mark.parametrize("cols", [1, 7, 65, 513, 1285, 2049, 4095, 14337, 32767])
 def test_act_odd_widths(cols, fmt, gran, dtype):
     check_act(5, cols, dtype, fmt, gran, "silu", seed=cols)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("base", [0, 2040, 4096, 20480])
+def test_act_ends_of_rows(base, dtype):
+    """A last unit of every length, and pieces of 2048 with fewer than eight elements."""
+    for cols in range(base + 1, base + 17):
+        check_act(3, cols, dtype, "fp8_e4m3", "row", seed=cols)
+        check_act(3, cols, dtype, None, None, seed=cols)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

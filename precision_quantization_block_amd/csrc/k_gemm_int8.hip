@@ -76,36 +76,76 @@ __device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm
 
 enum Out { kF32 = 0, kBf16 = 1 };
 
-// Eight results of row m from column n on, N and n multiples of 8.
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// Rows of C that are whole lines are stored with the streaming hint: 8192 x 8192 of 64, bf16, 41
+// us, 49 without.  Others share lines and go without it, up to 16 bytes at the alignment of a
+// result (8192 x 8200 54 us, 73 with it; one by one 6826 x 5735 of 48 65 us, 48 so).  (The larger
+// tiles' float32 rows gain by it from 64 bytes on: 4614 x 12208 of 592 81 us, 91 without.)
 template <int kOut>
-__device__ __forceinline__ void store_out8(void* c, int64_t m, int n, int N, const float (&v)[8]) {
-  if constexpr (kOut == kBf16) {
-    st_nt16(reinterpret_cast<uint16_t*>(c) + m * N + n, bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
-            bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+__device__ __forceinline__ bool whole_lines(int N) { return N % (kOut == kBf16 ? 64 : 32) == 0; }
+
+template <bool kLines, int kWords>
+__device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
+  if constexpr (kWords > 4) {
+    store_words<kLines, 4>(p, w);
+    store_words<kLines, kWords - 4>(reinterpret_cast<uint32_t*>(p) + 4, w + 4);
+  } else if constexpr (kLines && kWords == 4) {
+    st_nt16(p, w[0], w[1], w[2], w[3]);
   } else {
-    float* p = reinterpret_cast<float*>(c) + m * N + n;
-    st_nt16(p, as_u(v[0]), as_u(v[1]), as_u(v[2]), as_u(v[3]));
-    st_nt16(p + 4, as_u(v[4]), as_u(v[5]), as_u(v[6]), as_u(v[7]));
+    typedef uint32_t words __attribute__((ext_vector_type(kWords), aligned(2)));
+    words x;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) x[j] = w[j];
+    *reinterpret_cast<words*>(p) = x;
   }
 }
 
-// The result of sum x in row m, column n.
-__device__ __forceinline__ float scaled(const Int8Args& g, int x, int64_t m, int n) {
-  const float v = (float)x * g.a_scales[m * g.a_step] * g.b_scales[(int64_t)n * g.b_step];
-  return g.bias ? v + g.bias[n] : v;
+// kV results of row m from column n on, those in front of N.
+template <int kOut, bool kLines, int kV>
+__device__ __forceinline__ void store_out(void* c, int64_t m, int n, int N, const float (&v)[kV]) {
+  const bool all = kLines || n + kV <= N;
+  if constexpr (kOut == kBf16) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(c) + m * N + n;
+    uint32_t w[(kV + 1) / 2];
+#pragma unroll
+    for (int j = 0; j < kV; j += 2) w[j / 2] = bf16x2_rne(v[j], v[j + 1 < kV ? j + 1 : j]);
+    if (kV > 1 && all) store_words<kLines, (kV + 1) / 2>(p, w);
+    else
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        if (n + j < N) p[j] = (uint16_t)(w[j / 2] >> (j & 1) * 16);
+  } else {
+    float* p = reinterpret_cast<float*>(c) + m * N + n;
+    if (kV > 1 && all) {
+      uint32_t w[kV];
+#pragma unroll
+      for (int j = 0; j < kV; ++j) w[j] = as_u(v[j]);
+      store_words<kLines, kV>(p, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        if (n + j < N) p[j] = v[j];
+    }
+  }
 }
 
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-// p[n .. n + 3] (p[0] with step 0), 0 at and behind N.
-__device__ __forceinline__ v4f four_at(const float* p, int step, int n, int N) {
-  typedef float v4u __attribute__((ext_vector_type(4), aligned(4)));
-  if (step == 0) return v4f{p[0], p[0], p[0], p[0]};
-  if (n + 4 <= N) return *reinterpret_cast<const v4u*>(p + n);
-  v4f v{};
+// p[n .. n + kN - 1] (p[0] with step 0), 0 at and behind N; at most four.
+template <int kN>
+__device__ __forceinline__ auto some_at(const float* p, int step, int n, int N) {
+  typedef float some __attribute__((ext_vector_type(kN)));
+  typedef float any __attribute__((ext_vector_type(kN), aligned(4)));
+  some v{};
+  if (step == 0) {
 #pragma unroll
-  for (int j = 0; j < 3; ++j)
-    if (n + j < N) v[j] = p[n + j];
+    for (int j = 0; j < kN; ++j) v[j] = p[0];
+  } else if (n + kN <= N) {
+    v = *reinterpret_cast<const any*>(p + n);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kN - 1; ++j)
+      if (n + j < N) v[j] = p[n + j];
+  }
   return v;
 }
 
@@ -268,7 +308,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int ti
     v4f sb[S::nt];
     float sa[S::mt];
 #pragma unroll
-    for (int j = 0; j < S::nt; ++j) sb[j] = four_at(g.b_scales, g.b_step, n0 + 16 * j + 4 * quarter, g.N);
+    for (int j = 0; j < S::nt; ++j) sb[j] = some_at<4>(g.b_scales, g.b_step, n0 + 16 * j + 4 * quarter, g.N);
 #pragma unroll
     for (int i = 0; i < S::mt; ++i)
       sa[i] = g.a_scales[(int64_t)min(m0 + 16 * i + r16, g.M - 1) * g.a_step];
@@ -276,7 +316,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int ti
     // lane; 16-byte chunk c of row r at c ^ r, so that rows meet in no bank
     uint8_t* out = lds + 2 * S::slot + wave * S::stage;
     constexpr int kChunks = kOut == kBf16 ? 8 : 16, kEach = 64 / kChunks;   // chunks of a row, results of a chunk
-    const bool whole = m0 + 16 * S::mt <= g.M && n0 + 64 <= g.N && g.N % kEach == 0;
+    const bool whole = m0 + 16 * S::mt <= g.M && n0 + 64 <= g.N && (kOut == kBf16 ? whole_lines<kOut>(g.N) : g.N % 16 == 0);
 #pragma unroll
     for (int i = 0; i < S::mt; i += kRows / 16) {
 #pragma unroll
@@ -287,7 +327,7 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int ti
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[r] = (float)acc[i + h][j][r] * sa[i + h] * sb[j][r];
           if (g.bias) {   // (read again for every row: held, its 16 registers spilled others)
-            const v4f bias = four_at(g.bias, 1, n0 + 16 * j + 4 * quarter, g.N);
+            const v4f bias = some_at<4>(g.bias, 1, n0 + 16 * j + 4 * quarter, g.N);
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] += bias[r];
           }
@@ -307,15 +347,21 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int ti
           st_nt16(reinterpret_cast<uint8_t*>(g.c) + ((int64_t)(m0 + 16 * i + row) * g.N + n0 + kEach * c) * (16 / kEach),
                   x.x, x.y, x.z, x.w);
         }
-      } else if (n0 + lane < g.N) {   // a row of 64 at a time
-        const int rows = min(kRows, g.M - m0 - 16 * i);
-        for (int row = 0; row < rows; ++row) {
-          const uint8_t* x = out + row * (kChunks * 16) + (((lane / kEach) ^ (row & (kChunks - 1))) << 4);
-          const int64_t at = (int64_t)(m0 + 16 * i + row) * g.N + n0 + lane;
-          if constexpr (kOut == kBf16)
-            reinterpret_cast<uint16_t*>(g.c)[at] = reinterpret_cast<const uint16_t*>(x)[lane % kEach];
-          else
-            reinterpret_cast<float*>(g.c)[at] = reinterpret_cast<const float*>(x)[lane % kEach];
+      } else {
+        const int rows = min(kRows, g.M - m0 - 16 * i), c = lane % kChunks, most = g.N - n0 - kEach * c;
+        for (int row = lane / kChunks; row < rows; row += kRows / 4) {
+          const uint8_t* x = out + row * (kChunks * 16) + ((c ^ (row & (kChunks - 1))) << 4);
+          uint8_t* at = reinterpret_cast<uint8_t*>(g.c) + ((int64_t)(m0 + 16 * i + row) * g.N + n0 + kEach * c) * (16 / kEach);
+          if (most >= kEach) {
+            const uint4 w = *reinterpret_cast<const uint4*>(x);
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+            store_words<false, 4>(at, words);
+          } else {
+            for (int j = 0; j < most; ++j) {
+              if constexpr (kOut == kBf16) reinterpret_cast<uint16_t*>(at)[j] = reinterpret_cast<const uint16_t*>(x)[j];
+              else reinterpret_cast<uint32_t*>(at)[j] = reinterpret_cast<const uint32_t*>(x)[j];
+            }
+          }
         }
       }
       wave_sync();
@@ -348,6 +394,7 @@ struct Ring {
   static constexpr int loads = slot / 1024 / waves;
   static constexpr int most = 163840 / kPer / slot, slots = most < 8 ? most : 8;
   static constexpr int ld = kTN + 4, sums = wk * kTM * ld * 4;
+  static constexpr int most_cols = kTM * kTN / 512, cols = most_cols < 1 ? 1 : most_cols < 8 ? most_cols : 8;
   static constexpr int lds = slots * slot > sums ? slots * slot : sums;
   static_assert(wk * kWM * kWN == waves && mt * kWM * 16 == kTM && nt * kWN * 16 == kTN, "waves");
   static_assert(steps * wk * 64 == kBK && loads * waves * 1024 == slot && slots >= 3, "blocks");
@@ -452,36 +499,35 @@ __global__ __launch_bounds__(512, 2 * kPer) void k_int8_ring(Int8Args g, int til
                               4 * quarter) = acc[i][j];
   __syncthreads();
   const int rows = min(g.M - m0, kTM);
-  if (g.N % 8 == 0) {
-    for (int u = threadIdx.x; u < rows * (kTN / 8); u += 512) {   // eight columns of a row
-      const int r = u / (kTN / 8), c = 8 * (u % (kTN / 8)), n = n0 + c;
+  // A thread takes kV columns of a row: up to eight, if all threads have some (one row over 4096
+  // channels of 4096 6.3 us with eight, 5.6 with the one that its 16 x 16 tiles give)
+  constexpr int kV = S::cols, groups = kTN / kV, kRead = kV < 4 ? kV : 4;
+  typedef int some __attribute__((ext_vector_type(kRead)));
+  auto store = [&](auto lines) {
+    for (int u = threadIdx.x; u < rows * groups; u += 512) {
+      const int r = u / groups, c = kV * (u % groups), n = n0 + c;
       if (n >= g.N) continue;
-      v4i lo{}, hi{};
+      const float sa = g.a_scales[(int64_t)(m0 + r) * g.a_step];
+      float v[kV];
 #pragma unroll
-      for (int w = 0; w < S::wk; ++w) {
-        const v4i* p = reinterpret_cast<const v4i*>(sums + (w * kTM + r) * S::ld + c);
-        lo += p[0];
-        hi += p[1];
+      for (int h = 0; h < kV; h += kRead) {
+        some x{};
+#pragma unroll
+        for (int w = 0; w < S::wk; ++w) x += *reinterpret_cast<const some*>(sums + (w * kTM + r) * S::ld + c + h);
+        const auto sb = some_at<kRead>(g.b_scales, g.b_step, n + h, g.N);
+#pragma unroll
+        for (int j = 0; j < kRead; ++j) v[h + j] = (float)x[j] * sa * sb[j];
+        if (g.bias) {
+          const auto bias = some_at<kRead>(g.bias, 1, n + h, g.N);
+#pragma unroll
+          for (int j = 0; j < kRead; ++j) v[h + j] += bias[j];
+        }
       }
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = scaled(g, j < 4 ? lo[j & 3] : hi[j & 3], m0 + r, n + j);
-      store_out8<kOut>(g.c, m0 + r, n, g.N, v);
+      store_out<kOut, decltype(lines)::value>(g.c, m0 + r, n, g.N, v);
     }
-  } else {
-    for (int u = threadIdx.x; u < rows * kTN; u += 512) {
-      const int r = u / kTN, c = u % kTN, n = n0 + c;
-      if (n >= g.N) continue;
-      int x = 0;
-#pragma unroll
-      for (int w = 0; w < S::wk; ++w) x += sums[(w * kTM + r) * S::ld + c];
-      const float v = scaled(g, x, m0 + r, n);
-      if constexpr (kOut == kBf16)
-        reinterpret_cast<uint16_t*>(g.c)[(int64_t)(m0 + r) * g.N + n] = (uint16_t)(bf16x2_rne(v, 0.0f) & 0xFFFFu);
-      else
-        reinterpret_cast<float*>(g.c)[(int64_t)(m0 + r) * g.N + n] = v;
-    }
-  }
+  };
+  if (kV == 8 && whole_lines<kOut>(g.N)) store(std::bool_constant<kV == 8>{});
+  else store(std::false_type{});
 }
 
 template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer>

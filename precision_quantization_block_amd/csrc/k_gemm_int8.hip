@@ -403,15 +403,16 @@ struct Ring {
 };
 
 template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer, int kOut>
-__global__ __launch_bounds__(512, 2 * kPer) void k_int8_ring(Int8Args g, int tiles_m) {
+__global__ __launch_bounds__(512, 2 * kPer) void k_int8_ring(Int8Args g, int inner, bool along_n) {
   using S = Ring<kTM, kTN, kBK, kWM, kWN, kPer>;
   __shared__ __align__(16) uint8_t lds[S::lds];
   const int lane = threadIdx.x & 63, r16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Workgroups of one XCD take tiles in turn that share their rows of B
+  // Workgroups of one XCD take tiles in turn that share their rows of the larger matrix
   const int nwg = gridDim.x, xcd = blockIdx.x & 7, per = nwg >> 3, more = nwg & 7;
   const int tile = xcd * per + min(xcd, more) + (blockIdx.x >> 3);
-  const int tn = tile / tiles_m, m0 = (tile - tn * tiles_m) * kTM, n0 = tn * kTN;
+  const int shared = tile / inner, other = tile - shared * inner;
+  const int m0 = (along_n ? shared : other) * kTM, n0 = (along_n ? other : shared) * kTN;
   const int nkb = (g.K + kBK - 1) / kBK;
 
   // Instruction j of a wave fills rows (j waves + wave) S::rows ... of [A | B]
@@ -429,7 +430,7 @@ __global__ __launch_bounds__(512, 2 * kPer) void k_int8_ring(Int8Args g, int til
   const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(lds) + wave * 1024);
   // Workgroups start at different blocks: rows that lie a power of two apart would all be read from
   // the same few memory channels at a time (16 rows over 28672 channels of 4096 26 to 24 us).
-  const int turn = nkb ? tn % nkb : 0;
+  const int turn = nkb ? shared % nkb : 0;
   auto issue = [&](int kb, int slot) {
     const int at = kb + turn, k = kb < nkb ? (at < nkb ? at : at - nkb) * kBK : g.K;
 #pragma unroll
@@ -534,8 +535,10 @@ template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer>
 hipError_t launch_ring(const Int8Args& g, bool out_bf16, hipStream_t st) {
   const int tiles_m = (g.M + kTM - 1) / kTM, tiles_n = (g.N + kTN - 1) / kTN;
   const uint32_t grid = (uint32_t)tiles_m * (uint32_t)tiles_n;
-  if (out_bf16) k_int8_ring<kTM, kTN, kBK, kWM, kWN, kPer, kBf16><<<grid, 512, 0, st>>>(g, tiles_m);
-  else k_int8_ring<kTM, kTN, kBK, kWM, kWN, kPer, kF32><<<grid, 512, 0, st>>>(g, tiles_m);
+  const bool along_n = g.M > g.N;
+  const int inner = along_n ? tiles_n : tiles_m;
+  if (out_bf16) k_int8_ring<kTM, kTN, kBK, kWM, kWN, kPer, kBf16><<<grid, 512, 0, st>>>(g, inner, along_n);
+  else k_int8_ring<kTM, kTN, kBK, kWM, kWN, kPer, kF32><<<grid, 512, 0, st>>>(g, inner, along_n);
   return hipGetLastError();
 }
 
@@ -553,7 +556,7 @@ int64_t tiles(const Int8Args& g, int tm, int tn) {
   return (int64_t)((g.M + tm - 1) / tm) * ((g.N + tn - 1) / tn);
 }
 
-// The rings, smaller tiles first.
+// The rings, of two that move the same the faster one later.
 struct RingTile {
   int tm, tn;
   hipError_t (*launch)(const Int8Args&, bool, hipStream_t);
@@ -562,17 +565,38 @@ constexpr RingTile kRings[] = {
     {16, 16, launch_ring<16, 16, 512, 1, 1, 2>},   {16, 32, launch_ring<16, 32, 512, 1, 2, 2>},
     {32, 16, launch_ring<32, 16, 512, 1, 1, 2>},   {32, 32, launch_ring<32, 32, 256, 1, 2, 2>},
     {32, 64, launch_ring<32, 64, 256, 1, 4, 2>},   {64, 32, launch_ring<64, 32, 256, 2, 1, 2>},
-    {64, 64, launch_ring<64, 64, 128, 2, 2, 2>},   {64, 128, launch_ring<64, 128, 128, 1, 4, 2>},
-    {128, 64, launch_ring<128, 64, 128, 2, 2, 2>}};
-// 128 x 64 with one workgroup a CU and twice the bytes in flight, where there are no more: 512 rows over
-// 4096 channels of 14336, from HBM, 57 to 49 us; 1024 over 4096 of 4096 33 us with it, 27 without.
+    {64, 64, launch_ring<64, 64, 128, 2, 2, 2>},   {128, 64, launch_ring<128, 64, 128, 2, 2, 2>},
+    {64, 128, launch_ring<64, 128, 128, 1, 4, 2>}};
+// 128 x 64 with one workgroup a CU and twice the bytes in flight, where there are no more and K is
+// long enough to be short of them: 512 rows over 4096 channels of 14336, from HBM, 47 us, 53 without,
+// of 4096 15.8 and 14.7; 1024 over 4096 of 4096 33 us with it, 27 without.
 constexpr auto kDeepRing = launch_ring<128, 64, 256, 1, 2, 1>;
 
 }  // namespace
 
+// What a product takes, us, in units of K = 4096; with n tiles and `round` places a round,
+// the last round costs less the emptier it is.  Fitted to the table below.
+struct Parts {
+  int64_t full, rest;   // full rounds, tiles of the last one
+  double share;         // of its places
+  Parts(int64_t n, int round) : full(n / round), rest(n % round), share((double)(n % round) / round) {}
+};
+double ring_us(double k, double c) {   // c rounds of 128 x 64 tiles, or of as many bytes
+  return 3 + 1.8 * c + k * std::max(std::min(12 * c, 12 + 5.4 * (c - 1)), 13.3 * c - 9.3);
+}
+double small_us(double k, int64_t n) {   // 128 x 128, two a CU
+  const Parts p(n, 512);
+  const double last = p.rest == 0 ? 0 : p.share <= 0.5 ? 19 + 4 * p.share : 21 + 26 * (p.share - 0.5);
+  return 3 + 3 * p.full + (p.rest ? 2.5 + 0.5 * p.share : 0) + k * (34 * p.full + last);
+}
+double large_us(double k, int64_t n) {   // 256 x 256
+  const Parts p(n, 256);
+  return 6 + 6 * p.full + (p.rest ? 4 + 2 * p.share : 0) + k * (50 * p.full + (p.rest ? 30 + 20 * p.share * p.share : 0));
+}
+
 // The ring whose busiest of 256 CUs moves the fewest bytes into LDS for each byte of K, the
-// larger tile where two are equal; or tiles of 128 x 128 (two a CU) or 256 x 256, if they are
-// estimated to take less.  Measured, us:
+// later of them where two are equal; or tiles of 128 x 128 or 256 x 256, if they are estimated to
+// take less.  Measured, us:
 //   K = 4096, tiles        16 x 16  16 x 32  32 x 16  32 x 32  32 x 64  64 x 32  64 x 64  128 x 64
 //   16 over 14336             13.9     11.2               -      11.3                -         -
 //   64 over 2048               6.8      5.3      5.8      5.9      7.0      6.7      9.7      12.4
@@ -580,8 +604,12 @@ constexpr auto kDeepRing = launch_ring<128, 64, 256, 1, 2, 1>;
 //   33 over 14336             29.2     19.6     23.7     17.5     12.8     12.5     12.1      13.7
 //   128 over 4096             22.2     13.9     14.3      9.7      8.3      8.3     10.1      14.4
 //   256 over 4096             40.4     27.3     26.3     16.9     12.2     12.3     10.8      14.7
-//   rings of 128 x 64, 128 x 128, 256 x 256: 512 rows over 4096 16 / 26 / 44, 1024 rows 27 / 26 / 44,
-//   2048 rows 60 / 40 / 47, 4096 rows 151 / 83 / 65; 8192 over 7168 of 2048 269 / 146 / 122
+// and rings of 64 x 128, 128 x 128, 256 x 256 (in brackets what is estimated; all as they are
+// taken over 114 shapes, chosen 3% slower than the fastest of these and the small ones in the mean):
+//   K = 4096:  768 over 4096  22 (24)   24 (26)   41 (41);   1536  38 (39)   33 (33)   44 (44)
+//              2048  53 (54)   38 (40)   46 (46);   3000  79 (84)   63 (64)   54 (53);   4096 109 (114)   77 (77)   65 (62)
+//   8192 over 8192 of 64  72 (67)   33 (31)   38 (33);   of 512 104 (113)   65 (61)   58 (55)
+//   8192 over 7168 of 2048 204 (235)   145 (143)   123 (122);   1024 over 4096 of 14336 93 (67)   105 (79)   167 (120)
 // (The last, partial round of 256 x 256 tiles cut into 128 x 128 ones in a second launch gained
 // nothing, nor did parts of K summed by a second launch: 512 over 4096 of 14336 43 us as a
 // ring, 45 in four parts.)
@@ -592,15 +620,13 @@ hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st) {
     const int64_t n = tiles(g, r.tm, r.tn), cost = (n + 255) / 256 * (r.tm + r.tn);
     if (n < 1 << 22 && cost <= least) least = cost, ring = &r;   // (a grid has less than 2^32 threads)
   }
-  const double k = g.K / 4096.0;
-  const int64_t small = tiles(g, 128, 128), large = (tiles(g, 256, 256) + 255) / 256;
-  const double by_ring = 3 + 12 * k * ((double)least / 192), by_large = 8 + (54 * k + 3) * large;
-  const double by_small = 4 + 36 * k * (small / 512) + (small % 512 > 256 ? 36 * k : small % 512 ? 22 * k : 0);
-  if (least != INT64_MAX && by_ring <= by_small && by_ring <= by_large) {   // (K = 0: all are 0)
-    if (ring->tm == 128 && least == 192) return kDeepRing(g, out_bf16, st);   // one round
+  const double k = g.K / 4096.0, by_ring = ring_us(k, least / 192.0);
+  const double by_small = small_us(k, tiles(g, 128, 128)), by_large = large_us(k, tiles(g, 256, 256));
+  if (least != INT64_MAX && by_ring <= by_small && by_ring <= by_large) {
+    if (least == 192 && g.K > 4096 && tiles(g, 128, 64) <= 256) return kDeepRing(g, out_bf16, st);
     return ring->launch(g, out_bf16, st);
   }
-  if (by_small <= by_large) return launch_tile<128, 128, 2, 2>(g, out_bf16, small, st);
+  if (by_small <= by_large) return launch_tile<128, 128, 2, 2>(g, out_bf16, 512, st);
   return launch_tile<256, 256, 2, 4>(g, out_bf16, 256, st);
 }
 

@@ -107,6 +107,20 @@ def test_gemm_every_tile(m, n, k):
     check_gemm(m, n, k, BF if k % 32 else F32, seed=m, bias=m % 2 == 1, pads=(0, 16) if k == 400 else (0, 0))
 
 
+@pytest.mark.parametrize("k", [400, 2512])
+@pytest.mark.parametrize("m,n", [(974, 11), (1355, 81), (1319, 55), (1864, 66), (1610, 302), (4734, 40), (2480, 351), (5469, 312), (326, 5439),
+                                 (1771, 668), (7040, 316), (8100, 64)])
+def test_gemm_more_rows_than_channels(m, n, k):
+    """Tiles in the order that shares rows of A (and 128 x 64, either way)."""
+    check_gemm(m, n, k, F32 if k == 400 else BF, seed=n, bias=n % 2 == 1)
+
+
+@pytest.mark.parametrize("m,n,k", [(500, 4090, 4112), (4090, 500, 4368), (300, 4000, 5008)])
+def test_gemm_long_rows_few_tiles(m, n, k):
+    check_gemm(m, n, k, BF, seed=k, bias=True)
+    check_gemm(m, n, k, F32, seed=k, pads=(16, 0))
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_gemm_every_code_and_longest_sum(m):
     """Codes down to -128 over the longest k: sums up to 2^31 - 2^18."""

@@ -71,32 +71,37 @@ __device__ __forceinline__ Raw8 without(Raw8 r, const float*, int d) {
   return r;
 }
 
-// kOnce: read by this thread only (non-temporal); else shared with other rows.  `front` elements of
-// the row lie in front of p.
+// A row's units as loaded, and as floats: apart, so that several arrays' loads are on their way
+// before the first is waited for.  kOnce: read by this thread only (non-temporal); else shared with
+// other rows.  `front` elements of the row lie in front of p.
 template <bool kVec, int kU, bool kOnce, typename T>
-__device__ __forceinline__ void load_row(const T* __restrict__ p, int cols, Who t, float (&v)[kU][8], int front = 0) {
+__device__ __forceinline__ void fetch(const T* __restrict__ p, int cols, Who t, Raw8 (&raw)[kU], int front = 0) {
   if (!kVec && kU == 1 && front + cols < 8) {   // (such rows have one unit a thread)
+    uint32_t x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[0][j] = elem_at(0, j, t) < cols ? ld1(p + elem_at(0, j, t)) : 0.0f;
+    for (int j = 0; j < 8; ++j) x[j] = elem_at(0, j, t) < cols ? as_u(ld1(p + elem_at(0, j, t))) : 0;
+    if constexpr (sizeof(T) == 2)
+      raw[0] = Raw8{make_uint4(x[0] >> 16 | x[1], x[2] >> 16 | x[3], x[4] >> 16 | x[5], x[6] >> 16 | x[7]), {}};
+    else raw[0] = Raw8{make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7])};
     return;
   }
-  Raw8 raw[kU];
 #pragma unroll
   for (int k = 0; k < kU; ++k) {
     const int e = elem_at(k, 0, t);
     if constexpr (kVec) raw[k] = e < cols ? (kOnce ? load_raw8(p + e) : load_cached8(p + e)) : Raw8{};
     else raw[k] = e < cols ? load_any8(p + min(e, cols - 8)) : Raw8{};
   }
+}
+template <bool kVec, int kU, typename T>
+__device__ __forceinline__ void widen(const T* p, int cols, Who t, const Raw8 (&raw)[kU], float (&v)[kU][8], int front = 0) {
 #pragma unroll
   for (int k = 0; k < kU; ++k) {
-    if constexpr (!kVec) {
-      const int e = elem_at(k, 0, t);
-      if (e < cols && e > cols - 8) raw[k] = without(raw[k], p, e - (cols - 8));
-    }
-    widen8(raw[k], p, v[k]);
+    const int e = elem_at(k, 0, t);
+    Raw8 r = raw[k];
+    if (!kVec && front + cols >= 8 && e < cols && e > cols - 8) r = without(r, p, e - (cols - 8));
+    widen8(r, p, v[k]);
   }
 }
-
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)(bf16x2_rne(v, 0.0f) & 0xFFFFu); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ float rounded(const uint16_t*, float v) { return as_f(bf16x2_rne(v, 0.0f) << 16); }
@@ -262,31 +267,49 @@ __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
   const int64_t row = row_of<S>(t);
   if (row >= a.rows) return;   // all of a row's lanes; no barrier with several rows
 
-  // everything that the row alone decides is on its way before the first sum
-  float v[kU][8], res[kU][8];
-  load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.x) + row * a.x_stride, a.cols, t, v);
-  if (a.residual)
-    load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.residual) + row * a.res_stride, a.cols, t, res);
+  // The loads of x and residual are on their way before the first sum; where they fit the
+  // registers, so are those of all others
+  constexpr bool kEarly = kU == 1;
+  const T* post = reinterpret_cast<const T*>(a.post);
+  const T* gate = a.gate ? reinterpret_cast<const T*>(a.gate) + (int64_t)((uint32_t)row / a.per_gate) * a.gate_stride
+                         : nullptr;
+  const T* weight = reinterpret_cast<const T*>(a.weight);
+  const T* bias = reinterpret_cast<const T*>(a.bias);
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.x_stride;
+  Raw8 raw_x[kU], raw_res[kU], raw_post[kU], raw_gate[kU], raw_weight[kU], raw_bias[kU];
+  fetch<kVec, kU, true>(x, a.cols, t, raw_x);
+  if (a.residual) fetch<kVec, kU, true>(reinterpret_cast<const T*>(a.residual) + row * a.res_stride, a.cols, t, raw_res);
+  if (kEarly && post) fetch<kVec, kU, false>(post, a.cols, t, raw_post);
+  if (kEarly && gate) fetch<kVec, kU, false>(gate, a.cols, t, raw_gate);
+  if (kEarly && weight) fetch<kVec, kU, false>(weight, a.cols, t, raw_weight);
+  if (kEarly && bias) fetch<kVec, kU, false>(bias, a.cols, t, raw_bias);
+  auto get = [&](const T* p, Raw8 (&raw)[kU], float (&to)[kU][8]) {
+    if (!kEarly) fetch<kVec, kU, false>(p, a.cols, t, raw);
+    widen<kVec, kU>(p, a.cols, t, raw, to);
+  };
+  float v[kU][8];
+  widen<kVec, kU>(x, a.cols, t, raw_x, v);
   const bool layer = a.layer;
-  if (a.post) {
+  if (post) {
     const float r = norm_stats<kLanes, kU>(layer, a.eps, a.cols, t, v, red + 3 * kWaves);
     float w[kU][8];
-    load_row<kVec, kU, false>(reinterpret_cast<const T*>(a.post), a.cols, t, w);
+    get(post, raw_post, w);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * r * w[k][j];
   }
-  if (a.gate) {
+  if (gate) {
     float g[kU][8];
-    load_row<kVec, kU, false>(
-        reinterpret_cast<const T*>(a.gate) + (int64_t)((uint32_t)row / a.per_gate) * a.gate_stride, a.cols, t, g);
+    get(gate, raw_gate, g);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] *= g[k][j];
   }
   if (a.residual) {
+    float res[kU][8];
+    widen<kVec, kU>(x, a.cols, t, raw_res, res);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
@@ -303,8 +326,8 @@ __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
 
   // u, and r where it is not in u
   float w[kU][8];
-  if (a.weight) {
-    load_row<kVec, kU, false>(reinterpret_cast<const T*>(a.weight), a.cols, t, w);
+  if (weight) {
+    get(weight, raw_weight, w);
   } else {
 #pragma unroll
     for (int k = 0; k < kU; ++k)
@@ -316,7 +339,7 @@ __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
   if (layer) {
     const float rl = norm_stats<kLanes, kU>(true, a.eps, a.cols, t, v, red);
     float b[kU][8] = {};
-    if (a.bias) load_row<kVec, kU, false>(reinterpret_cast<const T*>(a.bias), a.cols, t, b);
+    if (bias) get(bias, raw_bias, b);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
 #pragma unroll
@@ -393,10 +416,14 @@ __device__ __forceinline__ float activate(int act, float g) {
 template <typename T, bool kVec, int kU>
 __device__ __forceinline__ void act_values(const ActArgs& a, int64_t row, int cols, int col0, Who t,
                                            float (&v)[kU][8]) {
+  const T* gate = reinterpret_cast<const T*>(a.gate) + row * a.gate_stride + col0;
+  const T* p = reinterpret_cast<const T*>(a.up) + row * a.up_stride + col0;
+  Raw8 raw_gate[kU], raw_up[kU];
+  fetch<kVec, kU, true>(gate, cols, t, raw_gate, col0);
+  if (a.up) fetch<kVec, kU, true>(p, cols, t, raw_up, col0);
+  widen<kVec, kU>(gate, cols, t, raw_gate, v, col0);
   float up[kU][8];
-  load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.gate) + row * a.gate_stride + col0, cols, t, v, col0);
-  if (a.up)
-    load_row<kVec, kU, true>(reinterpret_cast<const T*>(a.up) + row * a.up_stride + col0, cols, t, up, col0);
+  if (a.up) widen<kVec, kU>(p, cols, t, raw_up, up, col0);
 #pragma unroll
   for (int k = 0; k < kU; ++k)
 #pragma unroll
@@ -423,11 +450,12 @@ __global__ __launch_bounds__(S::threads) void k_act_row(ActArgs a) {
 
 // Plain values or 1x128 blocks: a workgroup takes 256 units of one row, or several narrow rows
 // by 2^shift threads each (327680 rows of 128, bf16 SwiGLU 44 us, 330 with a workgroup each).
-template <typename T, bool kVec>
+template <typename T, bool kVec, bool kNarrow>
 __global__ __launch_bounds__(256) void k_act_flat(ActArgs a, uint32_t pieces, int shift) {
-  const Who t{(int)threadIdx.x & ((1 << shift) - 1), 256};
-  const int64_t row = ((int64_t)(blockIdx.x / pieces) << (8 - shift)) + (threadIdx.x >> shift);
-  if (row >= a.rows) return;
+  const Who t{kNarrow ? (int)threadIdx.x & ((1 << shift) - 1) : (int)threadIdx.x, 256};
+  int64_t row = blockIdx.x / pieces;
+  if constexpr (kNarrow) row = (row << (8 - shift)) + (threadIdx.x >> shift);
+  if (kNarrow && row >= a.rows) return;
   const int col0 = (int)(blockIdx.x % pieces) * 2048, cols = min(a.cols - col0, 2048);
   float v[1][8];
   act_values<T, kVec, 1>(a, row, cols, col0, t, v);
@@ -503,7 +531,8 @@ hipError_t launch_act(const ActArgs& a, bool bf16, bool vec, hipStream_t st) {
       int shift = 3;
       while (shift < 8 && 8 << shift < a.cols) ++shift;
       const uint32_t grid = (uint32_t)((a.rows + (256 >> shift) - 1) >> (8 - shift)) * pieces;
-      k_act_flat<T, kVec><<<grid, 256, 0, st>>>(a, pieces, shift);
+      if (shift < 8) k_act_flat<T, kVec, true><<<grid, 256, 0, st>>>(a, pieces, shift);
+      else k_act_flat<T, kVec, false><<<grid, 256, 0, st>>>(a, pieces, shift);
     }
   });
   return hipGetLastError();

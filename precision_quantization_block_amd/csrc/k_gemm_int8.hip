@@ -380,10 +380,10 @@ __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int ti
 // products, the rest over the blocks' K, whose sums meet in LDS at the end.  Blocks of kBK
 // bytes of K pass through a ring of as many slots as fit: what memory latency asks to be
 // in flight.  A row of a block is kBK / 16 chunks, chunk c of row r at c ^ mix(r).  (Straight
-// from global memory into registers, 64 rows over 14336 channels of 4096 took 23 us, 12.5 so:
+// from global memory into registers, 64 rows over 14336 channels of 4096 took 23 us, 12 so:
 // a fragment's rows are 64-byte pieces, and each line was fetched twice.)  One row over 4096
-// channels of 14336 from HBM 12.7 us, 4.6 TB/s; 64 over 14336 of 4096 16 us from HBM, 12.5 from
-// the Infinity Cache (4.8 TB/s).
+// channels of 14336 from HBM 12.7 us, 4.6 TB/s; 64 over 14336 of 4096 16 us from HBM, 12 from
+// the Infinity Cache (5 TB/s).
 // ---------------------------------------------------------------------------
 template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer>
 struct Ring {

@@ -472,7 +472,7 @@ __global__ __launch_bounds__(256) void k_act_flat(ActArgs a, uint32_t pieces, in
 }
 
 // f(shape, grid, threads) for rows of `cols` elements.  Up to 512, or 1024 of many rows, fit a
-// wave, narrow ones a part of it (327680 heads of 128 31 us with 16 lanes each, 87 with 64; of 64
+// wave, narrow ones a part of it (327680 heads of 128 29 us with 16 lanes each, 87 with 64; of 64
 // 16 with 8, 24 with 16); wider ones get as many waves as they need.  Threads without an element cost as much
 // as others (16384 rows of 1024: 21 us with 64 threads a row, 30 with 256), and fewer units a
 // thread shorten a few rows (64 of 4096: 3.2 / 3.9 / 4.0 us at 1 / 2 / 4 units) and cost

@@ -670,7 +670,7 @@ pqb_status pqb_norm_quant(const pqb_norm* args, void* stream);
  *   SILU g / (1 + exp(-g));  GELU_TANH 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)));
  *   GELU_ERF 0.5 g erfc(-g / sqrt 2);  RELU2 max(g, 0)^2
  * in float32 to a few units of 2^-24 of the value (GELU_TANH: times 1 + 2 |g| + |g|^3 / 10, GELU_ERF:
- * times 1 + g^2 / 4; values below 2^-119 may be 0).  Written
+ * and up to 32 of its erfc; values below 2^-119 may be 0).  Written
  * to `out` (contiguous) rounded to dtype, or as codes and scales, pqb_quantize's of the
  * float32 v.  Inputs and v must be finite.  out may share no memory with the inputs.
  * Shape rules: cols >= 1, at most 32768 for ROW scales; BLK_1x128 needs cols % 128 == 0,

@@ -401,6 +401,19 @@ __device__ __forceinline__ float sigmoid_times(float g, float z) {
   return d < 0x1p126f ? c : 0.0f * g;                            // exp(-z) overflows: -0 for finite g
 }
 
+// 0.5 g erfc(z), z = -g / sqrt 2.  For z > 0, erfc turns the rounding of z into a relative error some
+// 2 z^2 times as large (76 units of 2^-24 at z = 6), so z's low part d is carried along: erfc(z + d) =
+// erfc(z) (1 - d h), h = -erfc'(z) / erfc(z).  h is taken as 2 z: it is more by at most 1 / z, which
+// with |d| <= z 2^-24 or so makes one rounding.
+__device__ __forceinline__ float gelu_erf(float g) {
+  constexpr float kRs2 = 0.707106781186547524f, kRs2Lo = 1.21016171e-8f;
+  const float x = __builtin_amdgcn_fmed3f(g, -20.0f, 20.0f);     // erfc is 0 or 2 there; keeps d and z d finite
+  const float z = -x * kRs2;
+  const float d = __builtin_fmaf(-x, kRs2Lo, __builtin_fmaf(-x, kRs2, -z));
+  const float e = erfcf(z);
+  return 0.5f * g * __builtin_fmaf(__builtin_fmaxf(z, 0.0f) * d, -2.0f * e, e);
+}
+
 __device__ __forceinline__ float activate(int act, float g) {
   if (act == kActSilu) return sigmoid_times(g, g);
   if (act == kActGeluTanh) {
@@ -408,7 +421,7 @@ __device__ __forceinline__ float activate(int act, float g) {
     const float g2 = __builtin_fminf(g * g, 1e10f);
     return sigmoid_times(g, 1.59576912160573072f * __builtin_fmaf(0.044715f * g2, g, g));
   }
-  if (act == kActGeluErf) return 0.5f * g * erfcf(-0.707106781186547524f * g);
+  if (act == kActGeluErf) return gelu_erf(g);
   const float p = __builtin_fmaxf(g, 0.0f);                      // squared relu
   return p * p;
 }

@@ -1,0 +1,35 @@
+"""The INT8 layer on the GPU where it is easiest to get wrong: far tails and infinities of the
+activations, and the large tiles of the product with rows of whole lines, several tiles to a workgroup
+and rows that end inside a tile."""
+import math
+
+import pytest
+import torch
+
+import precision_quantization_block_amd as pqb
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+# ---------------------------------------------------------------------------
+# activations
+# ---------------------------------------------------------------------------
+
+def test_gelu_erf_keeps_its_tail():
+    """0.5 g erfc(-g / sqrt 2) over all g whose value passes 2^-119, with one tolerance for all of them.
+    16 steps of 2^-23 are what an erfc may be off by (OpenCL's bound): 32 U; the product with 0.5 g, the
+    correction for the rounding of g / sqrt 2 and what it neglects: U each, one over.  (That rounding alone,
+    left uncorrected, reaches g^2 U: 76 measured at g = -9, 47 at -6.)"""
+    g = torch.linspace(-12.5, 9.0, 200001, dtype=torch.float64).float().to(DEV)
+    got = pqb.act_quant(g.view(1, -1), None, None, act="gelu_erf").view(-1).double()
+    want = 0.5 * g.double() * torch.special.erfc(-g.double() / math.sqrt(2))
+    off = (got - want).abs() / want.abs().clamp(min=2.0 ** -119) / U
+    at = off.argmax()
+    assert off[at] <= 36, (g[at].item(), off[at].item())

@@ -397,7 +397,8 @@ __device__ __forceinline__ float sigmoid_times(float g, float z) {
   const float d = 1.0f + __builtin_fmaf(p, lo * 0.693147180559945309f, p);
   const float y = __builtin_amdgcn_rcpf(d);
   const float q = g * y;                                         // one correction of g / d
-  const float c = __builtin_fmaf(__builtin_fmaf(-q, d, g), y, q);
+  const float off = __builtin_fmaxf(__builtin_fmaf(-q, d, g), -3.4e38f);   // (the maximum: not NaN for infinite g)
+  const float c = __builtin_fmaf(off, y, q);
   return d < 0x1p126f ? c : 0.0f * g;                            // exp(-z) overflows: -0 for finite g
 }
 

@@ -33,3 +33,18 @@ def test_gelu_erf_keeps_its_tail():
     off = (got - want).abs() / want.abs().clamp(min=2.0 ** -119) / U
     at = off.argmax()
     assert off[at] <= 36, (g[at].item(), off[at].item())
+
+
+INF = float("inf")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu_erf", "relu2"])
+def test_activations_of_plus_infinity(act, dtype):
+    """As the formulas have it, among finite values that they leave alone."""
+    x = torch.tensor([[1.0, INF, -2.0, 100.0, 17.5, 3.0e18]], dtype=dtype, device=DEV)
+    got = pqb.act_quant(x, None, None, act=act)[0].float()
+    alone = pqb.act_quant(x[:, [0, 2, 3, 4, 5]], None, None, act=act)[0].float()
+    assert got[1] == INF and torch.equal(got[[0, 2, 3, 4, 5]], alone) and torch.isfinite(alone).all()
+    up = torch.full_like(x, -0.5)
+    assert pqb.act_quant(x, up, None, act=act)[0, 1] == -INF

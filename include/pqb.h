@@ -672,7 +672,8 @@ pqb_status pqb_norm_quant(const pqb_norm* args, void* stream);
  * in float32 to a few units of 2^-24 of the value (GELU_TANH: times 1 + 2 |g| + |g|^3 / 10, GELU_ERF:
  * and up to 32 of its erfc; values below 2^-119 may be 0).  Written
  * to `out` (contiguous) rounded to dtype, or as codes and scales, pqb_quantize's of the
- * float32 v.  For codes, inputs and v must be finite; plain values take +inf to +inf.  out may share no memory with the inputs.
+ * float32 v.  For codes, inputs and v must be finite; plain values take +inf to +inf, and NaN
+ * and -inf to NaN (but RELU2's -inf to 0).  out may share no memory with the inputs.
  * Shape rules: cols >= 1, at most 32768 for ROW scales; BLK_1x128 needs cols % 128 == 0,
  * 16-byte aligned arrays and strides that are multiples of 8; strides in [cols, 2^40);
  * rows * ceil(cols / 2048) < 2^22.  Errors, before any launch: as pqb_norm_quant. */

@@ -423,7 +423,7 @@ __device__ __forceinline__ float activate(int act, float g) {
     return sigmoid_times(g, 1.59576912160573072f * __builtin_fmaf(0.044715f * g2, g, g));
   }
   if (act == kActGeluErf) return gelu_erf(g);
-  const float p = __builtin_fmaxf(g, 0.0f);                      // squared relu
+  const float p = __builtin_elementwise_maximum(g, 0.0f);        // squared relu (fmaxf drops NaN)
   return p * p;
 }
 

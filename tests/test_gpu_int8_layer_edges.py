@@ -48,3 +48,14 @@ def test_activations_of_plus_infinity(act, dtype):
     assert got[1] == INF and torch.equal(got[[0, 2, 3, 4, 5]], alone) and torch.isfinite(alone).all()
     up = torch.full_like(x, -0.5)
     assert pqb.act_quant(x, up, None, act=act)[0, 1] == -INF
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu_erf", "relu2"])
+def test_activations_keep_nan(act, dtype):
+    """NaN among finite values comes out as NaN, and -inf as 0 times inf (0 for the squared ReLU)."""
+    x = torch.tensor([[1.0, float("nan"), -2.0, -INF]], dtype=dtype, device=DEV)
+    got = pqb.act_quant(x, None, None, act=act)[0]
+    assert got.isnan().tolist() == [False, True, False, act != "relu2"] and (act != "relu2" or got[3] == 0)
+    gated = pqb.act_quant(torch.ones_like(x), x, None, act=act)[0]
+    assert gated.isnan().tolist() == [False, True, False, False] and gated[3] == -INF

@@ -22,6 +22,7 @@
 // k_int8_tile where they are read often.
 #include <algorithm>
 
+#include "int8_tiles.h"
 #include "launch.h"
 #include "quant.h"
 
@@ -535,7 +536,7 @@ template <int kTM, int kTN, int kBK, int kWM, int kWN, int kPer>
 hipError_t launch_ring(const Int8Args& g, bool out_bf16, hipStream_t st) {
   const int tiles_m = (g.M + kTM - 1) / kTM, tiles_n = (g.N + kTN - 1) / kTN;
   const uint32_t grid = (uint32_t)tiles_m * (uint32_t)tiles_n;
-  const bool along_n = g.M > g.N;
+  const bool along_n = int8_along_n(g.M, g.N);
   const int inner = along_n ? tiles_n : tiles_m;
   if (out_bf16) k_int8_ring<kTM, kTN, kBK, kWM, kWN, kPer, kBf16><<<grid, 512, 0, st>>>(g, inner, along_n);
   else k_int8_ring<kTM, kTN, kBK, kWM, kWN, kPer, kF32><<<grid, 512, 0, st>>>(g, inner, along_n);
@@ -552,82 +553,21 @@ hipError_t launch_tile(const Int8Args& g, bool out_bf16, int64_t most, hipStream
   return hipGetLastError();
 }
 
-int64_t tiles(const Int8Args& g, int tm, int tn) {
-  return (int64_t)((g.M + tm - 1) / tm) * ((g.N + tn - 1) / tn);
-}
-
-// The rings, of two that move the same the faster one later.
-struct RingTile {
-  int tm, tn;
-  hipError_t (*launch)(const Int8Args&, bool, hipStream_t);
-};
-constexpr RingTile kRings[] = {
-    {16, 16, launch_ring<16, 16, 512, 1, 1, 2>},   {16, 32, launch_ring<16, 32, 512, 1, 2, 2>},
-    {32, 16, launch_ring<32, 16, 512, 1, 1, 2>},   {32, 32, launch_ring<32, 32, 256, 1, 2, 2>},
-    {32, 64, launch_ring<32, 64, 256, 1, 4, 2>},   {64, 32, launch_ring<64, 32, 256, 2, 1, 2>},
-    {64, 64, launch_ring<64, 64, 128, 2, 2, 2>},   {128, 64, launch_ring<128, 64, 128, 2, 2, 2>},
-    {64, 128, launch_ring<64, 128, 128, 1, 4, 2>}};
-// 128 x 64 with one workgroup a CU and twice the bytes in flight, where there are no more and K is
-// long enough to be short of them: 512 rows over 4096 channels of 14336, from HBM, 47 us, 53 without,
-// of 4096 15.8 and 14.7; 1024 over 4096 of 4096 33 us with it, 27 without.
-constexpr auto kDeepRing = launch_ring<128, 64, 256, 1, 2, 1>;
+// In the order of kInt8Rings.
+constexpr hipError_t (*kRingLaunch[])(const Int8Args&, bool, hipStream_t) = {
+    launch_ring<16, 16, 512, 1, 1, 2>, launch_ring<16, 32, 512, 1, 2, 2>,  launch_ring<32, 16, 512, 1, 1, 2>,
+    launch_ring<32, 32, 256, 1, 2, 2>, launch_ring<32, 64, 256, 1, 4, 2>,  launch_ring<64, 32, 256, 2, 1, 2>,
+    launch_ring<64, 64, 128, 2, 2, 2>, launch_ring<128, 64, 128, 2, 2, 2>, launch_ring<64, 128, 128, 1, 4, 2>};
+static_assert(sizeof(kRingLaunch) / sizeof(kRingLaunch[0]) == sizeof(kInt8Rings) / sizeof(kInt8Rings[0]), "rings");
 
 }  // namespace
 
-// What a product takes, us, in units of K = 4096; with n tiles and `round` places a round,
-// the last round costs less the emptier it is.  Fitted to the table below.
-struct Parts {
-  int64_t full, rest;   // full rounds, tiles of the last one
-  double share;         // of its places
-  Parts(int64_t n, int round) : full(n / round), rest(n % round), share((double)(n % round) / round) {}
-};
-double ring_us(double k, double c) {   // c rounds of 128 x 64 tiles, or of as many bytes
-  return 3 + 1.8 * c + k * std::max(std::min(12 * c, 12 + 5.4 * (c - 1)), 13.3 * c - 9.3);
-}
-double small_us(double k, int64_t n) {   // 128 x 128, two a CU
-  const Parts p(n, 512);
-  const double last = p.rest == 0 ? 0 : p.share <= 0.5 ? 19 + 4 * p.share : 21 + 26 * (p.share - 0.5);
-  return 3 + 3 * p.full + (p.rest ? 2.5 + 0.5 * p.share : 0) + k * (34 * p.full + last);
-}
-double large_us(double k, int64_t n) {   // 256 x 256
-  const Parts p(n, 256);
-  return 6 + 6 * p.full + (p.rest ? 4 + 2 * p.share : 0) + k * (50 * p.full + (p.rest ? 30 + 20 * p.share * p.share : 0));
-}
-
-// The ring whose busiest of 256 CUs moves the fewest bytes into LDS for each byte of K, the
-// later of them where two are equal; or tiles of 128 x 128 or 256 x 256, if they are estimated to
-// take less.  Measured, us:
-//   K = 4096, tiles        16 x 16  16 x 32  32 x 16  32 x 32  32 x 64  64 x 32  64 x 64  128 x 64
-//   16 over 14336             13.9     11.2               -      11.3                -         -
-//   64 over 2048               6.8      5.3      5.8      5.9      7.0      6.7      9.7      12.4
-//   64 over 4096              12.4      8.3      8.8      6.9      8.0      8.2     10.1      13.2
-//   33 over 14336             29.2     19.6     23.7     17.5     12.8     12.5     12.1      13.7
-//   128 over 4096             22.2     13.9     14.3      9.7      8.3      8.3     10.1      14.4
-//   256 over 4096             40.4     27.3     26.3     16.9     12.2     12.3     10.8      14.7
-// and rings of 64 x 128, 128 x 128, 256 x 256 (in brackets what is estimated; all as they are
-// taken over 114 shapes, chosen 3% slower than the fastest of these and the small ones in the mean):
-//   K = 4096:  768 over 4096  22 (24)   24 (26)   41 (41);   1536  38 (39)   33 (33)   44 (44)
-//              2048  53 (54)   38 (40)   46 (46);   3000  79 (84)   63 (64)   54 (53);   4096 109 (114)   77 (77)   65 (62)
-//   8192 over 8192 of 64  72 (67)   33 (31)   38 (33);   of 512 104 (113)   65 (61)   58 (55)
-//   8192 over 7168 of 2048 204 (235)   145 (143)   123 (122);   1024 over 4096 of 14336 93 (67)   105 (79)   167 (120)
-// (The last, partial round of 256 x 256 tiles cut into 128 x 128 ones in a second launch gained
-// nothing, nor did parts of K summed by a second launch: 512 over 4096 of 14336 43 us as a
-// ring, 45 in four parts.)
 hipError_t launch_gemm_int8(const Int8Args& g, bool out_bf16, hipStream_t st) {
-  const RingTile* ring = kRings;
-  int64_t least = INT64_MAX;
-  for (const RingTile& r : kRings) {
-    const int64_t n = tiles(g, r.tm, r.tn), cost = (n + 255) / 256 * (r.tm + r.tn);
-    if (n < 1 << 22 && cost <= least) least = cost, ring = &r;   // (a grid has less than 2^32 threads)
-  }
-  const double k = g.K / 4096.0, by_ring = ring_us(k, least / 192.0);
-  const double by_small = small_us(k, tiles(g, 128, 128)), by_large = large_us(k, tiles(g, 256, 256));
-  if (least != INT64_MAX && by_ring <= by_small && by_ring <= by_large) {
-    if (least == 192 && g.K > 4096 && tiles(g, 128, 64) <= 256) return kDeepRing(g, out_bf16, st);
-    return ring->launch(g, out_bf16, st);
-  }
-  if (by_small <= by_large) return launch_tile<128, 128, 2, 2>(g, out_bf16, 512, st);
-  return launch_tile<256, 256, 2, 4>(g, out_bf16, 256, st);
+  const Int8Tile t = choose_int8(g.M, g.N, g.K);
+  if (t.kernel == Int8Kernel::kRing) return kRingLaunch[t.ring](g, out_bf16, st);
+  if (t.kernel == Int8Kernel::kDeepRing) return launch_ring<128, 64, 256, 1, 2, 1>(g, out_bf16, st);
+  if (t.tm == 128) return launch_tile<128, 128, 2, 2>(g, out_bf16, kInt8SmallGrid, st);
+  return launch_tile<256, 256, 2, 4>(g, out_bf16, kInt8LargeGrid, st);
 }
 
 }  // namespace pqb

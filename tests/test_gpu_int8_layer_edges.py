@@ -59,3 +59,85 @@ def test_activations_keep_nan(act, dtype):
     assert got.isnan().tolist() == [False, True, False, act != "relu2"] and (act != "relu2" or got[3] == 0)
     gated = pqb.act_quant(torch.ones_like(x), x, None, act=act)[0]
     assert gated.isnan().tolist() == [False, True, False, False] and gated[3] == -INF
+
+
+# ---------------------------------------------------------------------------
+# gemm_int8: every tile, both types of result, rows of whole lines and others
+# ---------------------------------------------------------------------------
+
+# Kernel ("ring", "deep" or "tile"), its tile, and products that it takes.  Each kernel has rows of C that
+# are whole lines (N a multiple of 64) and rows that are not, more rows than channels and fewer; the tiles
+# that workgroups take in turn also one, two, an even and an odd number of blocks of K, more tiles than
+# workgroups, and rows that end inside a tile, so that whole and partial waves meet in one.
+PRODUCTS = [
+    ("ring", 16, 16, [(4, 3, 64), (1, 3, 64), (65, 64, 64), (1, 64, 1040)]),
+    ("ring", 16, 32, [(388, 307, 64), (1, 4108, 208), (392, 320, 1040), (1, 4160, 64)]),
+    ("ring", 32, 16, [(4183, 3, 64), (17, 2103, 336), (337, 192, 64), (17, 2112, 1040)]),
+    ("ring", 32, 32, [(4221, 17, 64), (17, 4508, 1040), (403, 320, 336), (17, 4160, 64)]),
+    ("ring", 32, 64, [(1613, 294, 1040), (1, 8376, 64), (775, 640, 64), (1, 8320, 336)]),
+    ("ring", 64, 32, [(8380, 3, 64), (35, 4100, 1040), (803, 320, 64), (33, 4288, 208)]),
+    ("ring", 64, 64, [(8246, 34, 64), (33, 8694, 1040), (1346, 384, 336), (34, 8320, 64)]),
+    ("ring", 128, 64, [(8559, 131, 64), (339, 5428, 1040), (8346, 192, 336), (1349, 1472, 64)]),
+    ("ring", 64, 128, [(8231, 71, 336), (70, 8501, 64), (1233, 832, 64), (65, 8384, 1040)]),
+    ("deep", 128, 64, [(8217, 66, 4368), (65, 8435, 4112), (1218, 832, 4112), (65, 8320, 4368)]),
+    ("tile", 128, 128, [(5464, 321, 64), (203, 8398, 336), (8569, 1216, 64), (4619, 2240, 208), (8231, 1856, 1168),
+                        (1700, 6080, 128), (1169, 8768, 208), (1166, 8640, 336)]),
+    ("tile", 256, 256, [(8318, 5026, 208), (911, 8204, 1040), (8332, 4928, 208), (8485, 2880, 1168), (7193, 3456, 336),
+                        (9990, 20032, 128), (3591, 6720, 1168), (3333, 7296, 336)]),
+]
+
+
+def operands(g, m, n, k):
+    make = lambda r: (torch.randn((r, k), generator=g, device=DEV) * 40).round().clamp(-128, 127).to(torch.int8)  # noqa: E731
+    scales = lambda r: torch.rand(r, generator=g, device=DEV) * 0.02 + 1e-3  # noqa: E731
+    return make(m), scales(m), make(n), scales(n), torch.randn(n, generator=g, device=DEV)
+
+
+def rounded_product(a, sa, b, sb, bias):
+    """An exact sum, then float32 roundings one after the other."""
+    v = torch.matmul(a.double(), b.double().t()).float().mul_(sa[:, None]).mul_(sb)
+    return v if bias is None else v.add_(bias)
+
+
+@pytest.mark.parametrize("m,n,k", [p for *_, products in PRODUCTS for p in products])
+def test_product_of_every_kernel(m, n, k):
+    """Both types of result, with and without bias; bit for bit."""
+    a, sa, b, sb, bias = operands(gen(m + n), m, n, k)
+    for c in (None, bias):
+        want = rounded_product(a, sa, b, sb, c)
+        assert torch.equal(pqb.gemm_int8((a, sa), (b, sb), F32, bias=c), want)
+        want = want.to(BF)
+        assert torch.equal(pqb.gemm_int8((a, sa), (b, sb), BF, bias=c), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,n,k", [(4619, 2240, 208), (7193, 3456, 336)])
+def test_tiles_in_turn_on_two_streams_and_in_graphs(m, n, k, dtype):
+    """Workgroups that store one tile while the next one's blocks arrive, two products at a time."""
+    sets = [operands(gen(i), m, n, k) for i in range(2)]
+    want = [rounded_product(*s).to(dtype) for s in sets]
+    call = lambda s: pqb.gemm_int8(s[:2], s[2:4], dtype, bias=s[4])  # noqa: E731
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(6):
+        for st, s, w in zip(streams, sets, want):
+            with torch.cuda.stream(st):
+                outs.append((call(s), w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in outs)
+    graphs = []
+    for s in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call(s)
+        graphs.append((graph, out))
+    for _ in range(4):
+        for st, (graph, _) in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, out), w in zip(graphs, want):
+            assert torch.equal(out, w)
+            out.zero_()
+        torch.cuda.synchronize()

@@ -633,7 +633,7 @@ typedef enum pqb_norm_kind { PQB_NORM_RMS = 0, PQB_NORM_LAYER = 1 } pqb_norm_kin
  * All arrays of `dtype`, but scales (f32).  x, residual, h: rows x_stride, residual_stride,
  * h_stride elements apart; gate [gate_rows, cols], rows gate_stride apart, gate_rows
  * dividing rows: row t takes gate row t / (rows / gate_rows) (one per sequence, or per
- * token).  post_weight, weight, bias [cols]; weight NULL is all ones.  out is contiguous.  h may be x
+ * token; any number with rows = 0).  post_weight, weight, bias [cols]; weight NULL is all ones.  out is contiguous.  h may be x
  * or residual itself (the same address and stride); no other output may share memory
  * with an input or output.
  * Shape rules: cols in [1, 32768]; BLK_1x128 needs cols % 128 == 0, 16-byte aligned arrays

@@ -1060,7 +1060,7 @@ pqb_status pqb_norm_quant(const pqb_norm* n, void* stream) {
   if (!stride_ok(n->x, n->x_stride) || !stride_ok(n->residual, n->residual_stride) ||
       !stride_ok(n->gate, n->gate_stride) || !stride_ok(n->h, n->h_stride))
     return PQB_ERR_SHAPE;
-  if (n->gate && (n->gate_rows < 1 || rows % n->gate_rows)) return PQB_ERR_SHAPE;
+  if (n->gate && (rows == 0 ? n->gate_rows < 0 : n->gate_rows < 1 || rows % n->gate_rows)) return PQB_ERR_SHAPE;
   if (!(n->eps > 0.0f && n->eps <= 1.0f) || !(n->residual_scale - n->residual_scale == 0.0f)) return PQB_ERR_VALUE;
   if (n->bias && n->kind != PQB_NORM_LAYER) return PQB_ERR_NULL;
   if (rows == 0) return PQB_OK;

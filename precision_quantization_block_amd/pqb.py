@@ -909,7 +909,7 @@ def norm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, fmt: str | N
                 raise ValueError("residual must have x's shape")
     if gate is not None:
         g, gate_rows, gate_stride = _layer_rows(gate, "gate", dev, dtype, cols, block)
-        if gate_rows < 1 or rows % gate_rows:
+        if rows and (gate_rows < 1 or rows % gate_rows):
             raise ValueError("gate must have a number of rows that divides x's")
     weights = (post_weight, weight, bias)
     for w in weights:

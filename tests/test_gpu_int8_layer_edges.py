@@ -62,6 +62,19 @@ def test_activations_keep_nan(act, dtype):
 
 
 # ---------------------------------------------------------------------------
+# norm_quant
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("gates", [0, 1, 3])
+def test_norm_of_no_rows_with_a_gate(gates):
+    """A batch without tokens, its gates per token (none) or per sequence."""
+    x, gate = torch.empty(0, 256, dtype=BF, device=DEV), torch.ones(gates, 256, dtype=BF, device=DEV)
+    for fmt in ("int8_sym", None):
+        out, h = pqb.norm_quant(x, None, fmt, residual=x, gate=gate)
+        assert h.shape == (0, 256) and (out if fmt is None else out.codes).numel() == 0
+
+
+# ---------------------------------------------------------------------------
 # gemm_int8: every tile, both types of result, rows of whole lines and others
 # ---------------------------------------------------------------------------
 

@@ -85,6 +85,11 @@ def test_norm_refusals(L, want, changes):
     assert norm(L, **changes) == want
 
 
+@pytest.mark.parametrize("want,gate_rows", [(OK, 0), (OK, 1), (OK, 7), (SHAPE, -1)])
+def test_norm_of_no_rows_takes_any_gate(L, want, gate_rows):
+    assert norm(L, rows=0, gate=P, gate_rows=gate_rows) == want
+
+
 def test_norm_null(L):
     assert L.pqb_norm_quant(None, None) == NULL
 

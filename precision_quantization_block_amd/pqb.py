@@ -1005,6 +1005,8 @@ def rope_table(rotary_dim: int, base: float = 10000.0, *, interleaved: bool = Fa
         raise ValueError("rotary_dim must be even and at least 2")
     if not (factor > 0 and base > 0 and original_length > 0):
         raise ValueError("base, factor and original_length must be positive")
+    if scaling == "yarn" and base <= 1:
+        raise ValueError("yarn needs a base over 1")
     i = torch.arange(rotary_dim // 2, dtype=torch.float64)
     amp = 1.0
     if scaling == "ntk":

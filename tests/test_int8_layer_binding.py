@@ -208,3 +208,11 @@ def test_rope_tables():
                 dict(rotary_dim=2, scaling="ntk"), dict(rotary_dim=64, scaling="yarn", low=5.0, high=2.0)):
         with pytest.raises(ValueError):
             pqb.rope_table(device="cpu", **bad)
+
+
+@pytest.mark.parametrize("base", [1.0, 0.5])
+def test_yarn_needs_angles_that_fall(base):
+    """The pair that makes a number of turns is sought by log base."""
+    with pytest.raises(ValueError, match="base"):
+        pqb.rope_table(64, base, scaling="yarn", factor=4.0, device="cpu")
+    assert pqb.rope_table(64, base, scaling="by_turns", factor=4.0, device="cpu").angles.isfinite().all()

@@ -694,7 +694,8 @@ pqb_status pqb_act_quant(const void* gate, const void* up, pqb_dtype dtype, int6
  * for the pairs (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved != 0, of each head's
  * first rot values; the others are copied.  angles f64 [rot / 2], radians per token: a
  * scaled context is other angles (and amplitude).  The angle is taken in float64 and
- * reduced there; c and s are within 2^-22 of their values for |t| < 2^28.
+ * reduced there; c and s are within |amplitude| 2^-22 of their values
+ * for |t| < 2^28.
  * positions i32 [tokens]; or NULL, and token t is at the place that a step of the paged
  * cache gives it: request b owns tokens q_starts[b] .. q_starts[b + 1] - 1 (i32 [batch + 1],
  * rising), the last of them at kv_lens[b] - 1 (i32 [batch]), as pqb_kv_plan_paged writes

@@ -49,9 +49,13 @@ inline double int8_large_us(double k, int64_t n) {   // 256 x 256
   return 6 + 6 * p.full + (p.rest ? 4 + 2 * p.share : 0) + k * (50 * p.full + (p.rest ? 30 + 20 * p.share * p.share : 0));
 }
 
-// 128 x 64 tiles with one workgroup a CU and twice the bytes in flight, where there are no more and K is
-// long enough to be short of them: 512 rows over 4096 channels of 14336, from HBM, 47 us, 53 without,
-// of 4096 15.8 and 14.7; 1024 over 4096 of 4096 33 us with it, 27 without.
+// 128 x 64 tiles with one workgroup a CU and twice the bytes in flight, where there are no more tiles than
+// CUs (1024 over 4096 of 4096 33 us with it, 27 without) and K is longer than this.  512 over 4096, us,
+// without / with it:
+//   K                    2064         4096         4112         5120         8192        14336
+//   from HBM       14.5 / 14.3  18.2 / 17.4  24.0 / 21.7  23.8 / 21.3  31.7 / 28.8  52.4 / 45.6
+//   from its cache 10.5 / 11.1  13.9 / 14.5  17.0 / 16.4  17.4 / 17.3  24.0 / 23.7  38.7 / 37.6
+// and alike with 189 to 256 tiles of other shapes: above 4096 it gains or ties, wherever the operands are.
 constexpr int kInt8DeepK = 4096;
 
 // The ring whose busiest of 256 CUs moves the fewest bytes into LDS for each byte of K, the
@@ -64,12 +68,13 @@ constexpr int kInt8DeepK = 4096;
 //   33 over 14336             29.2     19.6     23.7     17.5     12.8     12.5     12.1      13.7
 //   128 over 4096             22.2     13.9     14.3      9.7      8.3      8.3     10.1      14.4
 //   256 over 4096             40.4     27.3     26.3     16.9     12.2     12.3     10.8      14.7
-// and rings of 64 x 128, 128 x 128, 256 x 256 (in brackets what is estimated; all as they are
-// taken over 114 shapes, chosen 3% slower than the fastest of these and the small ones in the mean):
+// and rings of 64 x 128, 128 x 128, 256 x 256 (in brackets what is estimated; over 114 shapes, the
+// one taken is 2% slower than the fastest of these and the small ones in the mean, 16% at worst):
 //   K = 4096:  768 over 4096  22 (24)   24 (26)   41 (41);   1536  38 (39)   33 (33)   44 (44)
 //              2048  53 (54)   38 (40)   46 (46);   3000  79 (84)   63 (64)   54 (53);   4096 109 (114)   77 (77)   65 (62)
 //   8192 over 8192 of 64  72 (67)   33 (31)   38 (33);   of 512 104 (113)   65 (61)   58 (55)
 //   8192 over 7168 of 2048 204 (235)   145 (143)   123 (122);   1024 over 4096 of 14336 93 (67)   105 (79)   167 (120)
+// (from HBM there, where all are estimated too low, by the same quarter)
 // (The last, partial round of 256 x 256 tiles cut into 128 x 128 ones in a second launch gained
 // nothing, nor did parts of K summed by a second launch: 512 over 4096 of 14336 43 us as a
 // ring, 45 in four parts.)

@@ -167,11 +167,13 @@ struct Tile {
 // products issue one between the other (left to the compiler, every read was waited for at
 // once: 8192^3 445 us, 435 so).  Chunk c of row r lies at c ^ (r / 2); at c ^ r the 16 rows met in
 // pairs, half of the LDS cycles.  Workgroups stay and take tiles in turn, and the blocks of
-// all their tiles are one stream: the first ones of the next tile are on their way, and its
-// first fragments in registers, while a tile's results are scaled and stored (8192 x 7168 x
-// 2048 142 to 122 us).  256 x 256 tiles, 8 waves of 128 x 64: 8192^3 in 410-425 us, 2.6 POP/s (the
+// all their tiles are one stream: before a tile's results are scaled, the next tile's first block is in
+// LDS, its first fragments in registers, and its second block on its way; the results' stores drain while
+// the first is multiplied (8192 x 7168 x 2048 142 to 122 us).  (Scales and bias are loaded behind that
+// second block, and loads return in order, so the first result waits for it.)  256 x 256 tiles, 8 waves of 128 x 64: 8192^3 in 410-425 us, 2.6 POP/s (the
 // vendor's 521); the same without its loads 354, without LDS reads too 314: what is left is
-// the operand stream and the clock that the power leaves (2.0 GHz).
+// the operand stream and the clock that the power leaves (2.0 GHz).  These tiles take all 256 registers, and
+// 9 more (6 for float32 results) that are spilled and read again between tiles, not in the loop over K.
 template <int kTM, int kTN, int kWM, int kWN, int kOut>
 __global__ __launch_bounds__(64 * kWM * kWN) void k_int8_tile(Int8Args g, int tiles_m, int tiles_n) {
   using S = Tile<kTM, kTN, kWM, kWN>;

@@ -17,7 +17,10 @@
 // workgroup has one row and as many waves as that takes, or several narrow ones (a wave or part
 // of one each).  All of it is bound by HBM, and by latency where there are few rows:
 // 8192 rows of 7168 (bf16, residual, E4M3 1x128) 70 us, 5.9 TB/s; 4096 rows of 14336 through
-// SwiGLU to E4M3 1x128 52 us, 5.6 TB/s; 64 rows of 4096 to INT8 3.2 us.
+// SwiGLU to E4M3 1x128 53 us, 5.5 TB/s; 64 rows of 4096 to INT8 3.7 us.  (Norms of more than 16384
+// columns, four units to each of 1024 threads, pass the 128 registers that leaves them by 14 to 37, which
+// are spilled: 1024 rows of 32768, bf16, with residual to INT8 70 us, 3.4 TB/s; 2048 of 16384 50 us,
+// 4.7.)
 #include "launch.h"
 #include "quant.h"
 
@@ -386,7 +389,8 @@ __global__ __launch_bounds__(S::threads) void k_norm(NormArgs a) {
 // ---------------------------------------------------------------------------
 // Activations.  Each takes a few float32 roundings (silu and tanh-gelu as
 // g / (1 + 2^-z): the product with log2(e) carries its rounding error along, since 2^z
-// turns an absolute error into a relative one).
+// turns an absolute error into a relative one; tanh-gelu's z itself is rounded, which costs its tail
+// |z| 2^-24 a rounding: 52 units at g = -6).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float sigmoid_times(float g, float z) {
   z = __builtin_fminf(__builtin_fmaxf(z, -150.0f), 150.0f);      // 2^t is 0 or inf there
@@ -489,7 +493,7 @@ __global__ __launch_bounds__(256) void k_act_flat(ActArgs a, uint32_t pieces, in
 // wave, narrow ones a part of it (327680 heads of 128 29 us with 16 lanes each, 87 with 64; of 64
 // 16 with 8, 24 with 16); wider ones get as many waves as they need.  Threads without an element cost as much
 // as others (16384 rows of 1024: 21 us with 64 threads a row, 30 with 256), and fewer units a
-// thread shorten a few rows (64 of 4096: 3.2 / 3.9 / 4.0 us at 1 / 2 / 4 units) and cost
+// thread shorten a few rows (64 of 4096, launches in a loop: 3.2 / 3.9 / 4.0 us at 1 / 2 / 4 units) and cost
 // many little (8192 of 4096: 41.7 / 39.8 / 39.8).  Many wide rows of an activation are
 // faster with four units (8192 of 14336 118 us, 136 with two; 512 11.8 and 10.3), of a norm,
 // which holds more arrays, with two (4096 of 12288 59 us, 79 with four).

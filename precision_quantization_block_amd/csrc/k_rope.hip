@@ -10,7 +10,7 @@
 // A workgroup takes one token, or up to four of small heads: its threads form each cosine and sine once, into
 // LDS, and every head of q and k is then turned from there.  Reading and writing q and k
 // is all that costs: bound by HBM (8192 tokens of 40 heads of 128, bf16, 29 us, 5.8 TB/s), by
-// latency for few tokens (64 3.1 us).
+// latency for few tokens (64 3.6 us).
 #include "launch.h"
 #include "quant.h"
 

@@ -1068,7 +1068,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions, table: RopeTable, *
     fused projection) turned by their positions' angles: the first 2 * len(table.angles) values
     of each head, the rest copied.  positions: int32 [tokens], or the PagedPlan of the step, which
     places token t where the paged cache does (tokens outside every request are left as they
-    were in the outputs).  q_out and k_out may be q and k themselves.  Returns (q_out, k_out), k_out
+    were in q_out and k_out; outputs made here are undefined there).  q_out and k_out may be q and k
+    themselves.  Returns (q_out, k_out), k_out
     None without k."""
     dev, dtype = _device_of(q, "q"), q.dtype
     q2, q_stride = _rope_rows(q, "q", dev, dtype)
